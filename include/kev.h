@@ -70,7 +70,11 @@ typedef enum {
   KEV_ERR_ADAPTER = 11       /* (device) a LoRA adapter id outside [-1, n_adapters) */
 } kev_status;
 
-typedef enum { KEV_BF16 = 0, KEV_FP32 = 1 } kev_dtype;
+typedef enum {
+  KEV_BF16 = 0,
+  KEV_FP32 = 1,
+  KEV_E4M3 = 2 /* paged caches of the span operators only: 8-bit codes with one fp32 scale per row */
+} kev_dtype;
 
 /* Half-open interval [begin, end) of packed-token indices owned by one question. */
 typedef struct {
@@ -365,6 +369,86 @@ kev_status kev_decode_attn_paged(const void* q_new, const void* k_new, const voi
  * changed when the free blocks do not suffice or a need[i] exceeds max_blocks. */
 int32_t kev_assign_blocks(const int32_t* need, int32_t n, uint8_t* free_map, int32_t n_blocks, int32_t* table,
                           int32_t max_blocks, int32_t contiguous_first);
+
+/* ---------------------------------------------------------------------------------------
+ * Spans: chunks of new tokens over a paged cache, sliding windows, 8-bit caches
+ *
+ * Question i brings the L_i packed tokens [begin_i, end_i), at positions P_i .. P_i + L_i - 1
+ * after the P_i = prefix_lens[i] positions its cache already holds: one token in a decode step,
+ * many in a piece of a prompt, both side by side in a mixed round (an empty interval takes no
+ * part, as a dropped question).  P_i and L_i are any lengths.  The token at position p sees
+ * position u of its own question iff
+ *     u <= p  and  (window == 0  or  p - u < window  or  u < sinks):
+ * everything before it (window 0), or the last `window` positions, itself among them, and the
+ * first `sinks` positions, which stay visible.
+ *
+ * Shapes: bf16 or fp32 q, k, v and out, d_h 64 or 128 (else KEV_ERR_UNSUPPORTED).  Cache: blocks
+ * of KEV_PAGE positions and a block table as for the paged slot pool above, of the type of q or
+ * of KEV_E4M3, with at most 2^20 blocks and fewer than 2^31 rows (n_blocks * H_kv * KEV_PAGE).
+ * Device-detected errors, found before anything is written: KEV_ERR_INTERVALS (also a question
+ * longer than max_chunk), KEV_ERR_PREFIX (negative), KEV_ERR_SLOT_OVERFLOW (P_i + L_i >
+ * max_blocks * KEV_PAGE), KEV_ERR_SLOT (a block out of range, or used twice).  Only pages that
+ * some new token sees or that are written are looked at: entries of pages that have wholly left
+ * the window may be anything.  The workspace (kev_paged_workspace_size bytes, 256-byte aligned)
+ * needs no initial value; calls in flight at the same time must not share one.
+ * ------------------------------------------------------------------------------------- */
+
+/* A paged cache.  With dtype KEV_E4M3, position p's row of kv head g is d_h codes c_e and the
+ * scale s at the same place, s = max_e |x_e| / 448 and c_e = x_e / s rounded to the nearest e4m3
+ * value (ties to even): each element comes back as c_e * s, off by at most max(2^-4 |x_e|,
+ * 2^-10 s) and the last place of s.  A row of zeros has s = 0.  A row that holds a NaN or an
+ * infinity comes back as NaN throughout. */
+typedef struct {
+  void* k;                    /* [n_blocks, H_kv, KEV_PAGE, d_h] of dtype, 16-byte aligned */
+  void* v;
+  float* k_scale;             /* KEV_E4M3: [n_blocks, H_kv, KEV_PAGE], 16-byte aligned; else not read */
+  float* v_scale;
+  const int32_t* block_table; /* device int32[n_questions, max_blocks] */
+  int32_t max_blocks;
+  int32_t n_blocks;
+  int32_t dtype;              /* the shape's dtype, or KEV_E4M3 */
+} kev_paged_cache;
+
+/* Bytes of device workspace the calls below need for at most `n_questions` questions with
+ * `total_tokens` packed new tokens.  0 on bad arguments. */
+size_t kev_paged_workspace_size(int32_t n_questions, int32_t total_tokens, const kev_attn_shape* shape);
+
+/* Rows begin_i + j of k and v [T, H_kv, d_h] into positions P_i + j of the cache, in its type
+ * (quantised as above, or a bit copy).  No other cached row is touched.  prefix_lens: device
+ * int32[n_questions].  Two kernels. */
+kev_status kev_paged_write(const void* k, const void* v, int32_t total_tokens, const kev_interval* intervals,
+                           int32_t n_questions, const int32_t* prefix_lens, const kev_paged_cache* cache,
+                           const kev_attn_shape* shape, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                           kev_stream_t stream);
+
+/* The way back: positions P_i + j of the cache into rows begin_i + j of k and v [T, H_kv, d_h], in
+ * the shape's type (c_e * s rounded once, or a bit copy).  Rows of tokens in no interval are not
+ * touched.  Two kernels. */
+kev_status kev_paged_read(void* k, void* v, int32_t total_tokens, const kev_interval* intervals, int32_t n_questions,
+                          const int32_t* prefix_lens, const kev_paged_cache* cache, const kev_attn_shape* shape,
+                          void* workspace, size_t workspace_bytes, int32_t* dev_status, kev_stream_t stream);
+
+/* The chunk's K/V rows into the cache (kev_paged_write), then attention of its tokens over it:
+ *   out[begin_i + j, h] = softmax_u(scale q[begin_i + j, h] . K_i[u, g]) V_i[u, g]   over the u seen
+ * with K_i, V_i as the cache holds them (c_e * s for KEV_E4M3, the chunk's own rows among them) and
+ * g = h / G.  Rows of tokens in no interval are written as zeros.  k and v NULL: the rows are in
+ * the cache already.  max_chunk: no question brings more tokens (0: not known); a caller that
+ * knows, above all of a decode step (1), gets the kernel for few rows.
+ * Arithmetic: bf16 q: products on the tensor cores, fp32 accumulation, softmax weights rounded to
+ * bf16 for the product with V; fp32 q: fp32 throughout.  What masked positions hold, NaN and
+ * infinities among it, does not reach the result. */
+kev_status kev_chunk_attn_paged(const void* q, const void* k, const void* v, int32_t total_tokens,
+                                const kev_interval* intervals, int32_t n_questions, const int32_t* prefix_lens,
+                                int32_t max_chunk, const kev_paged_cache* cache, int32_t window, int32_t sinks, void* out,
+                                const kev_attn_shape* shape, void* workspace, size_t workspace_bytes,
+                                int32_t* dev_status, kev_stream_t stream);
+
+/* Packed prefill attention (kev_prefill_attn without a cache: P_i = 0, keys and values from k and
+ * v) under a sliding window with sinks, as above. */
+kev_status kev_prefill_attn_window(const void* q, const void* k, const void* v, int32_t total_tokens,
+                                   const kev_interval* intervals, int32_t n_questions, int32_t window, int32_t sinks,
+                                   void* out, const kev_attn_shape* shape, void* workspace, size_t workspace_bytes,
+                                   int32_t* dev_status, kev_stream_t stream);
 
 /* ---------------------------------------------------------------------------------------
  * Rotary position encoding with positions counted per question

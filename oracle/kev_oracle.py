@@ -34,6 +34,9 @@ dense T x T mask, in float64:
 * Chunked prefill into slots (inference-engine notes, §2.6: a long input is
   prefilled in pieces that share rounds with decode steps, each later piece
   using the K/V of the pieces before it).
+* Spans: chunks of new tokens at any prefix over a paged cache, a sliding
+  window with sink positions, and an 8-bit (e4m3) cache with one fp32 scale
+  per row (no page has these; they are written from their formulas).
 * Per-question temperature sampling (Kev architecture article, §4.1: each
   question brings its own temperature, applied to the softmax of its logits
   at every decode step; nothing else in the model changes).
@@ -684,3 +687,92 @@ def validate_lora(adapter_ids, n_adapters: int):
     """None, or ADAPTER when an adapter id lies outside [-1, n_adapters)."""
     a = np.asarray(adapter_ids, dtype=np.int64)
     return ADAPTER if np.any((a < -1) | (a >= n_adapters)) else None
+
+
+# ---------------------------------------------------------------------------------------
+# spans: any prefix, sliding window with sinks, e4m3 rows
+# ---------------------------------------------------------------------------------------
+def e4m3_round(x):
+    """The e4m3 value (1 sign, 4 exponent, 3 mantissa bits; bias 7, largest 448) nearest to each x,
+    ties to the even mantissa; beyond the range the largest value.  NaN stays NaN."""
+    x = np.asarray(x, np.float64)
+    a = np.abs(x)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        e = np.floor(np.log2(np.where(a > 0, a, 1.0)))
+    e = np.where(a >= np.exp2(e + 1), e + 1, e)  # log2 rounded across a power of two
+    e = np.where(a < np.exp2(e), e - 1, e)
+    step = np.exp2(np.maximum(e, -6.0) - 3.0)
+    with np.errstate(invalid="ignore"):
+        r = np.rint(a / step) * step  # rint: ties to even
+    return np.where(np.isnan(x), np.nan, np.copysign(np.minimum(r, 448.0), x))
+
+
+def quantise_rows(x):
+    """x [..., d] float32 -> (code values float64 [..., d], scales float32 [...]): scale = max|x| / 448 and
+    code = x / scale rounded to e4m3, both quotients rounded to float32 first (the stored form)."""
+    x = np.asarray(x, np.float32)
+    with np.errstate(divide="ignore", invalid="ignore", over="ignore"):
+        scale = (np.abs(x).max(-1) / np.float32(448.0)).astype(np.float32)
+        y = np.where(scale[..., None] == 0, np.float32(0), x / scale[..., None]).astype(np.float32)
+    return e4m3_round(y), scale
+
+
+def span_visible(p: int, n: int, window: int, sinks: int) -> np.ndarray:
+    """bool[n]: which of positions 0 .. n - 1 the token at position p sees."""
+    u = np.arange(n)
+    seen = u <= p
+    if window:
+        seen &= (p - u < window) | (u < sinks)
+    return seen
+
+
+def span_attention(q, keys, values, prefix_lens, intervals, window: int = 0, sinks: int = 0, scale=None):
+    """q [T, H_q, d] float64; keys[i], values[i] [P_i + L_i, H_kv, d] float64: question i's whole cache, the
+    chunk's rows included.  Returns (out [T, H_q, d], weight [T, H_q, d]) where weight is the same sum with
+    |v| in place of v, the size that rounding errors of the sum go by.  Masked positions are left out of the
+    sums (they may hold anything); tokens in no interval are zero."""
+    q = np.asarray(q, np.float64)
+    T, h_q, d = q.shape
+    sc = _scale(scale, d)
+    out, size = np.zeros_like(q), np.zeros_like(q)
+    for i, (b, e) in enumerate(intervals):
+        for j in range(int(e) - int(b)):
+            p = int(prefix_lens[i]) + j
+            seen = span_visible(p, p + 1, window, sinks)
+            k, v = keys[i][:p + 1][seen], values[i][:p + 1][seen]
+            for h in range(h_q):
+                g = h // (h_q // k.shape[1])
+                z = sc * (k[:, g] @ q[b + j, h])
+                w = np.exp(z - z.max())
+                w /= w.sum()
+                out[b + j, h] = w @ v[:, g]
+                size[b + j, h] = w @ np.abs(v[:, g])
+    return out, size
+
+
+def validate_span(intervals, total_tokens, prefix_lens, table, n_blocks, max_chunk=None, window=0, sinks=0,
+                  attend=True, page: int = PAGE):
+    """The error a span call reports before it writes anything (INTERVALS, PREFIX, SLOT_OVERFLOW or SLOT,
+    the first that applies to any question, in that order), or None."""
+    spans = sorted((int(b), int(e)) for b, e in intervals if e != b)
+    if any(b < 0 or e < b or e > total_tokens for b, e in intervals) or \
+            any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+        return INTERVALS
+    if max_chunk and any(e - b > max_chunk for b, e in spans):
+        return INTERVALS
+    live = [(i, int(e) - int(b), int(prefix_lens[i])) for i, (b, e) in enumerate(intervals) if e > b]
+    if any(p < 0 for _, _, p in live):
+        return PREFIX
+    if any(p + n > len(table[0]) * page for _, n, p in live):
+        return SLOT_OVERFLOW
+    used = []
+    for i, n, p in live:
+        pages = set(range(p // page, (p + n - 1) // page + 1))
+        if attend:
+            for x in (p, p + n - 1):
+                pages |= {int(u) // page for u in np.flatnonzero(span_visible(x, x + 1, window, sinks))}
+            pages |= {int(u) // page for u in np.flatnonzero(span_visible(p, p + 1, window, sinks))}
+        used += [int(table[i][y]) for y in pages]
+    if any(x < 0 or x >= n_blocks for x in used) or len(set(used)) != len(used):
+        return SLOT
+    return None

@@ -11,7 +11,7 @@ import importlib
 
 
 def __getattr__(name):
-    if name.startswith("kev_") or name in ("KevError", "make_shape", "library_path", "binding"):
+    if name.startswith("kev_") or name in ("KevError", "make_shape", "make_paged_cache", "library_path", "binding"):
         mod = importlib.import_module(".binding", __name__)
         return mod if name == "binding" else getattr(mod, name)
     raise AttributeError(name)

@@ -36,6 +36,7 @@ KEV_ERR_SAMPLING = 10
 KEV_ERR_ADAPTER = 11
 KEV_BF16 = 0
 KEV_FP32 = 1
+KEV_E4M3 = 2
 KEV_PAGE = 128
 KEV_MAX_PAGED_ENTRIES = 16384
 KEV_MAX_QUESTIONS = 4096
@@ -55,12 +56,20 @@ EXPORTED = [
     "kev_rope_table_size", "kev_rope_table", "kev_rope_prefill", "kev_prefill_attn_rope", "kev_rope_decode",
     "kev_decode_attn_rope", "kev_prefill_attn_paged", "kev_kv_write_paged", "kev_decode_attn_paged",
     "kev_assign_blocks", "kev_prefill_chunk", "kev_sample", "kev_lora_apply",
+    "kev_paged_workspace_size", "kev_paged_write", "kev_paged_read", "kev_chunk_attn_paged",
+    "kev_prefill_attn_window",
 ]
 
 
 class kev_attn_shape(ctypes.Structure):
     _fields_ = [("h_q", ctypes.c_int32), ("h_kv", ctypes.c_int32), ("d_h", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class kev_paged_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("max_blocks", ctypes.c_int32),
+                ("n_blocks", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
 class KevError(RuntimeError):
@@ -74,6 +83,7 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int32
 _Z = ctypes.c_size_t
 _S = ctypes.POINTER(kev_attn_shape)
+_C = ctypes.POINTER(kev_paged_cache)
 
 
 def _sig(name, restype, *argtypes):
@@ -123,6 +133,13 @@ _c = {
     "kev_sample": _sig("kev_sample", _I, _P, _I, _I, _I, _P, _P, _P, _P, _P, _P),
     "kev_prefill_chunk": _sig("kev_prefill_chunk", _I, _P, _P, _P, _I, _P, _I, _P, _P, _P, _P, _I, _I, _P, _S, _P,
                               _Z, _P, _P),
+    "kev_paged_workspace_size": _sig("kev_paged_workspace_size", _Z, _I, _I, _S),
+    "kev_paged_write": _sig("kev_paged_write", _I, _P, _P, _I, _P, _I, _P, _C, _S, _P, _Z, _P, _P),
+    "kev_paged_read": _sig("kev_paged_read", _I, _P, _P, _I, _P, _I, _P, _C, _S, _P, _Z, _P, _P),
+    "kev_chunk_attn_paged": _sig("kev_chunk_attn_paged", _I, _P, _P, _P, _I, _P, _I, _P, _I, _C, _I, _I, _P, _S, _P,
+                                 _Z, _P, _P),
+    "kev_prefill_attn_window": _sig("kev_prefill_attn_window", _I, _P, _P, _P, _I, _P, _I, _I, _I, _P, _S, _P, _Z, _P,
+                                    _P),
 }
 
 
@@ -423,3 +440,57 @@ def kev_lora_apply(x, y, total_tokens, d_in, d_out, intervals, n_questions, adap
                               int(n_adapters), int(rank), _ptr(workspace), int(workspace_bytes), _ptr(dev_status),
                               _stream(stream))
     return _check(st, "kev_lora_apply", check)
+
+
+def make_paged_cache(k, v, block_table, max_blocks: int, n_blocks: int, dtype="bf16", k_scale=None,
+                     v_scale=None) -> kev_paged_cache:
+    """A ``kev_paged_cache`` over device tensors, which it keeps alive (pool ``k`` and ``v`` of
+    ``dtype`` "bf16", "fp32" or "e4m3"; the scales with "e4m3")."""
+    if isinstance(dtype, str):
+        dtype = {"bf16": KEV_BF16, "fp32": KEV_FP32, "e4m3": KEV_E4M3}[dtype]
+    c = kev_paged_cache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(block_table), int(max_blocks),
+                        int(n_blocks), int(dtype))
+    c.tensors = (k, v, k_scale, v_scale, block_table)
+    return c
+
+
+def kev_paged_workspace_size(n_questions: int, total_tokens: int, shape) -> int:
+    s = _shape(shape)
+    return int(_c["kev_paged_workspace_size"](int(n_questions), int(total_tokens), ctypes.byref(s)))
+
+
+def kev_paged_write(k, v, total_tokens, intervals, n_questions, prefix_lens, cache, shape, workspace,
+                    workspace_bytes, dev_status=None, stream=None, check=True) -> int:
+    s = _shape(shape)
+    st = _c["kev_paged_write"](_ptr(k), _ptr(v), int(total_tokens), _ptr(intervals), int(n_questions),
+                               _ptr(prefix_lens), ctypes.byref(cache), ctypes.byref(s), _ptr(workspace),
+                               int(workspace_bytes), _ptr(dev_status), _stream(stream))
+    return _check(st, "kev_paged_write", check)
+
+
+def kev_paged_read(k, v, total_tokens, intervals, n_questions, prefix_lens, cache, shape, workspace,
+                   workspace_bytes, dev_status=None, stream=None, check=True) -> int:
+    s = _shape(shape)
+    st = _c["kev_paged_read"](_ptr(k), _ptr(v), int(total_tokens), _ptr(intervals), int(n_questions),
+                              _ptr(prefix_lens), ctypes.byref(cache), ctypes.byref(s), _ptr(workspace),
+                              int(workspace_bytes), _ptr(dev_status), _stream(stream))
+    return _check(st, "kev_paged_read", check)
+
+
+def kev_chunk_attn_paged(q, k, v, total_tokens, intervals, n_questions, prefix_lens, max_chunk, cache, window, sinks,
+                         out, shape, workspace, workspace_bytes, dev_status=None, stream=None, check=True) -> int:
+    s = _shape(shape)
+    st = _c["kev_chunk_attn_paged"](_ptr(q), _ptr(k), _ptr(v), int(total_tokens), _ptr(intervals), int(n_questions),
+                                    _ptr(prefix_lens), int(max_chunk), ctypes.byref(cache), int(window), int(sinks),
+                                    _ptr(out), ctypes.byref(s), _ptr(workspace), int(workspace_bytes),
+                                    _ptr(dev_status), _stream(stream))
+    return _check(st, "kev_chunk_attn_paged", check)
+
+
+def kev_prefill_attn_window(q, k, v, total_tokens, intervals, n_questions, window, sinks, out, shape, workspace,
+                            workspace_bytes, dev_status=None, stream=None, check=True) -> int:
+    s = _shape(shape)
+    st = _c["kev_prefill_attn_window"](_ptr(q), _ptr(k), _ptr(v), int(total_tokens), _ptr(intervals),
+                                       int(n_questions), int(window), int(sinks), _ptr(out), ctypes.byref(s),
+                                       _ptr(workspace), int(workspace_bytes), _ptr(dev_status), _stream(stream))
+    return _check(st, "kev_prefill_attn_window", check)

@@ -1,0 +1,149 @@
+// Shared pieces of the "span" operators: attention of each question's new tokens over the span of
+// positions they see -- all earlier ones, or a sliding window and the first few (sinks) -- with
+// keys and values in a paged cache or in the packed rows themselves, and the writes and reads of
+// that cache (bf16, fp32 or e4m3 with one scale per row).
+//
+// Work.  Question i's L_i tokens sit at positions P_i .. P_i + L_i - 1.  A kv head's G q-heads
+// read the same keys, so rows are (token, q-head of the group) pairs: a row tile holds
+// floor(M / G) tokens of one question and one kv head, row = token * G + head.  An item is one or
+// two row tiles of consecutive tokens; a unit is an item and a kv head; its keys are 128-position
+// tiles: the tiles that hold sinks, then the tiles from the first token's window to the last
+// token.  The plan kernel (kev_span_plan.cu) lays all units' key tiles end to end and cuts that
+// line into equal parts, one per CTA, so every CTA does the same number of key tiles whatever the
+// lengths; the units that a cut goes through are joined from partial results.
+#pragma once
+
+#include "kev_internal.cuh"
+
+namespace kev {
+
+constexpr int kSpanKeys = 128;     // positions per key tile: one page
+constexpr int kSpanMaxCtas = 304;  // parts of the work line (2 CTAs on each of 152 SMs)
+constexpr int kSpanMaxBlocks = 1 << 20;  // pool blocks: the plan marks used blocks in a bit map in shared memory
+
+struct SpanHeader {
+  int32_t status;
+  int32_t n_items;
+  int32_t n_gaps;
+  int32_t n_new;  // tokens in questions
+};
+
+// Cut c of the work line: the unit (item, kv head) and the key tile of it where part c begins.
+// Where tile > 0 the cut is inside the unit: first = the part the unit begins in, parts = how many
+// parts it has.
+struct SpanCut {
+  int32_t item, head, tile, first, parts;
+};
+
+struct SpanItem {
+  int32_t question, token0, tokens, tiles;  // tokens [token0, token0 + tokens) of the question; key tiles
+};
+
+struct SpanLayout {
+  size_t cu;       // int32[n + 1] prefix sums of the lengths, in question order
+  size_t gaps;     // int2[n + 1] token ranges of no question
+  size_t items;    // SpanItem[max_items]
+  size_t cum;      // int64[max_items + 1] key tiles (over all kv heads) before each item
+  size_t cuts;     // SpanCut[kSpanMaxCtas + 1]
+  size_t arrived;  // int32[kSpanMaxCtas] finished parts of the unit that part c begins
+  size_t part_ml;  // float2[2 * kSpanMaxCtas][rows] running maximum (log2 units) and sum
+  size_t part_o;   // float[2 * kSpanMaxCtas][rows][d]
+  size_t total;
+  int32_t rows;    // rows of a partial result
+  int64_t max_items;
+};
+
+// Rows of a unit in the kernels: 256 on the tensor cores (two 128-row tiles), 64 on the CUDA
+// cores, 16 for a few rows.
+inline SpanLayout span_layout(int32_t n, int32_t T, int32_t group, int32_t d) {
+  SpanLayout L;
+  const int64_t rows = (int64_t)T * group;
+  L.rows = (int32_t)(rows < 16 ? 16 : rows > 256 ? 256 : (rows + 15) / 16 * 16);
+  L.max_items = (int64_t)T / 4 + n + 1;  // an item holds at least 4 tokens or a question's last ones
+  size_t off = align_up(sizeof(SpanHeader), 256);
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align_up(off + bytes, 256);
+    return at;
+  };
+  L.cu = take(sizeof(int32_t) * ((size_t)n + 1));
+  L.gaps = take(sizeof(int2) * ((size_t)n + 1));
+  L.items = take(sizeof(SpanItem) * (size_t)L.max_items);
+  L.cum = take(sizeof(int64_t) * ((size_t)L.max_items + 1));
+  L.cuts = take(sizeof(SpanCut) * (kSpanMaxCtas + 1));
+  L.arrived = take(sizeof(int32_t) * kSpanMaxCtas);
+  L.part_ml = take(sizeof(float2) * 2 * kSpanMaxCtas * (size_t)L.rows);
+  L.part_o = take(sizeof(float) * 2 * kSpanMaxCtas * (size_t)L.rows * d);
+  L.total = off;
+  return L;
+}
+
+// Everything the span kernels take.
+struct SpanArgs {
+  const void* q;
+  const void* k;  // packed new rows (the keys themselves without a cache)
+  const void* v;
+  void* out;
+  const kev_interval* intervals;
+  const int32_t* prefix;  // null: 0
+  int32_t n, T;
+  int32_t h_q, h_kv, group, d;
+  int32_t elem;       // bytes of a q/k/v/out element: 2 bf16, 4 fp32
+  int32_t pool_elem;  // bytes of a cached element: 0 no cache, 1 e4m3, 2 bf16, 4 fp32
+  float scale;
+  void* pool_k;
+  void* pool_v;
+  float* scale_k;
+  float* scale_v;
+  const int32_t* table;
+  int32_t max_blocks, n_blocks;
+  int32_t window, sinks;  // window 0: every earlier position
+  int32_t max_chunk;      // no question has more tokens
+  int32_t tile_rows;      // M: rows of a row tile (128, 64 or 16)
+  int32_t tile_tokens;    // floor(M / group)
+  int32_t item_tiles;     // row tiles of an item
+  int32_t ctas;           // parts of the work line
+  int32_t attend;         // 0: cache write or read only (no items)
+  char* ws;
+  SpanLayout layout;
+  int32_t* dev_status;
+};
+
+cudaError_t launch_span_plan(const SpanArgs& a, cudaStream_t s);
+cudaError_t launch_span_write(const SpanArgs& a, int num_sms, cudaStream_t s);
+cudaError_t launch_span_read(const SpanArgs& a, void* k_out, void* v_out, int num_sms, cudaStream_t s);
+cudaError_t launch_span_simt(const SpanArgs& a, cudaStream_t s);
+cudaError_t launch_span_merge(const SpanArgs& a, int num_sms, cudaStream_t s);
+
+// Key tiles of tokens at positions p0 .. p1: tile j holds positions 128 * at(j) ...
+struct SpanTiles {
+  int ns, lo, n;  // sink tiles 0 .. ns - 1, then tiles lo .. lo + n - ns - 1
+  __host__ __device__ SpanTiles(int p0, int p1, int window, int sinks) {
+    lo = window > 0 && p0 >= window ? (p0 - window + 1) / kSpanKeys : 0;
+    const int s = (int)(((int64_t)sinks + kSpanKeys - 1) / kSpanKeys);
+    ns = s < lo ? s : lo;
+    n = ns + p1 / kSpanKeys - lo + 1;
+  }
+  __host__ __device__ int at(int j) const { return j < ns ? j : lo + (j - ns); }
+};
+
+// Is position u visible to the token at position p?
+__device__ __forceinline__ bool span_sees(int p, int u, int window, int sinks) {
+  return u <= p && (window == 0 || p - u < window || u < sinks);
+}
+
+// Rows of tokens in no question are zero: the calling CTA's share, all its threads.
+__device__ __forceinline__ void span_zero_gaps(const SpanArgs& a) {
+  const SpanHeader* h = reinterpret_cast<const SpanHeader*>(a.ws);
+  const int2* gaps = reinterpret_cast<const int2*>(a.ws + a.layout.gaps);
+  const int64_t vec = (int64_t)a.h_q * a.d * a.elem / 16;
+  uint4* out = static_cast<uint4*>(a.out);
+  for (int i = 0; i < h->n_gaps; ++i) {
+    const int2 g = gaps[i];
+    for (int64_t x = g.x * vec + (int64_t)blockIdx.x * blockDim.x + threadIdx.x; x < g.y * vec;
+         x += (int64_t)gridDim.x * blockDim.x)
+      out[x] = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+}  // namespace kev

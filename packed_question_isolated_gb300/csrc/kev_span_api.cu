@@ -1,0 +1,181 @@
+// Host side of the span operators of include/kev.h: argument checks and launches.
+#include <math.h>
+
+#include "kev_span.cuh"
+
+using namespace kev;
+
+namespace {
+
+bool aligned(const void* p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
+
+kev_status from_cuda(cudaError_t e) { return e == cudaSuccess ? KEV_OK : KEV_ERR_CUDA; }
+
+int sms_of_current_device() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  return sms;
+}
+
+kev_status check_span_shape(const kev_attn_shape* s) {
+  if (!s || s->h_q <= 0 || s->h_kv <= 0) return KEV_ERR_INVALID_ARG;
+  if (s->h_q % s->h_kv || s->h_q / s->h_kv > 16) return KEV_ERR_UNSUPPORTED;
+  if (s->dtype != KEV_BF16 && s->dtype != KEV_FP32) return KEV_ERR_UNSUPPORTED;
+  if (s->d_h != 64 && s->d_h != 128) return KEV_ERR_UNSUPPORTED;
+  if (!(s->scale >= 0.f) || isinf(s->scale)) return KEV_ERR_INVALID_ARG;
+  return KEV_OK;
+}
+
+// The arguments every span call shares, checked and laid out.
+kev_status span_common(SpanArgs* a, int32_t T, const kev_interval* intervals, int32_t n, const kev_attn_shape* shape,
+                       void* ws, size_t ws_bytes, int32_t* dev_status) {
+  const kev_status st = check_span_shape(shape);
+  if (st != KEV_OK) return st;
+  if (T < 0 || n < 0) return KEV_ERR_INVALID_ARG;
+  if (n > kMaxQuestions) return KEV_ERR_UNSUPPORTED;
+  if (n > 0 && (!intervals || !aligned(intervals, 8))) return KEV_ERR_INVALID_ARG;
+  if (!ws || !aligned(ws, 256) || !aligned(dev_status, 4)) return KEV_ERR_INVALID_ARG;
+  *a = SpanArgs{};
+  a->intervals = intervals;
+  a->n = n;
+  a->T = T;
+  a->h_q = shape->h_q;
+  a->h_kv = shape->h_kv;
+  a->group = shape->h_q / shape->h_kv;
+  a->d = shape->d_h;
+  a->elem = shape->dtype == KEV_BF16 ? 2 : 4;
+  a->scale = shape->scale == 0.f ? 1.0f / sqrtf((float)shape->d_h) : shape->scale;
+  a->max_chunk = T;
+  a->ws = static_cast<char*>(ws);
+  a->layout = span_layout(n, T, a->group, a->d);
+  a->dev_status = dev_status;
+  return ws_bytes < a->layout.total ? KEV_ERR_INVALID_ARG : KEV_OK;
+}
+
+kev_status span_cache(SpanArgs* a, const kev_attn_shape* shape, const int32_t* prefix_lens, const kev_paged_cache* c) {
+  if (!c || !c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16)) return KEV_ERR_INVALID_ARG;
+  if (c->n_blocks <= 0 || c->max_blocks <= 0 || !c->block_table || !aligned(c->block_table, 4)) return KEV_ERR_INVALID_ARG;
+  if (c->dtype != KEV_E4M3 && c->dtype != shape->dtype) return KEV_ERR_UNSUPPORTED;
+  if (c->dtype == KEV_E4M3 && (!c->k_scale || !c->v_scale || !aligned(c->k_scale, 16) || !aligned(c->v_scale, 16)))
+    return KEV_ERR_INVALID_ARG;
+  if (c->n_blocks > kSpanMaxBlocks || (int64_t)c->max_blocks * kPage > (1 << 30) ||
+      (int64_t)c->n_blocks * a->h_kv * kPage > 0x7fffffffll)  // cached rows: coordinates of tensor copies
+    return KEV_ERR_UNSUPPORTED;
+  if (a->n > 0 && (!prefix_lens || !aligned(prefix_lens, 4))) return KEV_ERR_INVALID_ARG;
+  a->prefix = prefix_lens;
+  a->pool_k = c->k;
+  a->pool_v = c->v;
+  a->scale_k = c->k_scale;
+  a->scale_v = c->v_scale;
+  a->table = c->block_table;
+  a->max_blocks = c->max_blocks;
+  a->n_blocks = c->n_blocks;
+  a->pool_elem = c->dtype == KEV_E4M3 ? 1 : c->dtype == KEV_BF16 ? 2 : 4;
+  return KEV_OK;
+}
+
+void span_tiling(SpanArgs* a, int rows, int tiles, int ctas) {
+  a->attend = 1;
+  a->tile_rows = rows;
+  a->tile_tokens = rows / a->group;
+  a->item_tiles = tiles;
+  a->ctas = ctas;
+}
+
+kev_status span_attend(SpanArgs* a, bool write, cudaStream_t s) {
+  const int sms = sms_of_current_device();
+  if (sms <= 0) return KEV_ERR_CUDA;
+  span_tiling(a, 64, 1, 2 * sms < kSpanMaxCtas ? 2 * sms : kSpanMaxCtas);
+  cudaError_t e = launch_span_plan(*a, s);
+  if (e == cudaSuccess && write) e = launch_span_write(*a, sms, s);
+  if (e == cudaSuccess) e = launch_span_simt(*a, s);
+  if (e == cudaSuccess) e = launch_span_merge(*a, sms, s);
+  return from_cuda(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t kev_paged_workspace_size(int32_t n_questions, int32_t total_tokens, const kev_attn_shape* shape) {
+  if (check_span_shape(shape) != KEV_OK || n_questions < 0 || n_questions > kMaxQuestions || total_tokens < 0) return 0;
+  return span_layout(n_questions, total_tokens, shape->h_q / shape->h_kv, shape->d_h).total;
+}
+
+kev_status kev_paged_write(const void* k, const void* v, int32_t total_tokens, const kev_interval* intervals,
+                           int32_t n_questions, const int32_t* prefix_lens, const kev_paged_cache* cache,
+                           const kev_attn_shape* shape, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                           kev_stream_t stream) {
+  SpanArgs a;
+  kev_status st = span_common(&a, total_tokens, intervals, n_questions, shape, workspace, workspace_bytes, dev_status);
+  if (st == KEV_OK) st = span_cache(&a, shape, prefix_lens, cache);
+  if (st != KEV_OK) return st;
+  if (total_tokens > 0 && (!k || !v || !aligned(k, 16) || !aligned(v, 16))) return KEV_ERR_INVALID_ARG;
+  const int sms = sms_of_current_device();
+  if (sms <= 0) return KEV_ERR_CUDA;
+  a.k = k;
+  a.v = v;
+  cudaError_t e = launch_span_plan(a, (cudaStream_t)stream);
+  if (e == cudaSuccess) e = launch_span_write(a, sms, (cudaStream_t)stream);
+  return from_cuda(e);
+}
+
+kev_status kev_paged_read(void* k, void* v, int32_t total_tokens, const kev_interval* intervals, int32_t n_questions,
+                          const int32_t* prefix_lens, const kev_paged_cache* cache, const kev_attn_shape* shape,
+                          void* workspace, size_t workspace_bytes, int32_t* dev_status, kev_stream_t stream) {
+  SpanArgs a;
+  kev_status st = span_common(&a, total_tokens, intervals, n_questions, shape, workspace, workspace_bytes, dev_status);
+  if (st == KEV_OK) st = span_cache(&a, shape, prefix_lens, cache);
+  if (st != KEV_OK) return st;
+  if (total_tokens > 0 && (!k || !v || !aligned(k, 16) || !aligned(v, 16))) return KEV_ERR_INVALID_ARG;
+  const int sms = sms_of_current_device();
+  if (sms <= 0) return KEV_ERR_CUDA;
+  cudaError_t e = launch_span_plan(a, (cudaStream_t)stream);
+  if (e == cudaSuccess) e = launch_span_read(a, k, v, sms, (cudaStream_t)stream);
+  return from_cuda(e);
+}
+
+kev_status kev_chunk_attn_paged(const void* q, const void* k, const void* v, int32_t total_tokens,
+                                const kev_interval* intervals, int32_t n_questions, const int32_t* prefix_lens,
+                                int32_t max_chunk, const kev_paged_cache* cache, int32_t window, int32_t sinks, void* out,
+                                const kev_attn_shape* shape, void* workspace, size_t workspace_bytes,
+                                int32_t* dev_status, kev_stream_t stream) {
+  SpanArgs a;
+  kev_status st = span_common(&a, total_tokens, intervals, n_questions, shape, workspace, workspace_bytes, dev_status);
+  if (st == KEV_OK) st = span_cache(&a, shape, prefix_lens, cache);
+  if (st != KEV_OK) return st;
+  if (window < 0 || sinks < 0 || max_chunk < 0) return KEV_ERR_INVALID_ARG;
+  if ((k == nullptr) != (v == nullptr) || !aligned(k, 16) || !aligned(v, 16)) return KEV_ERR_INVALID_ARG;
+  if (total_tokens > 0 && (!q || !out || !aligned(q, 16) || !aligned(out, 16))) return KEV_ERR_INVALID_ARG;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.out = out;
+  a.window = window;
+  a.sinks = sinks;
+  if (max_chunk > 0 && max_chunk < a.max_chunk) a.max_chunk = max_chunk;
+  return span_attend(&a, k != nullptr, (cudaStream_t)stream);
+}
+
+kev_status kev_prefill_attn_window(const void* q, const void* k, const void* v, int32_t total_tokens,
+                                   const kev_interval* intervals, int32_t n_questions, int32_t window, int32_t sinks,
+                                   void* out, const kev_attn_shape* shape, void* workspace, size_t workspace_bytes,
+                                   int32_t* dev_status, kev_stream_t stream) {
+  SpanArgs a;
+  const kev_status st =
+      span_common(&a, total_tokens, intervals, n_questions, shape, workspace, workspace_bytes, dev_status);
+  if (st != KEV_OK) return st;
+  if (window < 0 || sinks < 0) return KEV_ERR_INVALID_ARG;
+  if (total_tokens > 0 && (!q || !k || !v || !out || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16)))
+    return KEV_ERR_INVALID_ARG;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.out = out;
+  a.window = window;
+  a.sinks = sinks;
+  return span_attend(&a, false, (cudaStream_t)stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,243 @@
+// Writing new K/V rows into a paged cache in the cache's own type, and reading cached rows back.
+//
+// An e4m3 cache holds, for each position and kv head, the row x (d elements) as codes
+// c_e = rn_e4m3(x_e / s) and one fp32 scale s = max_e |x_e| / 448 (448: the largest e4m3 value), so
+// a row's largest element is stored exactly up to fp32 rounding and every other one within half
+// an e4m3 step of its size (relative 2^-4, or 2^-10 s below the normal range).  A row of zeros has
+// s = 0 and codes 0; a row that holds a NaN or an infinity has a scale that is not finite and
+// reads back as NaN throughout.  Reading gives c_e * s, rounded once to the output type.  Both
+// divisions are IEEE: the codes do not depend on the kernel's shape.
+//
+// Bound by memory: 2 T H_kv (d elem + d + 4) bytes each way for an e4m3 cache.  A warp takes one
+// token's K or V rows of all kv heads: one search for the token's question and one page look-up,
+// then 16-byte loads with up to 4 in flight per lane (8 heads of 128 bf16: exactly 4).
+#include <cuda_fp8.h>
+
+#include "kev_span.cuh"
+
+namespace kev {
+namespace {
+
+constexpr int kThreads = 256;
+
+// the question of new token x: the last i with cu[i] <= x (empty questions share their successor's value)
+__device__ __forceinline__ int question_of(const int32_t* cu, int n, int x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (cu[mid] <= x) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+struct Place {
+  int token;      // packed row
+  int64_t block;  // pool block, row of it
+  int row;
+};
+__device__ __forceinline__ Place place_of(const SpanArgs& a, const int32_t* cu, int x) {
+  const int i = question_of(cu, a.n, x);
+  const int j = x - cu[i];
+  const int p = (a.prefix ? a.prefix[i] : 0) + j;
+  return {a.intervals[i].begin + j, a.table[(int64_t)i * a.max_blocks + p / kPage], p % kPage};
+}
+
+template <int E> struct Vec;  // 16 bytes of a row as floats
+template <> struct Vec<4> {
+  static constexpr int n = 4;
+  static __device__ void get(uint4 w, float (&f)[4]) {
+    f[0] = __uint_as_float(w.x);
+    f[1] = __uint_as_float(w.y);
+    f[2] = __uint_as_float(w.z);
+    f[3] = __uint_as_float(w.w);
+  }
+  static __device__ uint4 put(const float (&f)[4]) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  }
+};
+template <> struct Vec<2> {
+  static constexpr int n = 8;
+  static __device__ void get(uint4 w, float (&f)[8]) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(u[i] << 16);
+      f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+  }
+  static __device__ uint4 put(const float (&f)[8]) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      u[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+  }
+};
+
+// max |x| that keeps NaN
+__device__ __forceinline__ float nan_max(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// two e4m3 codes, the first in the low byte
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+template <int E, int D, bool Q8>
+__global__ void __launch_bounds__(kThreads) span_write_kernel(SpanArgs a) {
+  using V = Vec<E>;
+  constexpr int kLanes = D / V::n;       // lanes of a row: 8, 16 or 32
+  constexpr int kRows = 32 / kLanes;     // rows a warp handles at once
+  constexpr int kFlight = 4;             // of those in flight
+  pdl_wait();
+  pdl_trigger();
+  const SpanHeader* h = reinterpret_cast<const SpanHeader*>(a.ws);
+  if (h->status != ST_OK) return;
+  const int32_t* cu = reinterpret_cast<const int32_t*>(a.ws + a.layout.cu);
+  const int lane = threadIdx.x & 31, sub = lane % kLanes, r0 = lane / kLanes;
+  const int warps = gridDim.x * (kThreads / 32);
+  const int64_t todo = 2 * (int64_t)h->n_new;
+  for (int64_t w = blockIdx.x * (kThreads / 32) + threadIdx.x / 32; w < todo; w += warps) {
+    const Place at = place_of(a, cu, (int)(w >> 1));
+    const bool is_v = w & 1;
+    const uint4* src = static_cast<const uint4*>(is_v ? a.v : a.k) + (int64_t)at.token * a.h_kv * kLanes;
+    const int64_t cell0 = at.block * a.h_kv * kPage + at.row;  // + head * kPage: the cached row
+    for (int g0 = 0; g0 < a.h_kv; g0 += kRows * kFlight) {
+      uint4 x[kFlight];
+#pragma unroll
+      for (int e = 0; e < kFlight; ++e) {
+        const int g = g0 + e * kRows + r0;
+        if (g < a.h_kv) x[e] = src[g * kLanes + sub];
+      }
+#pragma unroll
+      for (int e = 0; e < kFlight; ++e) {
+        const int g = g0 + e * kRows + r0;
+        const int64_t cell = cell0 + (int64_t)g * kPage;
+        if (!Q8) {
+          if (g < a.h_kv) static_cast<uint4*>(is_v ? a.pool_v : a.pool_k)[cell * kLanes + sub] = x[e];
+        } else {
+          float f[V::n], top = 0.f;
+          if (g >= a.h_kv) x[e] = make_uint4(0u, 0u, 0u, 0u);
+          V::get(x[e], f);
+#pragma unroll
+          for (int i = 0; i < V::n; ++i) top = nan_max(top, fabsf(f[i]));
+#pragma unroll
+          for (int o = kLanes / 2; o > 0; o >>= 1) top = nan_max(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const float scale = __fdiv_rn(top, 448.f);
+          uint32_t c[V::n / 4];
+#pragma unroll
+          for (int i = 0; i < V::n / 4; ++i) {
+            float y[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] = scale == 0.f ? 0.f : __fdiv_rn(f[4 * i + j], scale);
+            c[i] = e4m3x2(y[0], y[1]) | e4m3x2(y[2], y[3]) << 16;
+          }
+          if (g < a.h_kv) {
+            unsigned char* dst = static_cast<unsigned char*>(is_v ? a.pool_v : a.pool_k) + cell * D + sub * V::n;
+            if (V::n == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(c[0], c[V::n / 4 - 1]);
+            else *reinterpret_cast<uint32_t*>(dst) = c[0];
+            if (sub == 0) (is_v ? a.scale_v : a.scale_k)[cell] = scale;
+          }
+        }
+      }
+    }
+  }
+}
+
+template <int E, int D, bool Q8>
+__global__ void __launch_bounds__(kThreads) span_read_kernel(SpanArgs a, void* k_out, void* v_out) {
+  using V = Vec<E>;
+  constexpr int kLanes = D / V::n, kRows = 32 / kLanes, kFlight = 4;
+  pdl_wait();
+  pdl_trigger();
+  const SpanHeader* h = reinterpret_cast<const SpanHeader*>(a.ws);
+  if (h->status != ST_OK) return;
+  const int32_t* cu = reinterpret_cast<const int32_t*>(a.ws + a.layout.cu);
+  const int lane = threadIdx.x & 31, sub = lane % kLanes, r0 = lane / kLanes;
+  const int warps = gridDim.x * (kThreads / 32);
+  const int64_t todo = 2 * (int64_t)h->n_new;
+  for (int64_t w = blockIdx.x * (kThreads / 32) + threadIdx.x / 32; w < todo; w += warps) {
+    const Place at = place_of(a, cu, (int)(w >> 1));
+    const bool is_v = w & 1;
+    uint4* dst = static_cast<uint4*>(is_v ? v_out : k_out) + (int64_t)at.token * a.h_kv * kLanes;
+    const int64_t cell0 = at.block * a.h_kv * kPage + at.row;
+    for (int g0 = 0; g0 < a.h_kv; g0 += kRows * kFlight) {
+      uint4 x[kFlight];
+      float s[kFlight];
+#pragma unroll
+      for (int e = 0; e < kFlight; ++e) {
+        const int g = g0 + e * kRows + r0;
+        const int64_t cell = cell0 + (int64_t)g * kPage;
+        if (g >= a.h_kv) continue;
+        if (Q8) {
+          const unsigned char* src = static_cast<const unsigned char*>(is_v ? a.pool_v : a.pool_k) + cell * D + sub * V::n;
+          if (V::n == 8) {
+            const uint2 c = *reinterpret_cast<const uint2*>(src);
+            x[e] = make_uint4(c.x, c.y, 0u, 0u);
+          } else {
+            x[e].x = *reinterpret_cast<const uint32_t*>(src);
+          }
+          s[e] = (is_v ? a.scale_v : a.scale_k)[cell];
+        } else {
+          x[e] = static_cast<const uint4*>(is_v ? a.pool_v : a.pool_k)[cell * kLanes + sub];
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < kFlight; ++e) {
+        const int g = g0 + e * kRows + r0;
+        if (g >= a.h_kv) continue;
+        if (Q8) {
+          const uint32_t c[2] = {x[e].x, x[e].y};
+          float f[V::n];
+#pragma unroll
+          for (int i = 0; i < V::n; i += 2) {
+            uint32_t half2;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(half2) : "h"((uint16_t)(c[i / 4] >> (i % 4 * 8))));
+            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&half2));
+            f[i] = v.x * s[e];
+            f[i + 1] = v.y * s[e];
+          }
+          dst[g * kLanes + sub] = V::put(f);
+        } else {
+          dst[g * kLanes + sub] = x[e];
+        }
+      }
+    }
+  }
+}
+
+int grid_of(const SpanArgs& a, int num_sms) {  // one warp per token and side, 8 CTAs of 8 warps per SM at most
+  const int64_t ctas = (2 * (int64_t)a.T + kThreads / 32 - 1) / (kThreads / 32);
+  return (int)(ctas < 8 * num_sms ? ctas : 8 * num_sms);
+}
+
+}  // namespace
+
+cudaError_t launch_span_write(const SpanArgs& a, int num_sms, cudaStream_t s) {
+  if (a.T <= 0) return cudaSuccess;
+  const bool q8 = a.pool_elem == 1;
+  auto kern = a.elem == 2 ? (a.d == 64 ? (q8 ? span_write_kernel<2, 64, true> : span_write_kernel<2, 64, false>)
+                                       : (q8 ? span_write_kernel<2, 128, true> : span_write_kernel<2, 128, false>))
+                          : (a.d == 64 ? (q8 ? span_write_kernel<4, 64, true> : span_write_kernel<4, 64, false>)
+                                       : (q8 ? span_write_kernel<4, 128, true> : span_write_kernel<4, 128, false>));
+  return launch_pdl(kern, dim3(grid_of(a, num_sms)), dim3(kThreads), 0, s, a);
+}
+
+cudaError_t launch_span_read(const SpanArgs& a, void* k_out, void* v_out, int num_sms, cudaStream_t s) {
+  if (a.T <= 0) return cudaSuccess;
+  const bool q8 = a.pool_elem == 1;
+  auto kern = a.elem == 2 ? (a.d == 64 ? (q8 ? span_read_kernel<2, 64, true> : span_read_kernel<2, 64, false>)
+                                       : (q8 ? span_read_kernel<2, 128, true> : span_read_kernel<2, 128, false>))
+                          : (a.d == 64 ? (q8 ? span_read_kernel<4, 64, true> : span_read_kernel<4, 64, false>)
+                                       : (q8 ? span_read_kernel<4, 128, true> : span_read_kernel<4, 128, false>));
+  return launch_pdl(kern, dim3(grid_of(a, num_sms)), dim3(kThreads), 0, s, a, k_out, v_out);
+}
+
+}  // namespace kev
