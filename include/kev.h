@@ -397,7 +397,8 @@ int32_t kev_assign_blocks(const int32_t* need, int32_t n, uint8_t* free_map, int
  * scale s at the same place, s = max_e |x_e| / 448 and c_e = x_e / s rounded to the nearest e4m3
  * value (ties to even): each element comes back as c_e * s, off by at most max(2^-4 |x_e|,
  * 2^-10 s) and the last place of s.  A row of zeros has s = 0.  A row that holds a NaN or an
- * infinity comes back as NaN throughout. */
+ * infinity has s = NaN and comes back as NaN throughout (rows of a cache filled by other means
+ * keep to this: the NaN codes 0x7f and 0xff only under a NaN scale). */
 typedef struct {
   void* k;                    /* [n_blocks, H_kv, KEV_PAGE, d_h] of dtype, 16-byte aligned */
   void* v;

@@ -709,10 +709,12 @@ def e4m3_round(x):
 
 def quantise_rows(x):
     """x [..., d] float32 -> (code values float64 [..., d], scales float32 [...]): scale = max|x| / 448 and
-    code = x / scale rounded to e4m3, both quotients rounded to float32 first (the stored form)."""
+    code = x / scale rounded to e4m3, both quotients rounded to float32 first (the stored form); a row that
+    holds a NaN or an infinity has a NaN for its scale."""
     x = np.asarray(x, np.float32)
     with np.errstate(divide="ignore", invalid="ignore", over="ignore"):
-        scale = (np.abs(x).max(-1) / np.float32(448.0)).astype(np.float32)
+        top = np.abs(x).max(-1)
+        scale = np.where(np.isfinite(top), top / np.float32(448.0), np.float32(np.nan)).astype(np.float32)
         y = np.where(scale[..., None] == 0, np.float32(0), x / scale[..., None]).astype(np.float32)
     return e4m3_round(y), scale
 

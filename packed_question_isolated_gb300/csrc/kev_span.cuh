@@ -35,8 +35,13 @@ struct SpanCut {
   int32_t item, head, tile, first, parts;
 };
 
-struct SpanItem {
-  int32_t question, token0, tokens, tiles;  // tokens [token0, token0 + tokens) of the question; key tiles
+struct alignas(16) SpanItem {
+  int32_t row0;      // packed row of its first token
+  int32_t p0;        // that token's position
+  int32_t tokens;    // its tokens
+  int32_t tiles;     // key tiles they see
+  int32_t question;
+  int32_t pad[3];
 };
 
 struct SpanLayout {
@@ -58,7 +63,7 @@ struct SpanLayout {
 inline SpanLayout span_layout(int32_t n, int32_t T, int32_t group, int32_t d) {
   SpanLayout L;
   const int64_t rows = (int64_t)T * group;
-  L.rows = (int32_t)(rows < 16 ? 16 : rows > 256 ? 256 : (rows + 15) / 16 * 16);
+  L.rows = (int32_t)(rows > 224 ? 256 : (rows + 31) / 16 * 16);  // up to 11 rows lie unused between two tiles
   L.max_items = (int64_t)T / 4 + n + 1;  // an item holds at least 4 tokens or a question's last ones
   size_t off = align_up(sizeof(SpanHeader), 256);
   auto take = [&](size_t bytes) {
@@ -112,7 +117,8 @@ struct SpanArgs {
 cudaError_t launch_span_plan(const SpanArgs& a, cudaStream_t s);
 cudaError_t launch_span_write(const SpanArgs& a, int num_sms, cudaStream_t s);
 cudaError_t launch_span_read(const SpanArgs& a, void* k_out, void* v_out, int num_sms, cudaStream_t s);
-cudaError_t launch_span_simt(const SpanArgs& a, cudaStream_t s);
+cudaError_t launch_span_simt(const SpanArgs& a, cudaStream_t s);  // fp32
+cudaError_t launch_span_tc(const SpanArgs& a, cudaStream_t s);    // bf16
 cudaError_t launch_span_merge(const SpanArgs& a, int num_sms, cudaStream_t s);
 
 // Key tiles of tokens at positions p0 .. p1: tile j holds positions 128 * at(j) ...
@@ -127,21 +133,61 @@ struct SpanTiles {
   __host__ __device__ int at(int j) const { return j < ns ? j : lo + (j - ns); }
 };
 
+// The units of part `part` of the work line, one after the other: unit (item, head) and its key
+// tiles [j0, j1).  The next item's record is loaded while the current one is worked on.
+struct SpanWalk {
+  const SpanItem* items;
+  SpanItem item, ahead;
+  SpanCut to;
+  int it, head, h_kv, j0, j1;
+  __device__ __forceinline__ SpanWalk(const SpanArgs& a, int part) {
+    items = reinterpret_cast<const SpanItem*>(a.ws + a.layout.items);
+    const SpanCut* cuts = reinterpret_cast<const SpanCut*>(a.ws + a.layout.cuts);
+    const SpanCut from = cuts[part];
+    to = cuts[part + 1];
+    it = from.item;
+    head = from.head;
+    h_kv = a.h_kv;
+    j0 = from.tile;
+    if (live()) {
+      item = items[it];
+      if (it < to.item) ahead = items[it + 1];  // one record past the last item is laid out
+      j1 = last();
+    }
+  }
+  __device__ __forceinline__ int last() const { return it == to.item && head == to.head ? to.tile : item.tiles; }
+  __device__ __forceinline__ bool live() const {
+    return it < to.item || (it == to.item && (head < to.head || (head == to.head && j0 < to.tile)));
+  }
+  __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == item.tiles; }
+  // slot of this unit's partial result: the unit began in an earlier part, or ends in a later one
+  __device__ __forceinline__ int64_t slot(int part) const { return 2 * (int64_t)part + (j0 == 0); }
+  __device__ __forceinline__ void next() {
+    j0 = 0;
+    if (++head == h_kv) {
+      head = 0;
+      ++it;
+      item = ahead;
+      if (it < to.item) ahead = items[it + 1];
+    }
+    j1 = last();
+  }
+};
+
 // Is position u visible to the token at position p?
 __device__ __forceinline__ bool span_sees(int p, int u, int window, int sinks) {
   return u <= p && (window == 0 || p - u < window || u < sinks);
 }
 
-// Rows of tokens in no question are zero: the calling CTA's share, all its threads.
-__device__ __forceinline__ void span_zero_gaps(const SpanArgs& a) {
+// Rows of tokens in no question are zero: the calling CTA's share, by its first `threads` threads.
+__device__ __forceinline__ void span_zero_gaps(const SpanArgs& a, int threads) {
   const SpanHeader* h = reinterpret_cast<const SpanHeader*>(a.ws);
   const int2* gaps = reinterpret_cast<const int2*>(a.ws + a.layout.gaps);
   const int64_t vec = (int64_t)a.h_q * a.d * a.elem / 16;
   uint4* out = static_cast<uint4*>(a.out);
   for (int i = 0; i < h->n_gaps; ++i) {
     const int2 g = gaps[i];
-    for (int64_t x = g.x * vec + (int64_t)blockIdx.x * blockDim.x + threadIdx.x; x < g.y * vec;
-         x += (int64_t)gridDim.x * blockDim.x)
+    for (int64_t x = g.x * vec + (int64_t)blockIdx.x * threads + threadIdx.x; x < g.y * vec; x += (int64_t)gridDim.x * threads)
       out[x] = make_uint4(0u, 0u, 0u, 0u);
   }
 }

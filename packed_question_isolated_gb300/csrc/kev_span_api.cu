@@ -86,10 +86,12 @@ void span_tiling(SpanArgs* a, int rows, int tiles, int ctas) {
 kev_status span_attend(SpanArgs* a, bool write, cudaStream_t s) {
   const int sms = sms_of_current_device();
   if (sms <= 0) return KEV_ERR_CUDA;
-  span_tiling(a, 64, 1, 2 * sms < kSpanMaxCtas ? 2 * sms : kSpanMaxCtas);
+  const bool tc = a->elem == 2;
+  const int ctas = tc ? sms : 2 * sms;
+  span_tiling(a, tc ? 128 : 64, tc ? 2 : 1, ctas < kSpanMaxCtas ? ctas : kSpanMaxCtas);
   cudaError_t e = launch_span_plan(*a, s);
   if (e == cudaSuccess && write) e = launch_span_write(*a, sms, s);
-  if (e == cudaSuccess) e = launch_span_simt(*a, s);
+  if (e == cudaSuccess) e = tc ? launch_span_tc(*a, s) : launch_span_simt(*a, s);
   if (e == cudaSuccess) e = launch_span_merge(*a, sms, s);
   return from_cuda(e);
 }

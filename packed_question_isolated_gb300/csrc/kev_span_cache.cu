@@ -4,8 +4,8 @@
 // c_e = rn_e4m3(x_e / s) and one fp32 scale s = max_e |x_e| / 448 (448: the largest e4m3 value), so
 // a row's largest element is stored exactly up to fp32 rounding and every other one within half
 // an e4m3 step of its size (relative 2^-4, or 2^-10 s below the normal range).  A row of zeros has
-// s = 0 and codes 0; a row that holds a NaN or an infinity has a scale that is not finite and
-// reads back as NaN throughout.  Reading gives c_e * s, rounded once to the output type.  Both
+// s = 0 and codes 0; a row that holds a NaN or an infinity has a NaN for its scale and reads
+// back as NaN throughout.  Reading gives c_e * s, rounded once to the output type.  Both
 // divisions are IEEE: the codes do not depend on the kernel's shape.
 //
 // Bound by memory: 2 T H_kv (d elem + d + 4) bytes each way for an e4m3 cache.  A warp takes one
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kThreads) span_write_kernel(SpanArgs a) {
           for (int i = 0; i < V::n; ++i) top = nan_max(top, fabsf(f[i]));
 #pragma unroll
           for (int o = kLanes / 2; o > 0; o >>= 1) top = nan_max(top, __shfl_xor_sync(0xffffffffu, top, o));
-          const float scale = __fdiv_rn(top, 448.f);
+          const float scale = top < INFINITY ? __fdiv_rn(top, 448.f) : __int_as_float(0x7fffffff);
           uint32_t c[V::n / 4];
 #pragma unroll
           for (int i = 0; i < V::n / 4; ++i) {

@@ -265,11 +265,13 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(SpanArgs a) {
         else hi = mid - 1;
       }
       SpanItem w;
+      const kev_interval v = a.intervals[lo];
+      const int token0 = (x - s_base[lo]) * item_tokens;
       w.question = lo;
-      w.token0 = (x - s_base[lo]) * item_tokens;
-      w.tokens = min(item_tokens, a.intervals[lo].end - a.intervals[lo].begin - w.token0);
-      const int p0 = prefix_of(lo) + w.token0;
-      w.tiles = SpanTiles(p0, p0 + w.tokens - 1, a.window, a.sinks).n;
+      w.row0 = v.begin + token0;
+      w.tokens = min(item_tokens, v.end - w.row0);
+      w.p0 = prefix_of(lo) + token0;
+      w.tiles = SpanTiles(w.p0, w.p0 + w.tokens - 1, a.window, a.sinks).n;
       out[x] = w;
       tiles = (long long)w.tiles * a.h_kv;
     }

@@ -1,4 +1,4 @@
-// Span attention on the CUDA cores: fp32 products (no TF32), q, k, v and out in fp32 or bf16, any cache.
+// Span attention on the CUDA cores: fp32 q, k, v (true fp32 products, no TF32), cache fp32 or e4m3.
 //
 // out = softmax(scale q K^T + M) V over the visible positions, one pass: running maximum m and sum
 // l of each row (log2 units), the accumulator rescaled when m moves, divided by l at the end.
@@ -23,24 +23,17 @@ template <int D> struct Smem {
   float p[kThreads / 32][kSub][kWarpRows];
 };
 
-// 4 consecutive elements, `elem` bytes each (bf16 or fp32)
-__device__ __forceinline__ float4 get4(const void* p, int64_t at, int elem) {
-  if (elem == 4) return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
-  const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + at);
-  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
-                     __uint_as_float(w.y & 0xffff0000u));
-}
-
 // 4 elements of row u of question i, kv head g
 template <int D>
 __device__ __forceinline__ float4 load4(const SpanArgs& a, bool is_v, int i, int begin, int g, int u, int e) {
   if (a.pool_elem == 0) {
     const int64_t at = ((int64_t)(begin + u) * a.h_kv + g) * D + e;
-    return get4(is_v ? a.v : a.k, at, a.elem);
+    return *reinterpret_cast<const float4*>(static_cast<const float*>(is_v ? a.v : a.k) + at);
   }
   const int64_t cell =
       ((int64_t)a.table[(int64_t)i * a.max_blocks + u / kPage] * a.h_kv + g) * kPage + u % kPage;
-  if (a.pool_elem != 1) return get4(is_v ? a.pool_v : a.pool_k, cell * D + e, a.pool_elem);
+  if (a.pool_elem == 4)
+    return *reinterpret_cast<const float4*>(static_cast<const float*>(is_v ? a.pool_v : a.pool_k) + cell * D + e);
   const uint32_t c = *reinterpret_cast<const uint32_t*>(static_cast<const unsigned char*>(is_v ? a.pool_v : a.pool_k) +
                                                         cell * D + e);
   const float s = (is_v ? a.scale_v : a.scale_k)[cell];
@@ -66,27 +59,23 @@ __global__ void __launch_bounds__(kThreads, 2) span_simt_kernel(SpanArgs a) {
   pdl_trigger();
   const SpanHeader* h = reinterpret_cast<const SpanHeader*>(a.ws);
   if (h->status != ST_OK) return;
-  span_zero_gaps(a);
-  const SpanItem* items = reinterpret_cast<const SpanItem*>(a.ws + a.layout.items);
-  const SpanCut* cuts = reinterpret_cast<const SpanCut*>(a.ws + a.layout.cuts);
-  const SpanCut from = cuts[blockIdx.x], to = cuts[blockIdx.x + 1];
+  span_zero_gaps(a, kThreads);
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const float sl2 = a.scale * 1.4426950408889634f;
 
-  int head = from.head, tile = from.tile;
-  for (int it = from.item; it < to.item || (it == to.item && (head < to.head || (head == to.head && tile < to.tile)));) {
-    const SpanItem w = items[it];
-    const int begin = a.intervals[w.question].begin, prefix = a.prefix ? a.prefix[w.question] : 0;
-    const int p0 = prefix + w.token0, p1 = p0 + w.tokens - 1;
+  for (SpanWalk walk(a, blockIdx.x); walk.live(); walk.next()) {
+    const SpanItem& w = walk.item;
+    const int head = walk.head, p0 = w.p0, p1 = p0 + w.tokens - 1;
     const SpanTiles tiles(p0, p1, a.window, a.sinks);
-    const int last = it == to.item && head == to.head ? to.tile : w.tiles;
     const int rows = w.tokens * a.group;
     __syncthreads();  // the shared tiles are free
     for (int x = t; x < kRows * (D / 4); x += kThreads) {
       const int r = x / (D / 4), e = x % (D / 4) * 4;
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < rows)
-        y = get4(a.q, ((int64_t)(begin + w.token0 + r / a.group) * a.h_q + head * a.group + r % a.group) * D + e, a.elem);
+        y = *reinterpret_cast<const float4*>(
+            static_cast<const float*>(a.q) +
+            ((int64_t)(w.row0 + r / a.group) * a.h_q + head * a.group + r % a.group) * D + e);
       *reinterpret_cast<float4*>(&sm.q[r][e]) = y;
     }
     int pos[kWarpRows];
@@ -99,7 +88,7 @@ __global__ void __launch_bounds__(kThreads, 2) span_simt_kernel(SpanArgs a) {
 #pragma unroll
       for (int e = 0; e < kDims; ++e) o[r][e] = 0.f;
     }
-    for (int j = tile; j < last; ++j)
+    for (int j = walk.j0; j < walk.j1; ++j)
       for (int s0 = 0; s0 < kSpanKeys; s0 += kSub) {
         const int u0 = tiles.at(j) * kSpanKeys + s0;
         if (u0 > p1) break;
@@ -108,7 +97,7 @@ __global__ void __launch_bounds__(kThreads, 2) span_simt_kernel(SpanArgs a) {
           const bool is_v = x >= kSub * (D / 4);
           const int y = is_v ? x - kSub * (D / 4) : x;
           const int r = y / (D / 4), e = y % (D / 4) * 4;
-          const float4 f = u0 + r <= p1 ? load4<D>(a, is_v, w.question, begin, head, u0 + r, e)
+          const float4 f = u0 + r <= p1 ? load4<D>(a, is_v, w.question, w.row0 - p0, head, u0 + r, e)
                                         : make_float4(0.f, 0.f, 0.f, 0.f);
           *reinterpret_cast<float4*>(is_v ? &sm.v[r][e] : &sm.k[r][e]) = f;
         }
@@ -170,31 +159,19 @@ __global__ void __launch_bounds__(kThreads, 2) span_simt_kernel(SpanArgs a) {
       for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
       const int row = warp * kWarpRows + r;
       if (row >= rows) continue;
-      if (tile == 0 && last == w.tiles) {
+      if (walk.whole()) {
         const float inv = 1.f / sum;
         const int64_t at =
-            ((int64_t)(begin + w.token0 + row / a.group) * a.h_q + head * a.group + row % a.group) * D + lane * kV;
+            ((int64_t)(w.row0 + row / a.group) * a.h_q + head * a.group + row % a.group) * D + lane * kV;
 #pragma unroll
-        for (int e = 0; e < kDims; ++e) {
-          if (a.elem == 4) static_cast<float*>(a.out)[at + e] = o[r][e] * inv;
-          else static_cast<__nv_bfloat16*>(a.out)[at + e] = __float2bfloat16_rn(o[r][e] * inv);
-        }
-      } else {  // a piece of a unit: slot 0 for one that began in an earlier part, slot 1 otherwise
-        const int64_t slot = (2 * (int64_t)blockIdx.x + (tile == 0)) * a.layout.rows + row;
+        for (int e = 0; e < kDims; ++e) static_cast<float*>(a.out)[at + e] = o[r][e] * inv;
+      } else {
+        const int64_t slot = walk.slot(blockIdx.x) * a.layout.rows + row;
         float* dst = reinterpret_cast<float*>(a.ws + a.layout.part_o) + slot * D + lane * kV;
         if (lane == 0) reinterpret_cast<float2*>(a.ws + a.layout.part_ml)[slot] = make_float2(m[r], sum);
 #pragma unroll
         for (int e = 0; e < kDims; ++e) dst[e] = o[r][e];
       }
-    }
-    tile = 0;
-    if (last == w.tiles) {
-      if (++head == a.h_kv) {
-        head = 0;
-        ++it;
-      }
-    } else {
-      break;
     }
   }
 }
@@ -238,7 +215,7 @@ __global__ void __launch_bounds__(256) span_merge_kernel(SpanArgs a) {
     }
     const float inv = 1.f / l;
     T* dst = static_cast<T*>(a.out) +
-             ((int64_t)(a.intervals[w.question].begin + w.token0 + token) * a.h_q + cut.head * a.group + rr % a.group) * D +
+             ((int64_t)(w.row0 + token) * a.h_q + cut.head * a.group + rr % a.group) * D +
              lane * kDims;
 #pragma unroll
     for (int e = 0; e < kDims; ++e) dst[e] = from_f32<T>(o[e] * inv);
