@@ -13,6 +13,8 @@
 // lengths; the units that a cut goes through are joined from partial results.
 #pragma once
 
+#include <cuda.h>
+
 #include "kev_internal.cuh"
 
 namespace kev {
@@ -50,7 +52,8 @@ struct SpanLayout {
   size_t items;    // SpanItem[max_items]
   size_t cum;      // int64[max_items + 1] key tiles (over all kv heads) before each item
   size_t cuts;     // SpanCut[kSpanMaxCtas + 1]
-  size_t arrived;  // int32[kSpanMaxCtas] finished parts of the unit that part c begins
+  size_t arrived;  // int32[kSpanMaxCtas][2] finished pieces of the unit that begins in part c and goes on
+                   // (one count per row tile)
   size_t part_ml;  // float2[2 * kSpanMaxCtas][rows] running maximum (log2 units) and sum
   size_t part_o;   // float[2 * kSpanMaxCtas][rows][d]
   size_t total;
@@ -76,7 +79,7 @@ inline SpanLayout span_layout(int32_t n, int32_t T, int32_t group, int32_t d) {
   L.items = take(sizeof(SpanItem) * (size_t)L.max_items);
   L.cum = take(sizeof(int64_t) * ((size_t)L.max_items + 1));
   L.cuts = take(sizeof(SpanCut) * (kSpanMaxCtas + 1));
-  L.arrived = take(sizeof(int32_t) * kSpanMaxCtas);
+  L.arrived = take(sizeof(int32_t) * 2 * kSpanMaxCtas);
   L.part_ml = take(sizeof(float2) * 2 * kSpanMaxCtas * (size_t)L.rows);
   L.part_o = take(sizeof(float) * 2 * kSpanMaxCtas * (size_t)L.rows * d);
   L.total = off;
@@ -114,11 +117,15 @@ struct SpanArgs {
   int32_t* dev_status;
 };
 
+// tensor maps (kev_span_tc.cu): `rank` dimensions, innermost first and contiguous, of `elem`-byte elements
+bool span_tensor_map(CUtensorMap* m, const void* base, int elem, int rank, const cuuint64_t* dims, const cuuint32_t* box,
+                     CUtensorMapSwizzle swizzle);
 cudaError_t launch_span_plan(const SpanArgs& a, cudaStream_t s);
 cudaError_t launch_span_write(const SpanArgs& a, int num_sms, cudaStream_t s);
 cudaError_t launch_span_read(const SpanArgs& a, void* k_out, void* v_out, int num_sms, cudaStream_t s);
 cudaError_t launch_span_simt(const SpanArgs& a, cudaStream_t s);  // fp32
 cudaError_t launch_span_tc(const SpanArgs& a, cudaStream_t s);    // bf16
+cudaError_t launch_span_rows(const SpanArgs& a, bool write, cudaStream_t s);  // bf16, at most 16 rows a question
 cudaError_t launch_span_merge(const SpanArgs& a, int num_sms, cudaStream_t s);
 
 // Key tiles of tokens at positions p0 .. p1: tile j holds positions 128 * at(j) ...
@@ -138,12 +145,12 @@ struct SpanTiles {
 struct SpanWalk {
   const SpanItem* items;
   SpanItem item, ahead;
-  SpanCut to;
+  SpanCut from, to;
   int it, head, h_kv, j0, j1;
   __device__ __forceinline__ SpanWalk(const SpanArgs& a, int part) {
     items = reinterpret_cast<const SpanItem*>(a.ws + a.layout.items);
     const SpanCut* cuts = reinterpret_cast<const SpanCut*>(a.ws + a.layout.cuts);
-    const SpanCut from = cuts[part];
+    from = cuts[part];
     to = cuts[part + 1];
     it = from.item;
     head = from.head;
@@ -162,6 +169,9 @@ struct SpanWalk {
   __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == item.tiles; }
   // slot of this unit's partial result: the unit began in an earlier part, or ends in a later one
   __device__ __forceinline__ int64_t slot(int part) const { return 2 * (int64_t)part + (j0 == 0); }
+  // the unit's pieces: the part it begins in, and how many
+  __device__ __forceinline__ int first() const { return j0 ? from.first : to.first; }
+  __device__ __forceinline__ int parts() const { return j0 ? from.parts : to.parts; }
   __device__ __forceinline__ void next() {
     j0 = 0;
     if (++head == h_kv) {

@@ -86,6 +86,15 @@ void span_tiling(SpanArgs* a, int rows, int tiles, int ctas) {
 kev_status span_attend(SpanArgs* a, bool write, cudaStream_t s) {
   const int sms = sms_of_current_device();
   if (sms <= 0) return KEV_ERR_CUDA;
+  // Few rows per question, and the caller said so: every cached row meets at most 16 rows, which the
+  // register kernel takes at memory speed; it writes the new rows itself and joins its own pieces.
+  const int64_t rows = (int64_t)a->max_chunk * a->group;
+  if (a->elem == 2 && a->pool_elem && rows <= 16) {
+    span_tiling(a, rows <= 8 ? 8 : 16, 1, sms < kSpanMaxCtas ? sms : kSpanMaxCtas);
+    cudaError_t e = launch_span_plan(*a, s);
+    if (e == cudaSuccess) e = launch_span_rows(*a, write, s);
+    return from_cuda(e);
+  }
   const bool tc = a->elem == 2;
   const int ctas = tc ? sms : 2 * sms;
   span_tiling(a, tc ? 128 : 64, tc ? 2 : 1, ctas < kSpanMaxCtas ? ctas : kSpanMaxCtas);

@@ -16,192 +16,215 @@ namespace kev {
 namespace {
 
 constexpr int kThreads = 1024;
-constexpr int kPer = kMaxQuestions / kThreads;  // questions per thread in the scans
+constexpr int kCumSmem = 4096;  // items whose tile counts are searched in shared memory
 
-template <typename T, typename Op>
-__device__ T block_scan(T v, Op op, T zero, T* tmp, T* total) {  // exclusive, in thread order
+// What the checks and the work line scan over the questions: end of the intervals so far, new
+// tokens, items, gaps.
+struct Scan {
+  int end, tokens, items, gaps;
+};
+__device__ __forceinline__ Scan join(const Scan& a, const Scan& b) {
+  return {max(a.end, b.end), a.tokens + b.tokens, a.items + b.items, a.gaps + b.gaps};
+}
+__device__ __forceinline__ Scan up(const Scan& x, int o) {
+  return {__shfl_up_sync(0xffffffffu, x.end, o), __shfl_up_sync(0xffffffffu, x.tokens, o),
+          __shfl_up_sync(0xffffffffu, x.items, o), __shfl_up_sync(0xffffffffu, x.gaps, o)};
+}
+__device__ __forceinline__ long long join(long long a, long long b) { return a + b; }
+__device__ __forceinline__ long long up(long long x, int o) { return __shfl_up_sync(0xffffffffu, x, o); }
+
+// Exclusive scan in thread order; two barriers.
+template <typename T>
+__device__ T block_scan(T v, T zero, T* tmp /* [33] */, T* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   T x = v;
-#pragma unroll
+#pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
-    const T y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x = op(x, y);
+    const T y = up(x, o);
+    if (lane >= o) x = join(y, x);
   }
-  T before = __shfl_up_sync(0xffffffffu, x, 1);
+  T before = up(x, 1);
   if (lane == 0) before = zero;
   if (lane == 31) tmp[warp] = x;
   __syncthreads();
   if (warp == 0) {
     T w = tmp[lane];
-#pragma unroll
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
-      const T y = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w = op(w, y);
+      const T y = up(w, o);
+      if (lane >= o) w = join(y, w);
     }
-    tmp[lane] = w;
+    T ex = up(w, 1);
+    tmp[lane] = lane == 0 ? zero : ex;
+    if (lane == 31) tmp[32] = w;
   }
   __syncthreads();
-  if (warp > 0) before = op(tmp[warp - 1], before);
-  *total = tmp[kThreads / 32 - 1];
-  __syncthreads();
-  return before;
-}
-
-struct AddI { __device__ int operator()(int a, int b) const { return a + b; } };
-struct AddL { __device__ long long operator()(long long a, long long b) const { return a + b; } };
-struct MaxI { __device__ int operator()(int a, int b) const { return a > b ? a : b; } };
-
-// Ends before each interval (prefix maximum over `get`, in its order); returns whether every
-// interval begins at or after it, and writes the gaps between them.
-template <typename Get>
-__device__ bool in_order(int n, int T, Get get, int* tmp, int2* gaps, int* n_gaps, int* flag) {
-  const int t = threadIdx.x;
-  int mine = 0;
-  for (int e = 0; e < kPer; ++e) {
-    const int i = t * kPer + e;
-    if (i < n) {
-      const kev_interval v = get(i);
-      if (v.end > v.begin) mine = max(mine, v.end);
-    }
-  }
-  int last;
-  int before = block_scan(mine, MaxI(), 0, tmp, &last);
-  bool ok = true;
-  int b = before, count = 0;
-  for (int e = 0; e < kPer; ++e) {
-    const int i = t * kPer + e;
-    if (i < n) {
-      const kev_interval v = get(i);
-      if (v.end > v.begin) {
-        ok = ok && v.begin >= b;
-        count += v.begin > b;
-        b = max(b, v.end);
-      }
-    }
-  }
-  if (t == 0) *flag = 0;
-  __syncthreads();
-  if (!ok) *flag = 1;
-  __syncthreads();
-  if (*flag) {
-    __syncthreads();  // everyone has read the flag
-    return false;
-  }
-  int total;
-  int at = block_scan(count, AddI(), 0, tmp, &total);
-  b = before;
-  for (int e = 0; e < kPer; ++e) {
-    const int i = t * kPer + e;
-    if (i < n) {
-      const kev_interval v = get(i);
-      if (v.end > v.begin) {
-        if (v.begin > b) gaps[at++] = make_int2(b, v.begin);
-        b = max(b, v.end);
-      }
-    }
-  }
-  if (t == 0) {
-    if (last < T) gaps[total] = make_int2(last, T);
-    *n_gaps = total + (last < T);
-  }
-  return true;
+  *total = tmp[32];
+  return join(tmp[warp], before);
 }
 
 __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(SpanArgs a) {
-  extern __shared__ unsigned long long dyn[];  // sort keys, then the bit map of used blocks
-  __shared__ int s_base[kMaxQuestions + 1];    // first item of each question
-  __shared__ long long s_tmp[32];
-  __shared__ int s_itmp[32];
-  __shared__ int s_flag, s_err, s_gaps;
+  extern __shared__ unsigned long long dyn[];  // intervals, prefixes; sort keys, bit map of used blocks or tile counts
+  __shared__ Scan s_scan[33];
+  __shared__ long long s_sum[33];
+  __shared__ int s_err;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, n = a.n;
+  kev_interval* iv = reinterpret_cast<kev_interval*>(dyn);
+  int* pre = reinterpret_cast<int*>(iv + n);
+  int* base = pre + n;  // first item of each question
+  unsigned long long* area = dyn + (16 * (size_t)n + 8 + 7) / 8;
+  unsigned* used = reinterpret_cast<unsigned*>(area);
+  const int words = a.pool_elem ? (a.n_blocks + 31) / 32 : 0;
+  if (t == 0) s_err = 0;
+  for (int i = t; i < words; i += kThreads) used[i] = 0u;
   pdl_wait();
   pdl_trigger();
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  __syncthreads();
   SpanHeader* hdr = reinterpret_cast<SpanHeader*>(a.ws);
   int32_t* cu = reinterpret_cast<int32_t*>(a.ws + a.layout.cu);
   int2* gaps = reinterpret_cast<int2*>(a.ws + a.layout.gaps);
-  if (t == 0) s_err = 0;
-  __syncthreads();
   // error ranks: intervals, prefix, overflow, slot -- the first that applies is reported
   auto error = [&](int rank) { atomicMax(&s_err, 8 - rank); };
-  auto prefix_of = [&](int i) { return a.prefix ? a.prefix[i] : 0; };
+  const int item_tokens = a.tile_tokens * a.item_tiles;
 
-  for (int i = t; i < a.n; i += kThreads) {
+  // A thread's questions: `per` consecutive ones.
+  const int per = (n + kThreads - 1) / kThreads;
+  Scan mine = {0, 0, 0, 0};
+#pragma unroll 1
+  for (int e = 0; e < per; ++e) {
+    const int i = t * per + e;
+    if (i >= n) break;
     const kev_interval v = a.intervals[i];
+    const int p = a.prefix ? a.prefix[i] : 0;
+    iv[i] = v;
+    pre[i] = p;
     if (v.begin < 0 || v.end < v.begin || v.end > a.T || v.end - v.begin > a.max_chunk) {
       error(0);
-    } else if (v.end > v.begin && a.prefix) {
-      const int p = a.prefix[i];
+    } else if (v.end > v.begin) {
+      const int L = v.end - v.begin;
       if (p < 0) error(1);
-      else if (a.pool_elem && (int64_t)p + (v.end - v.begin) > (int64_t)a.max_blocks * kPage) error(2);
+      else if (a.pool_elem && (int64_t)p + L > (int64_t)a.max_blocks * kPage) error(2);
+      mine.end = max(mine.end, v.end);
+      mine.tokens += L;
+      if (a.attend) mine.items += (L + item_tokens - 1) / item_tokens;
     }
   }
-  __syncthreads();
-  const bool bad = s_err != 0;
-  __syncthreads();
-  if (!bad) {
-    const kev_interval* iv = a.intervals;
-    bool ok = in_order(a.n, a.T, [&](int i) { return iv[i]; }, s_itmp, gaps, &s_gaps, &s_flag);
-    if (!ok) {  // sort by begin, then once more
-      int n2 = 1;
-      while (n2 < a.n) n2 <<= 1;
-      for (int i = t; i < n2; i += kThreads) {
-        kev_interval v = {0x7fffffff, 0x7fffffff};
-        if (i < a.n && iv[i].end > iv[i].begin) v = iv[i];
-        dyn[i] = (unsigned long long)(unsigned)v.begin << 32 | (unsigned)v.end;
-      }
-      __syncthreads();
-      for (int k = 2; k <= n2; k <<= 1)
-        for (int j = k >> 1; j > 0; j >>= 1) {
-          for (int i = t; i < n2; i += kThreads) {
-            const int p = i ^ j;
-            if (p > i) {
-              const unsigned long long x = dyn[i], y = dyn[p];
-              if ((x > y) == ((i & k) == 0)) {
-                dyn[i] = y;
-                dyn[p] = x;
-              }
-            }
-          }
-          __syncthreads();
-        }
-      ok = in_order(a.n, a.T,
-                    [&](int i) {
-                      return kev_interval{(int)(dyn[i] >> 32), (int)(dyn[i] & 0xffffffffu)};
-                    },
-                    s_itmp, gaps, &s_gaps, &s_flag);
-      if (!ok && t == 0) error(0);
-    }
-  }
+  Scan all;
+  const Scan before = block_scan(mine, Scan{0, 0, 0, 0}, s_scan, &all);
+
+  const bool clean = s_err == 0;  // the checks of single questions passed
   __syncthreads();
 
-  if (s_err == 0 && a.pool_elem) {
-    // pages: one warp per question, a lane per page; a block's bit may be set once
-    unsigned* used = reinterpret_cast<unsigned*>(dyn);
-    const int words = (a.n_blocks + 31) / 32;
-    for (int i = t; i < words; i += kThreads) used[i] = 0u;
-    __syncthreads();
-    for (int i = warp; i < a.n; i += kThreads / 32) {
-      const kev_interval v = a.intervals[i];
-      const int L = v.end - v.begin;
-      if (L <= 0) continue;
-      const int p0 = prefix_of(i), p1 = p0 + L - 1;
-      int ns = 0, lo = p0 / kPage;
-      if (a.attend) {
-        const SpanTiles s(p0, p1, a.window, a.sinks);
-        ns = s.ns;
-        lo = s.lo;
+  // Disjoint, if every interval begins at or after the end of all before it; otherwise sorted by
+  // beginning and looked at again.
+  bool ok = true;
+  if (clean) {
+    int end = before.end, tokens = before.tokens, items = before.items;
+#pragma unroll 1
+    for (int e = 0; e < per; ++e) {
+      const int i = t * per + e;
+      if (i >= n) break;
+      const int L = iv[i].end - iv[i].begin;
+      cu[i] = tokens;
+      base[i] = items;
+      if (L > 0) {
+        ok = ok && iv[i].begin >= end;
+        mine.gaps += iv[i].begin > end;
+        end = max(end, iv[i].end);
+        tokens += L;
+        if (a.attend) items += (L + item_tokens - 1) / item_tokens;
       }
-      const int pages = ns + p1 / kPage - lo + 1;
-      for (int e = lane; e < pages; e += 32) {
-        const int b = a.table[(int64_t)i * a.max_blocks + (e < ns ? e : lo + e - ns)];
-        if (b < 0 || b >= a.n_blocks) {
-          error(3);
-        } else {
+    }
+    if (t == 0) {
+      cu[n] = all.tokens;
+      base[n] = all.items;
+    }
+    if (words) {  // pages: one warp per question, a lane per page; a block's bit may be set once
+#pragma unroll 1
+      for (int i = warp; i < n; i += kThreads / 32) {
+        const int L = iv[i].end - iv[i].begin;
+        if (L <= 0) continue;
+        const int p0 = pre[i], p1 = p0 + L - 1;
+        int ns = 0, lo = p0 / kPage;
+        if (a.attend) {
+          const SpanTiles s(p0, p1, a.window, a.sinks);
+          ns = s.ns;
+          lo = s.lo;
+        }
+        const int pages = ns + p1 / kPage - lo + 1;
+        const int32_t* row = a.table + (int64_t)i * a.max_blocks;
+#pragma unroll 4
+        for (int e = lane; e < pages; e += 32) {
+          const int b = row[e < ns ? e : lo + e - ns];
           const unsigned bit = 1u << (b & 31);
-          if (atomicOr(&used[b >> 5], bit) & bit) error(3);
+          if (b < 0 || b >= a.n_blocks || atomicOr(&used[b >> 5], bit) & bit) error(3);
         }
       }
     }
+  }
+  bool sorted = __syncthreads_and(ok);
+  auto interval = [&](int i) { return iv[i]; };
+  auto ordered = [&](int i) { return kev_interval{(int)(area[i] >> 32), (int)(area[i] & 0xffffffffu)}; };
+  if (clean && !sorted) {
+    int n2 = 1;
+    while (n2 < n) n2 <<= 1;
+    for (int i = t; i < n2; i += kThreads)  // empty intervals last
+      area[i] = i < n && iv[i].end > iv[i].begin ? (unsigned long long)iv[i].begin << 32 | (unsigned)iv[i].end
+                                                 : 0x7fffffff7fffffffull;
+    __syncthreads();
+#pragma unroll 1
+    for (int k = 2; k <= n2; k <<= 1)
+#pragma unroll 1
+      for (int j = k >> 1; j > 0; j >>= 1) {
+        for (int i = t; i < n2; i += kThreads) {
+          const int p = i ^ j;
+          if (p > i) {
+            const unsigned long long x = area[i], y = area[p];
+            if ((x > y) == ((i & k) == 0)) {
+              area[i] = y;
+              area[p] = x;
+            }
+          }
+        }
+        __syncthreads();
+      }
+  }
+  // gaps between the intervals in order
+  auto find_gaps = [&](auto get, bool check) {
+    Scan v = {0, 0, 0, 0}, total;
+    for (int e = 0; e < per; ++e) {
+      const int i = t * per + e;
+      if (i < n && get(i).end > get(i).begin) v.end = max(v.end, get(i).end);
+    }
+    const int first = block_scan(v, Scan{0, 0, 0, 0}, s_scan, &total).end;
+    int end = first;
+    for (int e = 0; e < per; ++e) {
+      const int i = t * per + e;
+      if (i < n && get(i).end > get(i).begin) {
+        if (check && get(i).begin < end) error(0);
+        v.gaps += get(i).begin > end;
+        end = max(end, get(i).end);
+      }
+    }
+    __syncthreads();  // the scan's scratch is free
+    int at = block_scan(v, Scan{0, 0, 0, 0}, s_scan, &total).gaps;
+    end = first;
+    for (int e = 0; e < per; ++e) {
+      const int i = t * per + e;
+      if (i < n && get(i).end > get(i).begin) {
+        if (get(i).begin > end) gaps[at++] = make_int2(end, get(i).begin);
+        end = max(end, get(i).end);
+      }
+    }
+    if (t == 0) {
+      if (total.end < a.T) gaps[total.gaps] = make_int2(total.end, a.T);
+      hdr->n_gaps = total.gaps + (total.end < a.T);
+    }
+  };
+  if (clean) {
+    if (!sorted) find_gaps(ordered, true);
+    else if (a.attend && all.tokens < a.T) find_gaps(interval, false);
+    else if (t == 0) hdr->n_gaps = 0;
     __syncthreads();
   }
   if (s_err) {
@@ -213,75 +236,47 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(SpanArgs a) {
     }
     return;
   }
-
-  // prefix sums of the lengths, and of the items
-  int len = 0, items = 0;
-  const int item_tokens = a.tile_tokens * a.item_tiles;
-  for (int e = 0; e < kPer; ++e) {
-    const int i = t * kPer + e;
-    if (i < a.n) {
-      const int L = a.intervals[i].end - a.intervals[i].begin;
-      len += L;
-      if (a.attend) items += (L + item_tokens - 1) / item_tokens;
-    }
-  }
-  int n_new, n_items;
-  int at = block_scan(len, AddI(), 0, s_itmp, &n_new);
-  int ib = block_scan(items, AddI(), 0, s_itmp, &n_items);
-  for (int e = 0; e < kPer; ++e) {
-    const int i = t * kPer + e;
-    if (i < a.n) {
-      const int L = a.intervals[i].end - a.intervals[i].begin;
-      cu[i] = at;
-      s_base[i] = ib;
-      at += L;
-      if (a.attend) ib += (L + item_tokens - 1) / item_tokens;
-    }
-  }
   if (t == 0) {
-    cu[a.n] = n_new;
-    s_base[a.n] = n_items;
-    hdr->n_items = n_items;
-    hdr->n_gaps = s_gaps;
-    hdr->n_new = n_new;
+    hdr->n_items = all.items;
+    hdr->n_new = all.tokens;
     hdr->status = ST_OK;
     if (a.dev_status) *a.dev_status = ST_OK;
   }
-  __syncthreads();
   if (!a.attend) return;
 
   // items and the key tiles before each
   SpanItem* out = reinterpret_cast<SpanItem*>(a.ws + a.layout.items);
-  long long* cum = reinterpret_cast<long long*>(a.ws + a.layout.cum);
+  const int n_items = all.items;
+  long long* cum = n_items <= kCumSmem ? reinterpret_cast<long long*>(area)
+                                       : reinterpret_cast<long long*>(a.ws + a.layout.cum);
   long long run = 0;
-  for (int base = 0; base < n_items; base += kThreads) {
-    const int x = base + t;
+#pragma unroll 1
+  for (int first = 0; first < n_items; first += kThreads) {
+    const int x = first + t;
     long long tiles = 0;
     if (x < n_items) {
-      int lo = 0, hi = a.n - 1;  // the last question whose first item is at or before x
+      int lo = 0, hi = n - 1;  // the last question whose first item is at or before x
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (s_base[mid] <= x) lo = mid;
+        if (base[mid] <= x) lo = mid;
         else hi = mid - 1;
       }
       SpanItem w;
-      const kev_interval v = a.intervals[lo];
-      const int token0 = (x - s_base[lo]) * item_tokens;
+      const int token0 = (x - base[lo]) * item_tokens;
       w.question = lo;
-      w.row0 = v.begin + token0;
-      w.tokens = min(item_tokens, v.end - w.row0);
-      w.p0 = prefix_of(lo) + token0;
+      w.row0 = iv[lo].begin + token0;
+      w.tokens = min(item_tokens, iv[lo].end - w.row0);
+      w.p0 = pre[lo] + token0;
       w.tiles = SpanTiles(w.p0, w.p0 + w.tokens - 1, a.window, a.sinks).n;
       out[x] = w;
       tiles = (long long)w.tiles * a.h_kv;
     }
     long long sum;
-    const long long before = block_scan(tiles, AddL(), 0ll, s_tmp, &sum);
-    if (x < n_items) cum[x] = run + before;
+    const long long at = block_scan(tiles, 0ll, s_sum, &sum);
+    if (x < n_items) cum[x] = run + at;
     run += sum;
+    __syncthreads();
   }
-  if (t == 0) cum[n_items] = run;
-  __syncthreads();
 
   // cuts: part c begins at tile floor(c * total / parts) of the line; with at most one part per
   // tile, no part is empty
@@ -290,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(SpanArgs a) {
   const long long total = run;
   const int parts = total < a.ctas ? (int)total : a.ctas;
   for (int c = t; c <= a.ctas; c += kThreads) {
-    if (c < a.ctas) arrived[c] = 0;
+    if (c < a.ctas) arrived[2 * c] = arrived[2 * c + 1] = 0;
     const long long g = parts ? total / parts : 0, r = parts ? total % parts : 0;
     auto place = [&](int x) { return (long long)x * g + (long long)x * r / parts; };
     const long long w = c < parts ? place(c) : total;
@@ -302,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(SpanArgs a) {
         if (cum[mid] <= w) lo = mid;
         else hi = mid - 1;
       }
-      const int tiles = out[lo].tiles;
+      const int tiles = (int)(((lo + 1 < n_items ? cum[lo + 1] : total) - cum[lo]) / a.h_kv);
       const long long in = w - cum[lo];
       cut.item = lo;
       cut.head = (int)(in / tiles);
@@ -323,13 +318,20 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(SpanArgs a) {
 }  // namespace
 
 cudaError_t launch_span_plan(const SpanArgs& a, cudaStream_t s) {
-  size_t sort = 8;
-  while (sort < sizeof(unsigned long long) * (size_t)a.n) sort <<= 1;
+  // intervals, prefixes and first items of the questions, and beside them the largest of: the sort
+  // keys, the bit map of the blocks, the tile counts of the items
+  size_t area = 8;
+  while (area < 8 * (size_t)a.n) area <<= 1;
   const size_t map = a.pool_elem ? ((size_t)a.n_blocks + 63) / 64 * 8 : 0;
-  const size_t smem = sort > map ? sort : map;
-  if (smem > 24 * 1024) {  // always the same limit: calls from several threads do not lower each other's
-    const cudaError_t e =
-        cudaFuncSetAttribute(span_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSpanMaxBlocks / 8);
+  const int64_t items = a.attend ? (int64_t)a.T / (a.tile_tokens * a.item_tiles) + a.n : 0;
+  const size_t cum = items < kCumSmem ? 8 * (size_t)items : 8 * kCumSmem;
+  area = area > map ? area : map;
+  area = area > cum ? area : cum;
+  const size_t smem = 16 * (size_t)a.n + 16 + area;
+  constexpr int kMost = 16 * kMaxQuestions + 16 + kSpanMaxBlocks / 8;
+  static_assert(kMost <= 220 * 1024, "shared memory of the plan");
+  if (smem > 40 * 1024) {  // always the same limit: calls from several threads do not lower each other's
+    const cudaError_t e = cudaFuncSetAttribute(span_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
     if (e != cudaSuccess) return e;
   }
   return launch_pdl(span_plan_kernel, dim3(1), dim3(kThreads), smem, s, a);

@@ -1,0 +1,670 @@
+// Span attention for a few rows per question -- above all decode steps: bf16 q and out, paged cache
+// bf16 or e4m3, at most 16 (token, q-head of the group) rows per question and kv head.
+//
+// Every cached row is read once and meets only those rows, so the bound is HBM (the cache, once)
+// and below it the instructions per element that unpack it.  Here the matrix instruction takes the
+// cache as its A operand straight from registers (mma.sync m16n8k16): S^T[16 keys x 8 rows] = K q^T,
+// O^T[dims x 8 rows] += V^T P^T.  With 8 rows nothing is padded, where tcgen05 would spend a 128-row
+// tile (or an extra trip of the unpacked codes through shared memory, which at HBM speed is more than
+// shared memory carries); the matrix pipe stays below half its time.
+//
+// One persistent CTA per SM walks its equal part of the work line (kev_span.cuh):
+//   warp 8      loads pages into a ring: TMA boxes of 16 positions, only those that some row sees
+//   warp 9      first writes the new K/V rows that lie in this CTA's tiles (quantised for e4m3): every
+//               (unit, tile) has one owner, so a row is written once and read by the CTA that wrote it
+//   warps 0-7   a warp takes 16 of a page's 128 positions, with a running reference maximum, sum and
+//               accumulator of its own; they are joined through shared memory when the unit ends
+// A unit that a cut goes through is joined by the CTA that finishes its last piece, in the order of
+// the pieces, so the result does not depend on which CTA that is.
+//
+// Registers instead of ldmatrix: the contraction index of an MMA may be permuted freely, so a lane
+// takes whole 16-byte chunks of a row (8 bf16 or 16 codes) as its share of several k-steps.  For K,
+// lane (g, c) of group g = lane / 4 holds chunks c, c + 4, ... of the row of key slot g; for V, chunk g
+// of the rows of slots 2c, 2c + 1, 2c + 8, 2c + 9, byte-permuted into (key, key) pairs.  Slot s is
+// position perm(s) of its 8, chosen so that with the 128-byte swizzle a quarter warp's 16-byte loads
+// of either kind touch all banks once.
+#include "kev_sm100.cuh"
+#include "kev_span.cuh"
+
+namespace kev {
+namespace {
+
+using namespace sm100;
+
+constexpr int kWarps = 8;  // of 16 positions each: one page
+constexpr int kThreads = (kWarps + 2) * 32;
+constexpr int kLoadWarp = kWarps, kWriteWarp = kWarps + 1;
+constexpr float kBig = 1.8446744e19f;  // 2^64: a weight above it moves the reference
+constexpr long long kDrainBudget = 4000000000ll;
+
+template <int D, int E>
+struct Smem {
+  static constexpr int kRow = D * E;                        // bytes of a cached row
+  static constexpr int kPitch = kRow < 128 ? kRow : 128;    // row of a swizzled sub-tile
+  static constexpr int kSubs = kRow / kPitch;
+  static constexpr int kTile = kPage * kRow;                // K or V of a page
+  static constexpr int kScales = E == 1 ? 2 * kPage * 4 : 0;
+  static constexpr int kRaw = 2 * kTile + kScales;
+  static constexpr int kStageBytes = (kRaw + 1023) / 1024 * 1024;
+  static constexpr int kStages = 196608 / kStageBytes < 8 ? 196608 / kStageBytes : 8;
+  static constexpr int kPad = D + 4;                        // floats of a row in the join buffer
+  static constexpr int kJoin = kStages * kStageBytes;       // float [8 warps][8 rows][kPad]
+  static constexpr int kMl = kJoin + kWarps * 8 * kPad * 4;  // float2 [8 warps][8 rows]
+  static constexpr int kBar = kMl + kWarps * 8 * 8;
+  static constexpr int kBytes = kBar + 256 + 1024;
+};
+
+struct Bars {
+  uint64_t full[8], empty[8];
+  int written;  // units whose new rows are in the cache
+  int abort;
+  int never;
+  int last;
+};
+static_assert(sizeof(Bars) <= 256, "barriers");
+
+struct RowsArgs {
+  SpanArgs s;
+  float scale_log2;
+  long long wait_budget;
+  int write;
+};
+
+__device__ __forceinline__ int perm(int s) {  // position of slot s: 0 5 2 7 4 1 6 3
+  return s & 1 ? (s ^ 4) : s;
+}
+
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t at) {
+  uint32_t x;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(at));
+  return x;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 x;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at));
+  return x;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t at) {
+  uint2 x;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(at));
+  return x;
+}
+
+// two e4m3 codes in the high bytes of the halves of x (low bytes: anything) as exact bf16: exponent and
+// mantissa bits at their places, times 2^120 for the difference of the biases
+__device__ __forceinline__ uint32_t widen(uint32_t x) {
+  const uint32_t y = ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(y), "r"(0x7b807b80u));
+  return r;
+}
+
+__device__ __forceinline__ float nan_max(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+// Some row of the item (tokens at p0 .. p1) sees one of positions u .. u + 15.
+__device__ __forceinline__ bool group_seen(const SpanArgs& a, int u, int p0, int p1) {
+  return u <= p1 && (a.window == 0 || p0 - (u + 15) < a.window || u < a.sinks);
+}
+
+template <int D, int E, int NT>
+__global__ void __launch_bounds__(kThreads, 1)
+    span_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                     const __grid_constant__ RowsArgs p) {
+  using L = Smem<D, E>;
+  const SpanArgs& a = p.s;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Bars* bars = reinterpret_cast<Bars*>(smem + L::kBar);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 8; ++s) {
+      mbar_init(&bars->full[s], 1);
+      mbar_init(&bars->empty[s], kWarps);
+    }
+    bars->written = bars->abort = bars->never = bars->last = 0;
+    fence_mbar_init();
+  }
+  if (threadIdx.x == kLoadWarp * 32) {
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  __syncthreads();
+  volatile int* abort_flag = &bars->abort;
+  const volatile int* never = &bars->never;
+  const long long budget = p.wait_budget;
+  pdl_wait();
+  pdl_trigger();
+  if (reinterpret_cast<const SpanHeader*>(a.ws)->status != ST_OK) return;
+  auto timeout = [&]() {
+    atomicCAS(&reinterpret_cast<SpanHeader*>(a.ws)->status, 0, ST_TIMEOUT);
+    set_status(a.dev_status, ST_TIMEOUT);
+    *abort_flag = 1;
+  };
+
+  if (warp == kLoadWarp) {
+    // -------------------------------------------------------------------- page loads
+    constexpr int kBoxes = 2 * L::kSubs * 8;  // 16-position boxes of a page: one per lane
+    const int is_v = lane / (kBoxes / 2), sub = lane / 8 % L::kSubs, grp = lane % 8;
+    uint32_t seq = 0;
+    bool ok = true;
+    int n = 0;
+    for (SpanWalk w(a, blockIdx.x); ok && w.live(); w.next(), ++n) {
+      const int p0 = w.item.p0, p1 = p0 + w.item.tokens - 1;
+      const SpanTiles tiles(p0, p1, a.window, a.sinks);
+      const int32_t* row = a.table + (int64_t)w.item.question * a.max_blocks;
+      int ids = 0;
+      bool wrote = !p.write;
+      for (int j = w.j0; j < w.j1; ++j, ++seq) {
+        if ((j - w.j0) % 32 == 0) ids = j + lane < w.j1 ? row[tiles.at(j + lane)] : 0;  // 32 pages ahead
+        const int block = __shfl_sync(0xffffffffu, ids, (j - w.j0) % 32);
+        const int u0 = tiles.at(j) * kPage;
+        const int s = seq % L::kStages;
+        if (seq >= L::kStages)
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars->empty[s], (seq / L::kStages - 1) & 1, abort_flag, budget));
+        if (ok && !wrote && u0 + kPage > p0) {  // the page holds new rows: wait until they are written
+          const long long t0 = clock64();
+          const volatile int* written = &bars->written;
+          bool there;
+          while (!(there = *written > n) && !*abort_flag && clock64() - t0 < budget) {
+          }
+          ok = __all_sync(0xffffffffu, there);
+          __threadfence_block();
+          asm volatile("fence.proxy.async;" ::: "memory");
+          wrote = true;
+        }
+        if (!ok) break;
+        const bool mine = lane < kBoxes && group_seen(a, u0 + grp * 16, p0, p1);
+        const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
+        const int cell = (block * a.h_kv + w.head) * kPage;
+        unsigned char* dst = smem + s * L::kStageBytes;
+        if (lane == 0) mbar_arrive_expect_tx(&bars->full[s], boxes * 16 * L::kPitch + L::kScales);
+        __syncwarp();
+        if (mine)
+          tma_load_2d(dst + is_v * L::kTile + (sub * kPage + grp * 16) * L::kPitch, is_v ? &tm_v : &tm_k,
+                      sub * L::kPitch / E, cell + grp * 16, &bars->full[s]);
+        if (E == 1 && lane < 2)
+          bulk_load(dst + 2 * L::kTile + lane * kPage * 4, (lane ? a.scale_v : a.scale_k) + cell, kPage * 4, &bars->full[s]);
+      }
+    }
+    if (!ok && lane == 0) timeout();
+    if (*abort_flag)  // every copy issued lands before the CTA leaves
+      for (uint32_t q = seq < L::kStages ? 0 : seq - L::kStages; q < seq; ++q)
+        mbar_wait(&bars->full[q % L::kStages], (q / L::kStages) & 1, never, kDrainBudget);
+  } else if (warp == kWriteWarp) {
+    // -------------------------------------------------------------------- new rows into the cache
+    if (!p.write) return;
+    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;  // lanes of a bf16 row
+    const int sub = lane % kLanes;
+    int n = 0;
+    for (SpanWalk w(a, blockIdx.x); w.live(); w.next()) {
+      const int p0 = w.item.p0;
+      const SpanTiles tiles(p0, p0 + w.item.tokens - 1, a.window, a.sinks);
+      const int32_t* row = a.table + (int64_t)w.item.question * a.max_blocks;
+      for (int x0 = 0; x0 < 2 * w.item.tokens; x0 += kAtOnce) {
+        const int x = x0 + lane / kLanes, token = x >> 1, pos = p0 + token;
+        const bool is_v = x & 1;
+        // its tile's place on the work line: chunk positions lie in the tiles from lo on, or are sinks'
+        const int page = pos / kPage, j = page < tiles.ns ? page : tiles.ns + page - tiles.lo;
+        const bool mine = token < w.item.tokens && j >= w.j0 && j < w.j1;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (mine)
+          v = reinterpret_cast<const uint4*>(is_v ? a.v : a.k)[((int64_t)(w.item.row0 + token) * a.h_kv + w.head) * kLanes + sub];
+        const int64_t cell = mine ? ((int64_t)row[page] * a.h_kv + w.head) * kPage + pos % kPage : 0;
+        if (E == 2) {
+          if (mine) static_cast<uint4*>(is_v ? a.pool_v : a.pool_k)[cell * kLanes + sub] = v;
+        } else {
+          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+          float f[8], top = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            f[e] = __uint_as_float(e & 1 ? u[e / 2] & 0xffff0000u : u[e / 2] << 16);
+            top = nan_max(top, fabsf(f[e]));
+          }
+#pragma unroll
+          for (int o = kLanes / 2; o > 0; o >>= 1) top = nan_max(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const float scale = top < INFINITY ? __fdiv_rn(top, 448.f) : __int_as_float(0x7fffffff);
+          uint32_t c[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = scale == 0.f ? 0.f : __fdiv_rn(f[4 * i + e], scale);
+            c[i] = e4m3x2(y[0], y[1]) | e4m3x2(y[2], y[3]) << 16;
+          }
+          if (mine) {
+            *reinterpret_cast<uint2*>(static_cast<unsigned char*>(is_v ? a.pool_v : a.pool_k) + cell * D + sub * 8) =
+                make_uint2(c[0], c[1]);
+            if (sub == 0) (is_v ? a.scale_v : a.scale_k)[cell] = scale;
+          }
+        }
+      }
+      __threadfence();
+      asm volatile("fence.proxy.async;" ::: "memory");  // before the copies of the page, which the other warp issues
+      __syncwarp();
+      ++n;
+      if (lane == 0) *reinterpret_cast<volatile int*>(&bars->written) = n;
+    }
+  } else {
+    // -------------------------------------------------------------------- attention
+    span_zero_gaps(a, kWarps * 32);
+    constexpr int kChunks = L::kRow / 64;      // 16-byte chunks of a K row per lane
+    constexpr int kSteps = E == 2 ? 2 : 4;     // k-steps of a chunk
+    constexpr int kTiles = D / 16;             // 16-dim tiles of O^T
+    const int g = lane >> 2, c = lane & 3;
+    const uint32_t smem0 = smem_u32(smem);
+    float* join = reinterpret_cast<float*>(smem + L::kJoin);
+    float2* join_ml = reinterpret_cast<float2*>(smem + L::kMl);
+    // swizzled address of 16-byte chunk ch of row r
+    auto at = [&](uint32_t tile, int r, int ch) {
+      if (L::kPitch == 128)
+        return tile + (ch >> 3) * (kPage * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+      return tile + r * 64 + ((ch ^ (r >> 1 & 3)) << 4);
+    };
+    uint32_t seq = 0;
+    bool ok = true;
+    for (SpanWalk w(a, blockIdx.x); w.live(); w.next()) {
+      const int p0 = w.item.p0, p1 = p0 + w.item.tokens - 1, rows = w.item.tokens * a.group;
+      const SpanTiles tiles(p0, p1, a.window, a.sinks);
+      // q as the B operand: row nt * 8 + g, the dims of this lane's chunks
+      uint32_t q[NT][kChunks * kSteps][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int r = nt * 8 + g;
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(
+            static_cast<const __nv_bfloat16*>(a.q) +
+            ((int64_t)(w.item.row0 + (r < rows ? r / a.group : 0)) * a.h_q + w.head * a.group + (r < rows ? r % a.group : 0)) * D);
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+          for (int h = 0; h < kSteps; ++h) {
+            const int dim = (E == 2 ? 8 : 16) * (c + 4 * i) + 4 * h;
+            const uint2 x = r < rows ? *reinterpret_cast<const uint2*>(src + dim / 2) : make_uint2(0u, 0u);
+            q[nt][i * kSteps + h][0] = x.x;
+            q[nt][i * kSteps + h][1] = x.y;
+          }
+      }
+      int pos[NT][2];  // positions of rows nt * 8 + 2c, + 1
+      float m[NT][2], l[NT][2], o[kTiles][NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          pos[nt][x] = min(p0 + (nt * 8 + 2 * c + x) / a.group, p1);  // rows past the last: as its own
+          m[nt][x] = -INFINITY;
+          l[nt][x] = 0.f;
+        }
+#pragma unroll
+      for (int mt = 0; mt < kTiles; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) o[mt][nt][x] = 0.f;
+
+      for (int j = w.j0; j < w.j1; ++j, ++seq) {
+        const int s = seq % L::kStages;
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->full[s], (seq / L::kStages) & 1, abort_flag, budget));
+        const int u0 = tiles.at(j) * kPage + warp * 16;  // this warp's positions
+        if (!ok) continue;
+        if (group_seen(a, u0, p0, p1)) {
+          const uint32_t tk = smem0 + s * L::kStageBytes, tv = tk + L::kTile;
+          const int r0 = warp * 16 + perm(g);  // slots g and g + 8
+          float z[NT][4];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) z[nt][x] = 0.f;
+#pragma unroll
+          for (int i = 0; i < kChunks; ++i) {
+            const uint4 x = lds128(at(tk, r0, c + 4 * i)), y = lds128(at(tk, r0 + 8, c + 4 * i));
+            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int h = 0; h < kSteps; ++h) {
+              uint32_t a0, a1, a2, a3;
+              if (E == 2) {
+                a0 = xs[(2 * h) & 3];
+                a1 = ys[(2 * h) & 3];
+                a2 = xs[(2 * h + 1) & 3];
+                a3 = ys[(2 * h + 1) & 3];
+              } else {
+                a0 = widen(__byte_perm(xs[h & 3], 0u, 0x1404));
+                a1 = widen(__byte_perm(ys[h & 3], 0u, 0x1404));
+                a2 = widen(__byte_perm(xs[h & 3], 0u, 0x3424));
+                a3 = widen(__byte_perm(ys[h & 3], 0u, 0x3424));
+              }
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma(z[nt], a0, a1, a2, a3, q[nt][i * kSteps + h][0], q[nt][i * kSteps + h][1]);
+            }
+          }
+          float kf0 = p.scale_log2, kf1 = kf0, vf0 = 1.f, vf1 = 1.f;
+          if (E == 1) {
+            const uint32_t sc = tk + 2 * L::kTile + r0 * 4;
+            kf0 *= __uint_as_float(lds32(sc));
+            kf1 *= __uint_as_float(lds32(sc + 32));
+            vf0 = __uint_as_float(lds32(sc + kPage * 4));
+            vf1 = __uint_as_float(lds32(sc + kPage * 4 + 32));
+          }
+          // every row sees all 16 positions
+          const bool edge = !(u0 + 15 <= p0 && (a.window == 0 || p1 - u0 < a.window || u0 + 15 < a.sinks));
+          const int key0 = u0 + perm(g), key1 = key0 + 8;
+          bool unset = false;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              z[nt][x] *= kf0;
+              z[nt][2 + x] *= kf1;
+              if (edge) {
+                if (!span_sees(pos[nt][x], key0, a.window, a.sinks)) z[nt][x] = -INFINITY;
+                if (!span_sees(pos[nt][x], key1, a.window, a.sinks)) z[nt][2 + x] = -INFINITY;
+              }
+              unset = unset || m[nt][x] == -INFINITY;
+            }
+          }
+          // the largest of a row's 16 scores: over the lanes that share c
+          auto top_of = [&](int nt, int x) {
+            float t = fmaxf(z[nt][x], z[nt][2 + x]);
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+            return fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+          };
+          if (__any_sync(0xffffffffu, unset)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const float t = top_of(nt, x);
+                if (m[nt][x] == -INFINITY) m[nt][x] = t;
+              }
+          }
+          float pr[NT][4];
+          auto weights = [&]() {
+            bool big = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const float ref = m[nt][x & 1] == -INFINITY ? 0.f : m[nt][x & 1];
+                pr[nt][x] = ex2_approx(z[nt][x] - ref);
+                big = big || !(pr[nt][x] <= kBig);
+              }
+            return __any_sync(0xffffffffu, big);
+          };
+          if (weights()) {  // scores outgrew the reference (or are not numbers): the exact maximum, and all rescaled
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const float t = fmaxf(top_of(nt, x), m[nt][x]);
+                const float alpha = t == -INFINITY ? 1.f : ex2_approx(m[nt][x] - t);
+                m[nt][x] = t;
+                l[nt][x] *= alpha;
+#pragma unroll
+                for (int mt = 0; mt < kTiles; ++mt) {
+                  o[mt][nt][x] *= alpha;
+                  o[mt][nt][2 + x] *= alpha;
+                }
+              }
+            weights();
+          }
+          uint32_t b[NT][2];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) l[nt][x] += pr[nt][x] + pr[nt][2 + x];
+            float w0 = pr[nt][0] * vf0, w1 = pr[nt][1] * vf0, w2 = pr[nt][2] * vf1, w3 = pr[nt][3] * vf1;
+            if (E == 1 && edge) {  // the scale of a masked row may be anything
+              if (z[nt][0] == -INFINITY) w0 = 0.f;
+              if (z[nt][1] == -INFINITY) w1 = 0.f;
+              if (z[nt][2] == -INFINITY) w2 = 0.f;
+              if (z[nt][3] == -INFINITY) w3 = 0.f;
+            }
+            // the weights are rounded to bf16 here, as the product's operand
+            b[nt][0] = transpose8x8(pack_bf16x2(w0, w1));
+            b[nt][1] = transpose8x8(pack_bf16x2(w2, w3));
+          }
+          // V: rows of slots 2c, 2c + 1, 2c + 8, 2c + 9
+          const int v0 = warp * 16 + perm(2 * c), v1 = warp * 16 + perm(2 * c + 1);
+          const int vr[4] = {v0, v1, v0 + 8, v1 + 8};
+          if (E == 2) {
+#pragma unroll
+            for (int i = 0; i < L::kRow / 128; ++i) {
+              uint32_t x[4][4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint4 y = lds128(at(tv, vr[e], g + 8 * i));
+                x[e][0] = y.x;
+                x[e][1] = y.y;
+                x[e][2] = y.z;
+                x[e][3] = y.w;
+              }
+              if (edge) {
+                // What masked positions hold must not meet a weight of zero as a NaN or an infinity: those
+                // become zeros here, and the rows that do see them get them added below.
+                uint32_t any = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                  for (int t = 0; t < 4; ++t) {
+                    const uint32_t bad = ((x[e][t] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+                    any |= bad;
+                    if (bad & 0x8000u) x[e][t] &= 0xffff0000u;
+                    if (bad & 0x80000000u) x[e][t] &= 0x0000ffffu;
+                  }
+                if (__any_sync(0xffffffffu, any != 0)) {
+#pragma unroll 1
+                  for (int k = 0; k < 16; ++k) {
+                    const uint4 y = lds128(at(tv, warp * 16 + k, g + 8 * i));
+                    const uint32_t ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+#pragma unroll
+                      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                          if (!span_sees(pos[nt][r], u0 + k, a.window, a.sinks)) continue;
+                          if ((ys[t] & 0x7f80u) == 0x7f80u) o[4 * i + t][nt][r] += __uint_as_float(ys[t] << 16);
+                          if ((ys[t] & 0x7f800000u) == 0x7f800000u) o[4 * i + t][nt][2 + r] += __uint_as_float(ys[t] & 0xffff0000u);
+                        }
+                  }
+                }
+              }
+#pragma unroll
+              for (int t = 0; t < 4; ++t) {
+                const uint32_t a0 = __byte_perm(x[0][t], x[1][t], 0x5410), a1 = __byte_perm(x[0][t], x[1][t], 0x7632);
+                const uint32_t a2 = __byte_perm(x[2][t], x[3][t], 0x5410), a3 = __byte_perm(x[2][t], x[3][t], 0x7632);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma(o[4 * i + t][nt], a0, a1, a2, a3, b[nt][0], b[nt][1]);
+              }
+            }
+          } else {
+            uint32_t x[4][D / 32];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (D == 128) {
+                const uint4 y = lds128(at(tv, vr[e], g));
+                x[e][0] = y.x;
+                x[e][1] = y.y;
+                x[e][2 % (D / 32)] = y.z;
+                x[e][3 % (D / 32)] = y.w;
+              } else {
+                const uint2 y = lds64(at(tv, vr[e], g >> 1) + (g & 1) * 8);
+                x[e][0] = y.x;
+                x[e][1] = y.y;
+              }
+            }
+#pragma unroll
+            for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {  // dims 4t + 2h, + 1
+                const uint32_t s0 = h ? 0x6622 : 0x4400, s1 = h ? 0x7733 : 0x5511;
+                const uint32_t a0 = widen(__byte_perm(x[0][t], x[1][t], s0)), a1 = widen(__byte_perm(x[0][t], x[1][t], s1));
+                const uint32_t a2 = widen(__byte_perm(x[2][t], x[3][t], s0)), a3 = widen(__byte_perm(x[2][t], x[3][t], s1));
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma(o[2 * t + h][nt], a0, a1, a2, a3, b[nt][0], b[nt][1]);
+              }
+          }
+        }
+        mbar_arrive_warp(&bars->empty[s]);
+      }
+
+      // ------------------------------------------------------------------ the eight warps' results, joined
+      const bool whole = w.whole();
+      const int64_t slot = w.slot(blockIdx.x) * a.layout.rows;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float t = l[nt][x];
+          t += __shfl_xor_sync(0xffffffffu, t, 4);
+          t += __shfl_xor_sync(0xffffffffu, t, 8);
+          t += __shfl_xor_sync(0xffffffffu, t, 16);
+          l[nt][x] = t;
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");  // the buffers are free
+        float* mine = join + warp * 8 * L::kPad;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (g == 0) join_ml[warp * 8 + 2 * c + x] = make_float2(m[nt][x], l[nt][x]);
+#pragma unroll
+          for (int mt = 0; mt < kTiles; ++mt)  // [row][tile][g][2]: no two lanes of a half warp share a bank
+            *reinterpret_cast<float2*>(mine + (2 * c + x) * L::kPad + mt * 16 + 2 * g) =
+                make_float2(o[mt][nt][x], o[mt][nt][2 + x]);
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+        // a warp per row, D / 32 consecutive dims per lane
+        const int row = nt * 8 + warp;
+        if (row < rows && ok) {
+          constexpr int kD = D / 32;
+          float top = -INFINITY, sum = 0.f, acc[kD] = {};
+#pragma unroll
+          for (int v = 0; v < kWarps; ++v) top = fmaxf(top, join_ml[v * 8 + warp].x);
+          const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+          for (int v = 0; v < kWarps; ++v) {
+            const float2 y = join_ml[v * 8 + warp];
+            const float f = ex2_approx(y.x - ref);
+            sum = fmaf(y.y, f, sum);
+#pragma unroll
+            for (int e = 0; e < kD; e += 2) {
+              const int dim = lane * kD + e;  // held by group gg in its tile mt
+              const int gg = E == 1 ? dim / (D / 8) : dim / 8 % 8, mt = E == 1 ? dim % (D / 8) / 2 : dim / 64 * 4 + dim % 8 / 2;
+              const float2 z = *reinterpret_cast<const float2*>(join + (v * 8 + warp) * L::kPad + mt * 16 + 2 * gg);
+              acc[e] = fmaf(z.x, f, acc[e]);
+              acc[e + 1] = fmaf(z.y, f, acc[e + 1]);
+            }
+          }
+          if (whole) {
+            const float inv = 1.f / sum;
+            uint32_t* dst = reinterpret_cast<uint32_t*>(
+                static_cast<__nv_bfloat16*>(a.out) +
+                ((int64_t)(w.item.row0 + row / a.group) * a.h_q + w.head * a.group + row % a.group) * D + lane * kD);
+#pragma unroll
+            for (int e = 0; e < kD; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+          } else {
+            float* dst = reinterpret_cast<float*>(a.ws + a.layout.part_o) + (slot + row) * D + lane * kD;
+#pragma unroll
+            for (int e = 0; e < kD; ++e) dst[e] = acc[e];
+            if (lane == 0) reinterpret_cast<float2*>(a.ws + a.layout.part_ml)[slot + row] = make_float2(top, sum);
+          }
+        }
+      }
+      if (!whole) {
+        // The CTA that finishes the last piece joins them all, in their order.
+        __threadfence();
+        asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+        if (threadIdx.x == 0) {
+          int32_t* arrived = reinterpret_cast<int32_t*>(a.ws + a.layout.arrived) + 2 * w.first();
+          bars->last = ok && atomicAdd(arrived, 1) == w.parts() - 1;
+          __threadfence();
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+        if (bars->last) {
+          constexpr int kD = D / 32;
+          const float2* ml = reinterpret_cast<const float2*>(a.ws + a.layout.part_ml);
+          const float* po = reinterpret_cast<const float*>(a.ws + a.layout.part_o);
+          const int first = w.first(), parts = w.parts();
+          for (int row = warp; row < rows; row += kWarps) {
+            auto piece = [&](int i) { return (2 * (int64_t)(first + i) + (i == 0)) * a.layout.rows + row; };
+            float top = -INFINITY;
+            for (int i = lane; i < parts; i += 32) top = fmaxf(top, __ldcg(ml + piece(i)).x);
+            top = warp_max(top);
+            const float ref = top == -INFINITY ? 0.f : top;
+            float sum = 0.f, acc[kD] = {};
+#pragma unroll 4
+            for (int i = 0; i < parts; ++i) {
+              const float2 y = __ldcg(ml + piece(i));
+              const float f = ex2_approx(y.x - ref);
+              sum = fmaf(y.y, f, sum);
+#pragma unroll
+              for (int e = 0; e < kD; ++e) acc[e] = fmaf(__ldcg(po + piece(i) * D + lane * kD + e), f, acc[e]);
+            }
+            const float inv = 1.f / sum;
+            uint32_t* dst = reinterpret_cast<uint32_t*>(
+                static_cast<__nv_bfloat16*>(a.out) +
+                ((int64_t)(w.item.row0 + row / a.group) * a.h_q + w.head * a.group + row % a.group) * D + lane * kD);
+#pragma unroll
+            for (int e = 0; e < kD; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+          }
+        }
+      }
+    }
+    if (!ok && lane == 0) timeout();
+  }
+}
+
+template <int D, int E, int NT>
+cudaError_t launch(const SpanArgs& a, bool write, cudaStream_t s) {
+  using L = Smem<D, E>;
+  RowsArgs p;
+  p.s = a;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.wait_budget = wait_budget_cycles();
+  p.write = write;
+  CUtensorMap mk, mv;
+  const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)a.n_blocks * a.h_kv * kPage};
+  const cuuint32_t box[2] = {(cuuint32_t)(L::kPitch / E), 16};
+  const CUtensorMapSwizzle swizzle = L::kPitch == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  if (!span_tensor_map(&mk, a.pool_k, E, 2, dims, box, swizzle) || !span_tensor_map(&mv, a.pool_v, E, 2, dims, box, swizzle))
+    return cudaErrorInvalidValue;
+  static_assert(L::kBytes <= 232448, "shared memory");
+  const cudaError_t e =
+      cudaFuncSetAttribute(span_rows_kernel<D, E, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(span_rows_kernel<D, E, NT>, dim3(a.ctas), dim3(kThreads), (size_t)L::kBytes, s, mk, mv, p);
+}
+
+template <int D, int E>
+cudaError_t launch_nt(const SpanArgs& a, bool write, cudaStream_t s) {
+  return a.tile_rows == 8 ? launch<D, E, 1>(a, write, s) : launch<D, E, 2>(a, write, s);
+}
+
+}  // namespace
+
+cudaError_t launch_span_rows(const SpanArgs& a, bool write, cudaStream_t s) {
+  if (a.T <= 0) return cudaSuccess;
+  if (a.pool_elem == 1) return a.d == 64 ? launch_nt<64, 1>(a, write, s) : launch_nt<128, 1>(a, write, s);
+  return a.d == 64 ? launch_nt<64, 2>(a, write, s) : launch_nt<128, 2>(a, write, s);
+}
+
+}  // namespace kev

@@ -697,15 +697,24 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// bf16 view of `rank` dimensions (innermost first, contiguous), boxes of 64 x box..., 128-byte swizzle
-bool make_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint32_t* box) {
+}  // namespace
+
+bool span_tensor_map(CUtensorMap* m, const void* base, int elem, int rank, const cuuint64_t* dims, const cuuint32_t* box,
+                     CUtensorMapSwizzle swizzle) {
   const EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
-  cuuint64_t strides[2] = {dims[0] * 2, dims[0] * dims[1] * 2};
+  const cuuint64_t strides[2] = {dims[0] * elem, dims[0] * dims[1] * elem};
   const cuuint32_t ones[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, ones,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  return fn(m, elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base),
+            dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+namespace {
+
+// bf16, boxes of 64 x box..., 128-byte swizzle
+bool make_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint32_t* box) {
+  return span_tensor_map(m, base, 2, rank, dims, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 template <int D, bool Q8>
