@@ -111,6 +111,7 @@ struct SpanArgs {
   int32_t tile_tokens;    // floor(M / group)
   int32_t item_tiles;     // row tiles of an item
   int32_t ctas;           // parts of the work line
+  int32_t unit_cost;      // what a unit costs beside its key tiles, in key tiles
   int32_t attend;         // 0: cache write or read only (no items)
   char* ws;
   SpanLayout layout;

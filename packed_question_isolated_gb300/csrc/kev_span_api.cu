@@ -90,7 +90,9 @@ kev_status span_attend(SpanArgs* a, bool write, cudaStream_t s) {
   // register kernel takes at memory speed; it writes the new rows itself and joins its own pieces.
   const int64_t rows = (int64_t)a->max_chunk * a->group;
   if (a->elem == 2 && a->pool_elem && rows <= 16) {
-    span_tiling(a, rows <= 8 ? 8 : 16, 1, sms < kSpanMaxCtas ? sms : kSpanMaxCtas);
+    const int ctas = rows <= 8 ? 2 * sms : sms;
+    span_tiling(a, rows <= 8 ? 8 : 16, 1, ctas < kSpanMaxCtas ? ctas : kSpanMaxCtas);
+    a->unit_cost = 1;
     cudaError_t e = launch_span_plan(*a, s);
     if (e == cudaSuccess) e = launch_span_rows(*a, write, s);
     return from_cuda(e);

@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(SpanArgs a) {
       w.p0 = pre[lo] + token0;
       w.tiles = SpanTiles(w.p0, w.p0 + w.tokens - 1, a.window, a.sinks).n;
       out[x] = w;
-      tiles = (long long)w.tiles * a.h_kv;
+      tiles = (long long)(w.tiles + a.unit_cost) * a.h_kv;
     }
     long long sum;
     const long long at = block_scan(tiles, 0ll, s_sum, &sum);
@@ -278,8 +278,8 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(SpanArgs a) {
     __syncthreads();
   }
 
-  // cuts: part c begins at tile floor(c * total / parts) of the line; with at most one part per
-  // tile, no part is empty
+  // cuts: part c begins at place floor(c * total / parts) of the line, where a unit is its fixed cost
+  // and then its tiles; a cut in the fixed cost moves to the unit's beginning
   SpanCut* cuts = reinterpret_cast<SpanCut*>(a.ws + a.layout.cuts);
   int32_t* arrived = reinterpret_cast<int32_t*>(a.ws + a.layout.arrived);
   const long long total = run;
@@ -297,13 +297,14 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(SpanArgs a) {
         if (cum[mid] <= w) lo = mid;
         else hi = mid - 1;
       }
-      const int tiles = (int)(((lo + 1 < n_items ? cum[lo + 1] : total) - cum[lo]) / a.h_kv);
+      const int size = (int)(((lo + 1 < n_items ? cum[lo + 1] : total) - cum[lo]) / a.h_kv);
       const long long in = w - cum[lo];
       cut.item = lo;
-      cut.head = (int)(in / tiles);
-      cut.tile = (int)(in - (long long)cut.head * tiles);
+      cut.head = (int)(in / size);
+      const int at = (int)(in - (long long)cut.head * size);
+      cut.tile = max(0, at - a.unit_cost);
       if (cut.tile > 0) {
-        const long long begin = w - cut.tile, end = begin + tiles;
+        const long long begin = w - cut.tile, end = w - at + size;  // its tiles
         int first = c - 1, last = c;  // parts that hold a piece of the unit
         while (first > 0 && place(first) > begin) --first;
         while (last + 1 < parts && place(last + 1) < end) ++last;

@@ -2,16 +2,20 @@
 // bf16 or e4m3, at most 16 (token, q-head of the group) rows per question and kv head.
 //
 // Every cached row is read once and meets only those rows, so the bound is HBM (the cache, once)
-// and below it the instructions per element that unpack it.  Here the matrix instruction takes the
+// and below it the instructions per element that unpack it: e4m3 codes become fp16 (one conversion
+// per two; as bf16 it takes four integer operations), and q and the weights fp16 with scales of
+// their own.  Here the matrix instruction takes the
 // cache as its A operand straight from registers (mma.sync m16n8k16): S^T[16 keys x 8 rows] = K q^T,
 // O^T[dims x 8 rows] += V^T P^T.  With 8 rows nothing is padded, where tcgen05 would spend a 128-row
 // tile (or an extra trip of the unpacked codes through shared memory, which at HBM speed is more than
 // shared memory carries); the matrix pipe stays below half its time.
 //
-// One persistent CTA per SM walks its equal part of the work line (kev_span.cuh):
+// Two persistent CTAs per SM (one with 16 rows) walk their equal parts of the work line
+// (kev_span.cuh), so one's beginnings and ends of units lie beside the other's streaming:
 //   warp 8      loads pages into a ring: TMA boxes of 16 positions, only those that some row sees
-//   warp 9      first writes the new K/V rows that lie in this CTA's tiles (quantised for e4m3): every
-//               (unit, tile) has one owner, so a row is written once and read by the CTA that wrote it
+//   warp 9      writes the new K/V rows that lie in this CTA's tiles (quantised for e4m3) while the first
+//               pages arrive: every (unit, tile) has one owner, so a row is written once and read by the
+//               CTA that wrote it; pages with new rows are loaded after that
 //   warps 0-7   a warp takes 16 of a page's 128 positions, with a running reference maximum, sum and
 //               accumulator of its own; they are joined through shared memory when the unit ends
 // A unit that a cut goes through is joined by the CTA that finishes its last piece, in the order of
@@ -31,32 +35,39 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kWarps = 8;  // of 16 positions each: one page
+constexpr int kWarps = 8;  // of 16 positions each
 constexpr int kThreads = (kWarps + 2) * 32;
 constexpr int kLoadWarp = kWarps, kWriteWarp = kWarps + 1;
 constexpr float kBig = 1.8446744e19f;  // 2^64: a weight above it moves the reference
 constexpr long long kDrainBudget = 4000000000ll;
 
-template <int D, int E>
+template <int D, int E, int NT>
 struct Smem {
+  static constexpr int kCtas = NT == 1 ? 2 : 1;             // per SM
+  static constexpr int kKeys = E == 2 ? 64 : 128;           // positions of a stage: half a page, or a page
+  static constexpr int kHalves = kPage / kKeys;
+  static constexpr int kStageWarps = kKeys / 16;            // a stage's warps; with half pages two sets take turns
   static constexpr int kRow = D * E;                        // bytes of a cached row
   static constexpr int kPitch = kRow < 128 ? kRow : 128;    // row of a swizzled sub-tile
   static constexpr int kSubs = kRow / kPitch;
-  static constexpr int kTile = kPage * kRow;                // K or V of a page
-  static constexpr int kScales = E == 1 ? 2 * kPage * 4 : 0;
-  static constexpr int kRaw = 2 * kTile + kScales;
-  static constexpr int kStageBytes = (kRaw + 1023) / 1024 * 1024;
-  static constexpr int kStages = 196608 / kStageBytes < 8 ? 196608 / kStageBytes : 8;
+  static constexpr int kTile = kKeys * kRow;                // K or V of a stage
+  static constexpr int kScales = E == 1 ? 2 * kKeys * 4 : 0;
+  static constexpr int kStageBytes = 2 * kTile + (kScales + 1023) / 1024 * 1024;
   static constexpr int kPad = D + 4;                        // floats of a row in the join buffer
-  static constexpr int kJoin = kStages * kStageBytes;       // float [8 warps][8 rows][kPad]
-  static constexpr int kMl = kJoin + kWarps * 8 * kPad * 4;  // float2 [8 warps][8 rows]
-  static constexpr int kBar = kMl + kWarps * 8 * 8;
+  static constexpr int kJoinBytes = kWarps * 8 * kPad * 4;  // float [8 warps][8 rows][kPad]
+  static constexpr int kRoom = (kCtas == 2 ? 113 * 1024 : 226 * 1024) - 2048 - kJoinBytes - kWarps * 64;
+  // A warp waits for the stages of its own turns only, so each stage has to belong to one set of warps
+  // (a phase it did not wait for would pass for the one before): an even number with half pages.
+  static constexpr int kStages = (kRoom / kStageBytes < 8 ? kRoom / kStageBytes : 8) / kHalves * kHalves;
+  static constexpr int kJoin = kStages * kStageBytes;
+  static constexpr int kMl = kJoin + kJoinBytes;            // float2 [8 warps][8 rows]
+  static constexpr int kBar = kMl + kWarps * 64;
   static constexpr int kBytes = kBar + 256 + 1024;
 };
 
 struct Bars {
   uint64_t full[8], empty[8];
-  int written;  // units whose new rows are in the cache
+  uint64_t written;  // the new rows are in the cache
   int abort;
   int never;
   int last;
@@ -74,20 +85,28 @@ __device__ __forceinline__ int perm(int s) {  // position of slot s: 0 5 2 7 4 1
   return s & 1 ? (s ^ 4) : s;
 }
 
+// D += A B, bf16 (E = 2) or fp16 (E = 1) operands
+template <int E>
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  if (E == 2)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t at) {
-  uint32_t x;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(at));
+__device__ __forceinline__ float lds32(uint32_t at) {
+  float x;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at));
   return x;
 }
 __device__ __forceinline__ uint4 lds128(uint32_t at) {
@@ -101,12 +120,20 @@ __device__ __forceinline__ uint2 lds64(uint32_t at) {
   return x;
 }
 
-// two e4m3 codes in the high bytes of the halves of x (low bytes: anything) as exact bf16: exponent and
-// mantissa bits at their places, times 2^120 for the difference of the biases
-__device__ __forceinline__ uint32_t widen(uint32_t x) {
-  const uint32_t y = ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
+// two e4m3 codes (the low or high half of w) as fp16, which holds every one of them exactly
+__device__ __forceinline__ uint32_t widen_lo(uint32_t w) {
   uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(y), "r"(0x7b807b80u));
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t widen_hi(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 
@@ -121,16 +148,17 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
   return r;
 }
 
-// Some row of the item (tokens at p0 .. p1) sees one of positions u .. u + 15.
+// Some row of the item (tokens at p0 .. p1) sees one of positions u .. u + N - 1.
+template <int N = 16>
 __device__ __forceinline__ bool group_seen(const SpanArgs& a, int u, int p0, int p1) {
-  return u <= p1 && (a.window == 0 || p0 - (u + 15) < a.window || u < a.sinks);
+  return u <= p1 && (a.window == 0 || p0 - (u + N - 1) < a.window || u < a.sinks);
 }
 
 template <int D, int E, int NT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
     span_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ RowsArgs p) {
-  using L = Smem<D, E>;
+  using L = Smem<D, E, NT>;
   const SpanArgs& a = p.s;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem =
@@ -140,9 +168,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < 8; ++s) {
       mbar_init(&bars->full[s], 1);
-      mbar_init(&bars->empty[s], kWarps);
+      mbar_init(&bars->empty[s], L::kStageWarps);
     }
-    bars->written = bars->abort = bars->never = bars->last = 0;
+    mbar_init(&bars->written, 1);
+    bars->abort = bars->never = bars->last = 0;
     fence_mbar_init();
   }
   if (threadIdx.x == kLoadWarp * 32) {
@@ -164,47 +193,43 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kLoadWarp) {
     // -------------------------------------------------------------------- page loads
-    constexpr int kBoxes = 2 * L::kSubs * 8;  // 16-position boxes of a page: one per lane
-    const int is_v = lane / (kBoxes / 2), sub = lane / 8 % L::kSubs, grp = lane % 8;
+    constexpr int kBoxes = 2 * L::kSubs * L::kStageWarps;  // 16-position boxes of a stage: one per lane
+    const int is_v = lane / (kBoxes / 2), sub = lane / L::kStageWarps % L::kSubs, grp = lane % L::kStageWarps;
     uint32_t seq = 0;
-    bool ok = true;
-    int n = 0;
-    for (SpanWalk w(a, blockIdx.x); ok && w.live(); w.next(), ++n) {
+    bool ok = true, wrote = !p.write;
+    for (SpanWalk w(a, blockIdx.x); ok && w.live(); w.next()) {
       const int p0 = w.item.p0, p1 = p0 + w.item.tokens - 1;
       const SpanTiles tiles(p0, p1, a.window, a.sinks);
       const int32_t* row = a.table + (int64_t)w.item.question * a.max_blocks;
       int ids = 0;
-      bool wrote = !p.write;
-      for (int j = w.j0; j < w.j1; ++j, ++seq) {
+      for (int j = w.j0; ok && j < w.j1; ++j) {
         if ((j - w.j0) % 32 == 0) ids = j + lane < w.j1 ? row[tiles.at(j + lane)] : 0;  // 32 pages ahead
         const int block = __shfl_sync(0xffffffffu, ids, (j - w.j0) % 32);
-        const int u0 = tiles.at(j) * kPage;
-        const int s = seq % L::kStages;
-        if (seq >= L::kStages)
-          ok = __all_sync(0xffffffffu, mbar_wait(&bars->empty[s], (seq / L::kStages - 1) & 1, abort_flag, budget));
-        if (ok && !wrote && u0 + kPage > p0) {  // the page holds new rows: wait until they are written
-          const long long t0 = clock64();
-          const volatile int* written = &bars->written;
-          bool there;
-          while (!(there = *written > n) && !*abort_flag && clock64() - t0 < budget) {
+        for (int half = 0; half < L::kHalves; ++half) {
+          const int u0 = tiles.at(j) * kPage + half * L::kKeys;
+          if (L::kHalves > 1 && !group_seen<L::kKeys>(a, u0, p0, p1)) continue;
+          const int s = seq % L::kStages;
+          if (seq >= L::kStages)
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars->empty[s], (seq / L::kStages - 1) & 1, abort_flag, budget));
+          if (ok && !wrote && u0 + L::kKeys > p0) {  // new rows among them: wait until they are written
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars->written, 0, abort_flag, budget));
+            asm volatile("fence.proxy.async;" ::: "memory");
+            wrote = true;
           }
-          ok = __all_sync(0xffffffffu, there);
-          __threadfence_block();
-          asm volatile("fence.proxy.async;" ::: "memory");
-          wrote = true;
+          if (!ok) break;
+          const bool mine = lane < kBoxes && group_seen(a, u0 + grp * 16, p0, p1);
+          const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
+          const int cell = (block * a.h_kv + w.head) * kPage + half * L::kKeys;
+          unsigned char* dst = smem + s * L::kStageBytes;
+          if (lane == 0) mbar_arrive_expect_tx(&bars->full[s], boxes * 16 * L::kPitch + L::kScales);
+          __syncwarp();
+          if (mine)
+            tma_load_2d(dst + is_v * L::kTile + (sub * L::kKeys + grp * 16) * L::kPitch, is_v ? &tm_v : &tm_k,
+                        sub * L::kPitch / E, cell + grp * 16, &bars->full[s]);
+          if (E == 1 && lane < 2)
+            bulk_load(dst + 2 * L::kTile + lane * L::kKeys * 4, (lane ? a.scale_v : a.scale_k) + cell, L::kKeys * 4, &bars->full[s]);
+          ++seq;
         }
-        if (!ok) break;
-        const bool mine = lane < kBoxes && group_seen(a, u0 + grp * 16, p0, p1);
-        const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
-        const int cell = (block * a.h_kv + w.head) * kPage;
-        unsigned char* dst = smem + s * L::kStageBytes;
-        if (lane == 0) mbar_arrive_expect_tx(&bars->full[s], boxes * 16 * L::kPitch + L::kScales);
-        __syncwarp();
-        if (mine)
-          tma_load_2d(dst + is_v * L::kTile + (sub * kPage + grp * 16) * L::kPitch, is_v ? &tm_v : &tm_k,
-                      sub * L::kPitch / E, cell + grp * 16, &bars->full[s]);
-        if (E == 1 && lane < 2)
-          bulk_load(dst + 2 * L::kTile + lane * kPage * 4, (lane ? a.scale_v : a.scale_k) + cell, kPage * 4, &bars->full[s]);
       }
     }
     if (!ok && lane == 0) timeout();
@@ -216,7 +241,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!p.write) return;
     constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;  // lanes of a bf16 row
     const int sub = lane % kLanes;
-    int n = 0;
     for (SpanWalk w(a, blockIdx.x); w.live(); w.next()) {
       const int p0 = w.item.p0;
       const SpanTiles tiles(p0, p0 + w.item.tokens - 1, a.window, a.sinks);
@@ -259,12 +283,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      __threadfence();
-      asm volatile("fence.proxy.async;" ::: "memory");  // before the copies of the page, which the other warp issues
-      __syncwarp();
-      ++n;
-      if (lane == 0) *reinterpret_cast<volatile int*>(&bars->written) = n;
     }
+    __threadfence();
+    asm volatile("fence.proxy.async;" ::: "memory");  // before the copies of these pages, which the other warp issues
+    mbar_arrive_warp(&bars->written);
   } else {
     // -------------------------------------------------------------------- attention
     span_zero_gaps(a, kWarps * 32);
@@ -278,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // swizzled address of 16-byte chunk ch of row r
     auto at = [&](uint32_t tile, int r, int ch) {
       if (L::kPitch == 128)
-        return tile + (ch >> 3) * (kPage * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+        return tile + (ch >> 3) * (L::kKeys * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
       return tile + r * 64 + ((ch ^ (r >> 1 & 3)) << 4);
     };
     uint32_t seq = 0;
@@ -304,15 +326,43 @@ __global__ void __launch_bounds__(kThreads, 1)
             q[nt][i * kSteps + h][1] = x.y;
           }
       }
+      // fp16 has no exponents to spare: a row of q is scaled by a power of two that puts its largest element
+      // in [2^14, 2^15) -- exact down to 2^-29 of it, and off by at most 2^-40 of it below -- and the
+      // scores by its inverse
+      float q_inv[NT][2];
+      if (E == 1) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          uint32_t top = 0;
+#pragma unroll
+          for (int i = 0; i < kChunks * kSteps; ++i)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              top = max(top, max(q[nt][i][x] & 0x7fffu, q[nt][i][x] >> 16 & 0x7fffu));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const int up = min(127 + 14 - (int)(top >> 7), 100);  // 2^up; 14 - (exponent - 127)
+          const float mul = __int_as_float((127 + up) << 23);
+#pragma unroll
+          for (int i = 0; i < kChunks * kSteps; ++i)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              q[nt][i][x] = pack_f16x2(__uint_as_float(q[nt][i][x] << 16) * mul, __uint_as_float(q[nt][i][x] & 0xffff0000u) * mul);
+          const float inv = __int_as_float((127 - up) << 23);  // of row g: rows 2c, 2c + 1 are other lanes'
+          q_inv[nt][0] = __shfl_sync(0xffffffffu, inv, 8 * c) * p.scale_log2;
+          q_inv[nt][1] = __shfl_sync(0xffffffffu, inv, 8 * c + 4) * p.scale_log2;
+        }
+      }
       int pos[NT][2];  // positions of rows nt * 8 + 2c, + 1
       float m[NT][2], l[NT][2], o[kTiles][NT][4];
+      float per[NT][2];  // e4m3: O is in units of 1 / per (below); 0: none yet
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           pos[nt][x] = min(p0 + (nt * 8 + 2 * c + x) / a.group, p1);  // rows past the last: as its own
           m[nt][x] = -INFINITY;
-          l[nt][x] = 0.f;
+          l[nt][x] = per[nt][x] = 0.f;
         }
 #pragma unroll
       for (int mt = 0; mt < kTiles; ++mt)
@@ -321,14 +371,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int x = 0; x < 4; ++x) o[mt][nt][x] = 0.f;
 
-      for (int j = w.j0; j < w.j1; ++j, ++seq) {
-        const int s = seq % L::kStages;
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->full[s], (seq / L::kStages) & 1, abort_flag, budget));
-        const int u0 = tiles.at(j) * kPage + warp * 16;  // this warp's positions
+      for (int j = w.j0; j < w.j1; ++j)
+      for (int half = 0; half < L::kHalves; ++half) {
+        const int h0 = tiles.at(j) * kPage + half * L::kKeys;
+        if (L::kHalves > 1 && !group_seen<L::kKeys>(a, h0, p0, p1)) continue;
+        const uint32_t here = seq++;
+        if (L::kHalves > 1 && (here & 1) != warp / L::kStageWarps) continue;  // the other warps' turn
+        const int s = here % L::kStages;
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->full[s], (here / L::kStages) & 1, abort_flag, budget));
         if (!ok) continue;
+        const int k0 = warp % L::kStageWarps * 16, u0 = h0 + k0;  // this warp's 16 positions of the stage
         if (group_seen(a, u0, p0, p1)) {
           const uint32_t tk = smem0 + s * L::kStageBytes, tv = tk + L::kTile;
-          const int r0 = warp * 16 + perm(g);  // slots g and g + 8
+          const int r0 = k0 + perm(g);  // slots g and g + 8
           float z[NT][4];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -347,22 +402,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 a2 = xs[(2 * h + 1) & 3];
                 a3 = ys[(2 * h + 1) & 3];
               } else {
-                a0 = widen(__byte_perm(xs[h & 3], 0u, 0x1404));
-                a1 = widen(__byte_perm(ys[h & 3], 0u, 0x1404));
-                a2 = widen(__byte_perm(xs[h & 3], 0u, 0x3424));
-                a3 = widen(__byte_perm(ys[h & 3], 0u, 0x3424));
+                a0 = widen_lo(xs[h & 3]);
+                a1 = widen_lo(ys[h & 3]);
+                a2 = widen_hi(xs[h & 3]);
+                a3 = widen_hi(ys[h & 3]);
               }
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma(z[nt], a0, a1, a2, a3, q[nt][i * kSteps + h][0], q[nt][i * kSteps + h][1]);
+              for (int nt = 0; nt < NT; ++nt) mma<E>(z[nt], a0, a1, a2, a3, q[nt][i * kSteps + h][0], q[nt][i * kSteps + h][1]);
             }
           }
           float kf0 = p.scale_log2, kf1 = kf0, vf0 = 1.f, vf1 = 1.f;
           if (E == 1) {
             const uint32_t sc = tk + 2 * L::kTile + r0 * 4;
-            kf0 *= __uint_as_float(lds32(sc));
-            kf1 *= __uint_as_float(lds32(sc + 32));
-            vf0 = __uint_as_float(lds32(sc + kPage * 4));
-            vf1 = __uint_as_float(lds32(sc + kPage * 4 + 32));
+            kf0 = lds32(sc);
+            kf1 = lds32(sc + 32);
+            vf0 = lds32(sc + L::kKeys * 4);
+            vf1 = lds32(sc + L::kKeys * 4 + 32);
           }
           // every row sees all 16 positions
           const bool edge = !(u0 + 15 <= p0 && (a.window == 0 || p1 - u0 < a.window || u0 + 15 < a.sinks));
@@ -372,32 +427,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              z[nt][x] *= kf0;
-              z[nt][2 + x] *= kf1;
+              z[nt][x] *= E == 1 ? kf0 * q_inv[nt][x] : kf0;
+              z[nt][2 + x] *= E == 1 ? kf1 * q_inv[nt][x] : kf1;
               if (edge) {
                 if (!span_sees(pos[nt][x], key0, a.window, a.sinks)) z[nt][x] = -INFINITY;
                 if (!span_sees(pos[nt][x], key1, a.window, a.sinks)) z[nt][2 + x] = -INFINITY;
               }
-              unset = unset || m[nt][x] == -INFINITY;
+              unset = unset || m[nt][x] == -INFINITY || (E == 1 && per[nt][x] == 0.f);
             }
           }
-          // the largest of a row's 16 scores: over the lanes that share c
-          auto top_of = [&](int nt, int x) {
-            float t = fmaxf(z[nt][x], z[nt][2 + x]);
+          // the largest over a row's 16 positions: over the lanes that share c
+          auto top_of = [&](float x, float y) {
+            float t = fmaxf(x, y);
             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
             return fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
           };
-          if (__any_sync(0xffffffffu, unset)) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const float t = top_of(nt, x);
-                if (m[nt][x] == -INFINITY) m[nt][x] = t;
-              }
-          }
-          float pr[NT][4];
+          // The weights exp2(z - m), and for V the weight times V's scale times `per`.  m and 1 / per are
+          // references, not exact maxima: they move only when a weight outgrows them -- 2^64 for bf16
+          // weights, 2^14 for fp16 ones (the row's largest stays above 1, so what fp16 rounds below its
+          // normal range is off by 2^-25 of it at most) -- so between moves no row maximum is taken.
+          float pr[NT][4], wv[NT][4];
           auto weights = [&]() {
             bool big = false;
 #pragma unroll
@@ -406,45 +456,55 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int x = 0; x < 4; ++x) {
                 const float ref = m[nt][x & 1] == -INFINITY ? 0.f : m[nt][x & 1];
                 pr[nt][x] = ex2_approx(z[nt][x] - ref);
+                if (E == 1) {
+                  wv[nt][x] = pr[nt][x] * ((x < 2 ? vf0 : vf1) * per[nt][x & 1]);
+                  if (edge && z[nt][x] == -INFINITY) wv[nt][x] = 0.f;  // a masked row's scale may be anything
+                  big = big || !(wv[nt][x] <= 16384.f);
+                } else {
+                  wv[nt][x] = pr[nt][x];
+                }
                 big = big || !(pr[nt][x] <= kBig);
               }
-            return __any_sync(0xffffffffu, big);
+            return big;
           };
-          if (weights()) {  // scores outgrew the reference (or are not numbers): the exact maximum, and all rescaled
+          bool move = weights();
+          if (__any_sync(0xffffffffu, move || unset)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
-                const float t = fmaxf(top_of(nt, x), m[nt][x]);
-                const float alpha = t == -INFINITY ? 1.f : ex2_approx(m[nt][x] - t);
+                const float t = fmaxf(top_of(z[nt][x], z[nt][2 + x]), m[nt][x]);
+                const float alpha = m[nt][x] == -INFINITY ? 0.f : ex2_approx(m[nt][x] - t);
                 m[nt][x] = t;
                 l[nt][x] *= alpha;
+                float mul = alpha;
+                if (E == 1) {  // O keeps its size when m moves, its unit takes the factor
+                  const float ref = t == -INFINITY ? 0.f : t;
+                  const float w0 = z[nt][x] == -INFINITY ? 0.f : ex2_approx(z[nt][x] - ref) * vf0;
+                  const float w1 = z[nt][2 + x] == -INFINITY ? 0.f : ex2_approx(z[nt][2 + x] - ref) * vf1;
+                  const float top = top_of(w0, w1), old = per[nt][x] > 0.f ? alpha / per[nt][x] : 0.f;
+                  mul = top > old * 16384.f ? old / top : 1.f;
+                  const float unit = top > old * 16384.f ? top : old;
+                  per[nt][x] = unit > 0.f ? 1.f / unit : 0.f;
+                }
 #pragma unroll
                 for (int mt = 0; mt < kTiles; ++mt) {
-                  o[mt][nt][x] *= alpha;
-                  o[mt][nt][2 + x] *= alpha;
+                  o[mt][nt][x] *= mul;
+                  o[mt][nt][2 + x] *= mul;
                 }
               }
             weights();
           }
-          uint32_t b[NT][2];
+          uint32_t b[NT][2];  // rounded to 16 bits here, as the product's operand
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int x = 0; x < 2; ++x) l[nt][x] += pr[nt][x] + pr[nt][2 + x];
-            float w0 = pr[nt][0] * vf0, w1 = pr[nt][1] * vf0, w2 = pr[nt][2] * vf1, w3 = pr[nt][3] * vf1;
-            if (E == 1 && edge) {  // the scale of a masked row may be anything
-              if (z[nt][0] == -INFINITY) w0 = 0.f;
-              if (z[nt][1] == -INFINITY) w1 = 0.f;
-              if (z[nt][2] == -INFINITY) w2 = 0.f;
-              if (z[nt][3] == -INFINITY) w3 = 0.f;
-            }
-            // the weights are rounded to bf16 here, as the product's operand
-            b[nt][0] = transpose8x8(pack_bf16x2(w0, w1));
-            b[nt][1] = transpose8x8(pack_bf16x2(w2, w3));
+            b[nt][0] = transpose8x8(E == 1 ? pack_f16x2(wv[nt][0], wv[nt][1]) : pack_bf16x2(wv[nt][0], wv[nt][1]));
+            b[nt][1] = transpose8x8(E == 1 ? pack_f16x2(wv[nt][2], wv[nt][3]) : pack_bf16x2(wv[nt][2], wv[nt][3]));
           }
           // V: rows of slots 2c, 2c + 1, 2c + 8, 2c + 9
-          const int v0 = warp * 16 + perm(2 * c), v1 = warp * 16 + perm(2 * c + 1);
+          const int v0 = k0 + perm(2 * c), v1 = k0 + perm(2 * c + 1);
           const int vr[4] = {v0, v1, v0 + 8, v1 + 8};
           if (E == 2) {
 #pragma unroll
@@ -474,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (__any_sync(0xffffffffu, any != 0)) {
 #pragma unroll 1
                   for (int k = 0; k < 16; ++k) {
-                    const uint4 y = lds128(at(tv, warp * 16 + k, g + 8 * i));
+                    const uint4 y = lds128(at(tv, k0 + k, g + 8 * i));
                     const uint32_t ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
                     for (int t = 0; t < 4; ++t)
@@ -494,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t a0 = __byte_perm(x[0][t], x[1][t], 0x5410), a1 = __byte_perm(x[0][t], x[1][t], 0x7632);
                 const uint32_t a2 = __byte_perm(x[2][t], x[3][t], 0x5410), a3 = __byte_perm(x[2][t], x[3][t], 0x7632);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma(o[4 * i + t][nt], a0, a1, a2, a3, b[nt][0], b[nt][1]);
+                for (int nt = 0; nt < NT; ++nt) mma<E>(o[4 * i + t][nt], a0, a1, a2, a3, b[nt][0], b[nt][1]);
               }
             }
           } else {
@@ -513,15 +573,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 x[e][1] = y.y;
               }
             }
+            if (edge) {  // the NaN codes of masked positions; rows that see one have its NaN scale in their weight
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int t = 0; t < D / 32; ++t) {
+                  const uint32_t bad = ((x[e][t] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                  x[e][t] &= ~((bad >> 7) * 0xffu);
+                }
+            }
 #pragma unroll
             for (int t = 0; t < D / 32; ++t)
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {  // dims 4t + 2h, + 1
-                const uint32_t s0 = h ? 0x6622 : 0x4400, s1 = h ? 0x7733 : 0x5511;
-                const uint32_t a0 = widen(__byte_perm(x[0][t], x[1][t], s0)), a1 = widen(__byte_perm(x[0][t], x[1][t], s1));
-                const uint32_t a2 = widen(__byte_perm(x[2][t], x[3][t], s0)), a3 = widen(__byte_perm(x[2][t], x[3][t], s1));
+              for (int h = 0; h < 2; ++h) {  // (key, key) pairs of dims 4t + 2h, + 1
+                const uint32_t u = __byte_perm(x[0][t], x[1][t], h ? 0x7362 : 0x5140);
+                const uint32_t v = __byte_perm(x[2][t], x[3][t], h ? 0x7362 : 0x5140);
+                const uint32_t a0 = widen_lo(u), a1 = widen_hi(u), a2 = widen_lo(v), a3 = widen_hi(v);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma(o[2 * t + h][nt], a0, a1, a2, a3, b[nt][0], b[nt][1]);
+                for (int nt = 0; nt < NT; ++nt) mma<E>(o[2 * t + h][nt], a0, a1, a2, a3, b[nt][0], b[nt][1]);
               }
           }
         }
@@ -545,11 +614,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         float* mine = join + warp * 8 * L::kPad;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
+          const float unit = per[nt][x] > 0.f ? 1.f / per[nt][x] : 0.f;
           if (g == 0) join_ml[warp * 8 + 2 * c + x] = make_float2(m[nt][x], l[nt][x]);
 #pragma unroll
           for (int mt = 0; mt < kTiles; ++mt)  // [row][tile][g][2]: no two lanes of a half warp share a bank
             *reinterpret_cast<float2*>(mine + (2 * c + x) * L::kPad + mt * 16 + 2 * g) =
-                make_float2(o[mt][nt][x], o[mt][nt][2 + x]);
+                E == 1 ? make_float2(o[mt][nt][x] * unit, o[mt][nt][2 + x] * unit)
+                       : make_float2(o[mt][nt][x], o[mt][nt][2 + x]);
         }
         asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
         // a warp per row, D / 32 consecutive dims per lane
@@ -635,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int D, int E, int NT>
 cudaError_t launch(const SpanArgs& a, bool write, cudaStream_t s) {
-  using L = Smem<D, E>;
+  using L = Smem<D, E, NT>;
   RowsArgs p;
   p.s = a;
   p.scale_log2 = a.scale * 1.4426950408889634f;
@@ -647,7 +718,7 @@ cudaError_t launch(const SpanArgs& a, bool write, cudaStream_t s) {
   const CUtensorMapSwizzle swizzle = L::kPitch == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
   if (!span_tensor_map(&mk, a.pool_k, E, 2, dims, box, swizzle) || !span_tensor_map(&mv, a.pool_v, E, 2, dims, box, swizzle))
     return cudaErrorInvalidValue;
-  static_assert(L::kBytes <= 232448, "shared memory");
+  static_assert(L::kStages >= 2 && L::kStages % L::kHalves == 0 && L::kCtas * (L::kBytes + 1024) <= 228 * 1024, "shared memory");
   const cudaError_t e =
       cudaFuncSetAttribute(span_rows_kernel<D, E, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
   if (e != cudaSuccess) return e;
