@@ -21,6 +21,7 @@ namespace kev {
 
 constexpr int kSpanKeys = 128;     // positions per key tile: one page
 constexpr int kSpanMaxCtas = 304;  // parts of the work line (2 CTAs on each of 152 SMs)
+constexpr int kSpanRows = 16;      // rows of a unit in the kernel for few rows
 constexpr int kSpanMaxBlocks = 1 << 20;  // pool blocks: the plan marks used blocks in a bit map in shared memory
 
 struct SpanHeader {
@@ -28,13 +29,6 @@ struct SpanHeader {
   int32_t n_items;
   int32_t n_gaps;
   int32_t n_new;  // tokens in questions
-};
-
-// Cut c of the work line: the unit (item, kv head) and the key tile of it where part c begins.
-// Where tile > 0 the cut is inside the unit: first = the part the unit begins in, parts = how many
-// parts it has.
-struct SpanCut {
-  int32_t item, head, tile, first, parts;
 };
 
 struct alignas(16) SpanItem {
@@ -46,14 +40,22 @@ struct alignas(16) SpanItem {
   int32_t pad[3];
 };
 
+// Cut c of the work line: the unit (item, kv head) and the key tile of it where part c begins, with
+// the item's record beside them (a part begins with one load).  Where tile > 0 the cut is inside the
+// unit: first = the part the unit begins in, parts = how many parts it has.
+struct alignas(16) SpanCut {
+  SpanItem record;
+  int32_t item, head, tile, first, parts;
+  int32_t pad[3];
+};
+
 struct SpanLayout {
   size_t cu;       // int32[n + 1] prefix sums of the lengths, in question order
   size_t gaps;     // int2[n + 1] token ranges of no question
   size_t items;    // SpanItem[max_items]
   size_t cum;      // int64[max_items + 1] key tiles (over all kv heads) before each item
   size_t cuts;     // SpanCut[kSpanMaxCtas + 1]
-  size_t arrived;  // int32[kSpanMaxCtas][2] finished pieces of the unit that begins in part c and goes on
-                   // (one count per row tile)
+  size_t arrived;  // int32[kSpanMaxCtas][kSpanRows] finished pieces of the unit that begins in part c and goes on
   size_t part_ml;  // float2[2 * kSpanMaxCtas][rows] running maximum (log2 units) and sum
   size_t part_o;   // float[2 * kSpanMaxCtas][rows][d]
   size_t total;
@@ -79,7 +81,7 @@ inline SpanLayout span_layout(int32_t n, int32_t T, int32_t group, int32_t d) {
   L.items = take(sizeof(SpanItem) * (size_t)L.max_items);
   L.cum = take(sizeof(int64_t) * ((size_t)L.max_items + 1));
   L.cuts = take(sizeof(SpanCut) * (kSpanMaxCtas + 1));
-  L.arrived = take(sizeof(int32_t) * 2 * kSpanMaxCtas);
+  L.arrived = take(sizeof(int32_t) * kSpanRows * kSpanMaxCtas);
   L.part_ml = take(sizeof(float2) * 2 * kSpanMaxCtas * (size_t)L.rows);
   L.part_o = take(sizeof(float) * 2 * kSpanMaxCtas * (size_t)L.rows * d);
   L.total = off;
@@ -146,19 +148,21 @@ struct SpanTiles {
 struct SpanWalk {
   const SpanItem* items;
   SpanItem item, ahead;
-  SpanCut from, to;
-  int it, head, h_kv, j0, j1;
+  SpanCut to;
+  int from_first, from_parts, it, head, h_kv, j0, j1;
   __device__ __forceinline__ SpanWalk(const SpanArgs& a, int part) {
     items = reinterpret_cast<const SpanItem*>(a.ws + a.layout.items);
     const SpanCut* cuts = reinterpret_cast<const SpanCut*>(a.ws + a.layout.cuts);
-    from = cuts[part];
+    const SpanCut from = cuts[part];
     to = cuts[part + 1];
+    from_first = from.first;
+    from_parts = from.parts;
     it = from.item;
     head = from.head;
     h_kv = a.h_kv;
     j0 = from.tile;
     if (live()) {
-      item = items[it];
+      item = from.record;
       if (it < to.item) ahead = items[it + 1];  // one record past the last item is laid out
       j1 = last();
     }
@@ -167,12 +171,16 @@ struct SpanWalk {
   __device__ __forceinline__ bool live() const {
     return it < to.item || (it == to.item && (head < to.head || (head == to.head && j0 < to.tile)));
   }
+  __device__ __forceinline__ bool ends() const {  // the part's last unit
+    return it == to.item ? head == to.head || (to.tile == 0 && head + 1 == to.head)
+                         : to.tile == 0 && to.head == 0 && it + 1 == to.item && head + 1 == h_kv;
+  }
   __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == item.tiles; }
   // slot of this unit's partial result: the unit began in an earlier part, or ends in a later one
   __device__ __forceinline__ int64_t slot(int part) const { return 2 * (int64_t)part + (j0 == 0); }
   // the unit's pieces: the part it begins in, and how many
-  __device__ __forceinline__ int first() const { return j0 ? from.first : to.first; }
-  __device__ __forceinline__ int parts() const { return j0 ? from.parts : to.parts; }
+  __device__ __forceinline__ int first() const { return j0 ? from_first : to.first; }
+  __device__ __forceinline__ int parts() const { return j0 ? from_parts : to.parts; }
   __device__ __forceinline__ void next() {
     j0 = 0;
     if (++head == h_kv) {

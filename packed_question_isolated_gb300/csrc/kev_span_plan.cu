@@ -139,9 +139,11 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(SpanArgs a) {
       cu[n] = all.tokens;
       base[n] = all.items;
     }
-    if (words) {  // pages: one warp per question, a lane per page; a block's bit may be set once
+    if (words) {  // pages: one or more warps per question, a lane per page; a block's bit may be set once
+      const int slices = n < kThreads / 32 ? kThreads / 32 / n : 1;
 #pragma unroll 1
-      for (int i = warp; i < n; i += kThreads / 32) {
+      for (int x = warp; x < n * slices; x += kThreads / 32) {
+        const int i = x / slices;
         const int L = iv[i].end - iv[i].begin;
         if (L <= 0) continue;
         const int p0 = pre[i], p1 = p0 + L - 1;
@@ -154,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(SpanArgs a) {
         const int pages = ns + p1 / kPage - lo + 1;
         const int32_t* row = a.table + (int64_t)i * a.max_blocks;
 #pragma unroll 4
-        for (int e = lane; e < pages; e += 32) {
+        for (int e = x % slices * 32 + lane; e < pages; e += 32 * slices) {
           const int b = row[e < ns ? e : lo + e - ns];
           const unsigned bit = 1u << (b & 31);
           if (b < 0 || b >= a.n_blocks || atomicOr(&used[b >> 5], bit) & bit) error(3);
@@ -249,25 +251,29 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(SpanArgs a) {
   const int n_items = all.items;
   long long* cum = n_items <= kCumSmem ? reinterpret_cast<long long*>(area)
                                        : reinterpret_cast<long long*>(a.ws + a.layout.cum);
+  auto record = [&](int x) {
+    int lo = 0, hi = n - 1;  // the last question whose first item is at or before x
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (base[mid] <= x) lo = mid;
+      else hi = mid - 1;
+    }
+    SpanItem w = {};
+    const int token0 = (x - base[lo]) * item_tokens;
+    w.question = lo;
+    w.row0 = iv[lo].begin + token0;
+    w.tokens = min(item_tokens, iv[lo].end - w.row0);
+    w.p0 = pre[lo] + token0;
+    w.tiles = SpanTiles(w.p0, w.p0 + w.tokens - 1, a.window, a.sinks).n;
+    return w;
+  };
   long long run = 0;
 #pragma unroll 1
   for (int first = 0; first < n_items; first += kThreads) {
     const int x = first + t;
     long long tiles = 0;
     if (x < n_items) {
-      int lo = 0, hi = n - 1;  // the last question whose first item is at or before x
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (base[mid] <= x) lo = mid;
-        else hi = mid - 1;
-      }
-      SpanItem w;
-      const int token0 = (x - base[lo]) * item_tokens;
-      w.question = lo;
-      w.row0 = iv[lo].begin + token0;
-      w.tokens = min(item_tokens, iv[lo].end - w.row0);
-      w.p0 = pre[lo] + token0;
-      w.tiles = SpanTiles(w.p0, w.p0 + w.tokens - 1, a.window, a.sinks).n;
+      const SpanItem w = record(x);
       out[x] = w;
       tiles = (long long)(w.tiles + a.unit_cost) * a.h_kv;
     }
@@ -282,14 +288,15 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(SpanArgs a) {
   // and then its tiles; a cut in the fixed cost moves to the unit's beginning
   SpanCut* cuts = reinterpret_cast<SpanCut*>(a.ws + a.layout.cuts);
   int32_t* arrived = reinterpret_cast<int32_t*>(a.ws + a.layout.arrived);
+  for (int x = t; x < a.ctas * kSpanRows; x += kThreads) arrived[x] = 0;
   const long long total = run;
   const int parts = total < a.ctas ? (int)total : a.ctas;
   for (int c = t; c <= a.ctas; c += kThreads) {
-    if (c < a.ctas) arrived[2 * c] = arrived[2 * c + 1] = 0;
-    const long long g = parts ? total / parts : 0, r = parts ? total % parts : 0;
-    auto place = [&](int x) { return (long long)x * g + (long long)x * r / parts; };
-    const long long w = c < parts ? place(c) : total;
-    SpanCut cut = {n_items, 0, 0, 0, 0};
+    // part c begins at c * total / parts; the part that holds place x is ((x + 1) * parts - 1) / total
+    auto part_of = [&](long long x) { return (int)(((x + 1) * parts - 1) / total); };
+    const long long w = c < parts ? c * total / parts : total;
+    SpanCut cut = {};
+    cut.item = n_items;
     if (w < total) {
       int lo = 0, hi = n_items - 1;
       while (lo < hi) {
@@ -300,16 +307,14 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(SpanArgs a) {
       const int size = (int)(((lo + 1 < n_items ? cum[lo + 1] : total) - cum[lo]) / a.h_kv);
       const long long in = w - cum[lo];
       cut.item = lo;
+      cut.record = record(lo);
       cut.head = (int)(in / size);
       const int at = (int)(in - (long long)cut.head * size);
       cut.tile = max(0, at - a.unit_cost);
       if (cut.tile > 0) {
         const long long begin = w - cut.tile, end = w - at + size;  // its tiles
-        int first = c - 1, last = c;  // parts that hold a piece of the unit
-        while (first > 0 && place(first) > begin) --first;
-        while (last + 1 < parts && place(last + 1) < end) ++last;
-        cut.first = first;
-        cut.parts = last - first + 1;
+        cut.first = part_of(begin);
+        cut.parts = part_of(end - 1) - cut.first + 1;
       }
     }
     cuts[c] = cut;

@@ -13,13 +13,14 @@
 // Two persistent CTAs per SM (one with 16 rows) walk their equal parts of the work line
 // (kev_span.cuh), so one's beginnings and ends of units lie beside the other's streaming:
 //   warp 8      loads pages into a ring: TMA boxes of 16 positions, only those that some row sees
-//   warp 9      writes the new K/V rows that lie in this CTA's tiles (quantised for e4m3) while the first
-//               pages arrive: every (unit, tile) has one owner, so a row is written once and read by the
-//               CTA that wrote it; pages with new rows are loaded after that
 //   warps 0-7   a warp takes 16 of a page's 128 positions, with a running reference maximum, sum and
-//               accumulator of its own; they are joined through shared memory when the unit ends
-// A unit that a cut goes through is joined by the CTA that finishes its last piece, in the order of
-// the pieces, so the result does not depend on which CTA that is.
+//               accumulator of its own, which it leaves in shared memory when the unit ends
+//               A warp that comes to positions of the chunk itself takes their K/V rows from the inputs:
+//               into the loaded page, and (quantised for e4m3) into the cache.  Every (unit, tile) has
+//               one owner, so a row is written once, and nobody waits for the write
+//   warp 9      joins the eight warps' results while they work on the next unit, and the pieces of a
+//               unit that a cut goes through, if its own piece is the last one done -- in the order of
+//               the pieces, so the result does not depend on which CTA that is
 //
 // Registers instead of ldmatrix: the contraction index of an MMA may be permuted freely, so a lane
 // takes whole 16-byte chunks of a row (8 bf16 or 16 codes) as its share of several k-steps.  For K,
@@ -37,7 +38,7 @@ using namespace sm100;
 
 constexpr int kWarps = 8;  // of 16 positions each
 constexpr int kThreads = (kWarps + 2) * 32;
-constexpr int kLoadWarp = kWarps, kWriteWarp = kWarps + 1;
+constexpr int kLoadWarp = kWarps, kJoinWarp = kWarps + 1;
 constexpr float kBig = 1.8446744e19f;  // 2^64: a weight above it moves the reference
 constexpr long long kDrainBudget = 4000000000ll;
 
@@ -55,22 +56,26 @@ struct Smem {
   static constexpr int kStageBytes = 2 * kTile + (kScales + 1023) / 1024 * 1024;
   static constexpr int kPad = D + 4;                        // floats of a row in the join buffer
   static constexpr int kJoinBytes = kWarps * 8 * kPad * 4;  // float [8 warps][8 rows][kPad]
-  static constexpr int kRoom = (kCtas == 2 ? 113 * 1024 : 226 * 1024) - 2048 - kJoinBytes - kWarps * 64;
+  static constexpr int kQPitch = 2 * D + 16;                // bytes of a staged q row
+  static constexpr int kQBytes = NT * 8 * kQPitch;          // q rows of a unit
+  static constexpr int kRoom = (kCtas == 2 ? 113 * 1024 : 226 * 1024) - 2048 - kJoinBytes - kWarps * 64 - 2 * kQBytes;
   // A warp waits for the stages of its own turns only, so each stage has to belong to one set of warps
   // (a phase it did not wait for would pass for the one before): an even number with half pages.
   static constexpr int kStages = (kRoom / kStageBytes < 8 ? kRoom / kStageBytes : 8) / kHalves * kHalves;
   static constexpr int kJoin = kStages * kStageBytes;
   static constexpr int kMl = kJoin + kJoinBytes;            // float2 [8 warps][8 rows]
-  static constexpr int kBar = kMl + kWarps * 64;
+  static constexpr int kQ = kMl + kWarps * 64;              // two units' q rows
+  static constexpr int kBar = kQ + 2 * kQBytes;
   static constexpr int kBytes = kBar + 256 + 1024;
 };
 
 struct Bars {
   uint64_t full[8], empty[8];
-  uint64_t written;  // the new rows are in the cache
+  uint64_t q_full[2], q_empty[2];
+  uint64_t join_full, join_empty;
+  uint64_t join_empty8;  // the last unit's first 8 rows are joined
   int abort;
   int never;
-  int last;
 };
 static_assert(sizeof(Bars) <= 256, "barriers");
 
@@ -154,6 +159,91 @@ __device__ __forceinline__ bool group_seen(const SpanArgs& a, int u, int p0, int
   return u <= p1 && (a.window == 0 || p0 - (u + N - 1) < a.window || u < a.sinks);
 }
 
+// A row of the output: D / 32 consecutive dims per lane.
+template <int D>
+__device__ __forceinline__ void store_row(const SpanArgs& a, const SpanItem& w, int head, int row, const float (&o)[D / 32],
+                                          float sum) {
+  constexpr int kD = D / 32;
+  const float inv = 1.f / sum;
+  uint32_t x[kD / 2];
+#pragma unroll
+  for (int e = 0; e < kD; e += 2) x[e / 2] = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
+  uint32_t* dst = reinterpret_cast<uint32_t*>(
+      static_cast<__nv_bfloat16*>(a.out) +
+      ((int64_t)(w.row0 + row / a.group) * a.h_q + head * a.group + row % a.group) * D + (threadIdx.x & 31) * kD);
+  if (kD == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(x[0], x[kD / 2 - 1]);
+  else *dst = x[0];
+}
+
+// The pieces of a row of a unit, joined by a warp.
+template <int D>
+__device__ __forceinline__ void join_pieces(const SpanArgs& a, const SpanItem& w, int head, int row, int first, int parts) {
+  constexpr int kD = D / 32;
+  const int lane = threadIdx.x & 31;
+  const float2* ml = reinterpret_cast<const float2*>(a.ws + a.layout.part_ml);
+  const float* po = reinterpret_cast<const float*>(a.ws + a.layout.part_o);
+  auto piece = [&](int i) { return (2 * (int64_t)(first + i) + (i == 0)) * a.layout.rows + row; };
+  float top = -INFINITY;
+  for (int i = lane; i < parts; i += 32) top = fmaxf(top, __ldcg(ml + piece(i)).x);
+  top = warp_max(top);
+  const float ref = top == -INFINITY ? 0.f : top;
+  float sum = 0.f, acc[kD] = {};
+#pragma unroll 4
+  for (int i = 0; i < parts; ++i) {
+    const float2 y = __ldcg(ml + piece(i));
+    const float f = ex2_approx(y.x - ref);
+    sum = fmaf(y.y, f, sum);
+#pragma unroll
+    for (int e = 0; e < kD; e += 2) {
+      const float2 x = __ldcg(reinterpret_cast<const float2*>(po + piece(i) * D + lane * kD + e));
+      acc[e] = fmaf(x.x, f, acc[e]);
+      acc[e + 1] = fmaf(x.y, f, acc[e + 1]);
+    }
+  }
+  store_row<D>(a, w, head, row, acc, sum);
+}
+
+// Row r of the eight warps' results in the join buffer, by a warp: D / 32 consecutive dims per lane.
+template <int D, int E>
+__device__ __forceinline__ void join_warps(const float* join, const float2* join_ml, int r, float (&acc)[D / 32], float& top,
+                                           float& sum) {
+  constexpr int kD = D / 32, kPad = D + 4;
+  const int lane = threadIdx.x & 31;
+  float2 y[kWarps];
+  top = -INFINITY;
+  sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < kD; ++e) acc[e] = 0.f;
+#pragma unroll
+  for (int v = 0; v < kWarps; ++v) {
+    y[v] = join_ml[v * 8 + r];
+    top = fmaxf(top, y[v].x);
+  }
+  const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+  for (int v = 0; v < kWarps; ++v) {
+    const float f = ex2_approx(y[v].x - ref);
+    sum = fmaf(y[v].y, f, sum);
+#pragma unroll
+    for (int e = 0; e < kD; e += 2) {
+      const int dim = lane * kD + e;  // held by group g in its tile mt
+      const int g = E == 1 ? dim / (D / 8) : dim / 8 % 8, mt = E == 1 ? dim % (D / 8) / 2 : dim / 64 * 4 + dim % 8 / 2;
+      const float2 z = *reinterpret_cast<const float2*>(join + (v * 8 + r) * kPad + mt * 16 + 2 * g);
+      acc[e] = fmaf(z.x, f, acc[e]);
+      acc[e + 1] = fmaf(z.y, f, acc[e + 1]);
+    }
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void store_piece(const SpanArgs& a, int64_t slot, const float (&acc)[D / 32], float top, float sum) {
+  const int lane = threadIdx.x & 31;
+  float* dst = reinterpret_cast<float*>(a.ws + a.layout.part_o) + slot * D + lane * (D / 32);
+#pragma unroll
+  for (int e = 0; e < D / 32; e += 2) *reinterpret_cast<float2*>(dst + e) = make_float2(acc[e], acc[e + 1]);
+  if (lane == 0) reinterpret_cast<float2*>(a.ws + a.layout.part_ml)[slot] = make_float2(top, sum);
+}
+
 template <int D, int E, int NT>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
     span_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -170,8 +260,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
       mbar_init(&bars->full[s], 1);
       mbar_init(&bars->empty[s], L::kStageWarps);
     }
-    mbar_init(&bars->written, 1);
-    bars->abort = bars->never = bars->last = 0;
+    for (int u = 0; u < 2; ++u) {
+      mbar_init(&bars->q_full[u], 1);
+      mbar_init(&bars->q_empty[u], kWarps);
+    }
+    mbar_init(&bars->join_full, kWarps);
+    mbar_init(&bars->join_empty, 1);
+    mbar_init(&bars->join_empty8, kWarps);
+    bars->abort = bars->never = 0;
     fence_mbar_init();
   }
   if (threadIdx.x == kLoadWarp * 32) {
@@ -185,6 +281,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
   pdl_wait();
   pdl_trigger();
   if (reinterpret_cast<const SpanHeader*>(a.ws)->status != ST_OK) return;
+  float* join = reinterpret_cast<float*>(smem + L::kJoin);
+  float2* join_ml = reinterpret_cast<float2*>(smem + L::kMl);
   auto timeout = [&]() {
     atomicCAS(&reinterpret_cast<SpanHeader*>(a.ws)->status, 0, ST_TIMEOUT);
     set_status(a.dev_status, ST_TIMEOUT);
@@ -195,13 +293,23 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
     // -------------------------------------------------------------------- page loads
     constexpr int kBoxes = 2 * L::kSubs * L::kStageWarps;  // 16-position boxes of a stage: one per lane
     const int is_v = lane / (kBoxes / 2), sub = lane / L::kStageWarps % L::kSubs, grp = lane % L::kStageWarps;
-    uint32_t seq = 0;
-    bool ok = true, wrote = !p.write;
+    uint32_t seq = 0, n = 0;
+    bool ok = true;
     for (SpanWalk w(a, blockIdx.x); ok && w.live(); w.next()) {
-      const int p0 = w.item.p0, p1 = p0 + w.item.tokens - 1;
+      const int p0 = w.item.p0, p1 = p0 + w.item.tokens - 1, rows = w.item.tokens * a.group;
       const SpanTiles tiles(p0, p1, a.window, a.sinks);
       const int32_t* row = a.table + (int64_t)w.item.question * a.max_blocks;
       int ids = 0;
+      if (n >= 2) ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_empty[n & 1], (n / 2 - 1) & 1, abort_flag, budget));
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(&bars->q_full[n & 1], rows * 2 * D);
+      __syncwarp();
+      if (lane < rows)
+        bulk_load(smem + L::kQ + (n & 1) * L::kQBytes + lane * L::kQPitch,
+                  static_cast<const __nv_bfloat16*>(a.q) +
+                      ((int64_t)(w.item.row0 + lane / a.group) * a.h_q + w.head * a.group + lane % a.group) * D,
+                  2 * D, &bars->q_full[n & 1]);
+      ++n;
       for (int j = w.j0; ok && j < w.j1; ++j) {
         if ((j - w.j0) % 32 == 0) ids = j + lane < w.j1 ? row[tiles.at(j + lane)] : 0;  // 32 pages ahead
         const int block = __shfl_sync(0xffffffffu, ids, (j - w.j0) % 32);
@@ -211,11 +319,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
           const int s = seq % L::kStages;
           if (seq >= L::kStages)
             ok = __all_sync(0xffffffffu, mbar_wait(&bars->empty[s], (seq / L::kStages - 1) & 1, abort_flag, budget));
-          if (ok && !wrote && u0 + L::kKeys > p0) {  // new rows among them: wait until they are written
-            ok = __all_sync(0xffffffffu, mbar_wait(&bars->written, 0, abort_flag, budget));
-            asm volatile("fence.proxy.async;" ::: "memory");
-            wrote = true;
-          }
           if (!ok) break;
           const bool mine = lane < kBoxes && group_seen(a, u0 + grp * 16, p0, p1);
           const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
@@ -233,60 +336,42 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
       }
     }
     if (!ok && lane == 0) timeout();
-    if (*abort_flag)  // every copy issued lands before the CTA leaves
+    if (*abort_flag) {  // every copy issued lands before the CTA leaves
+      for (uint32_t u = n < 2 ? 0 : n - 2; u < n; ++u) mbar_wait(&bars->q_full[u & 1], (u / 2) & 1, never, kDrainBudget);
       for (uint32_t q = seq < L::kStages ? 0 : seq - L::kStages; q < seq; ++q)
         mbar_wait(&bars->full[q % L::kStages], (q / L::kStages) & 1, never, kDrainBudget);
-  } else if (warp == kWriteWarp) {
-    // -------------------------------------------------------------------- new rows into the cache
-    if (!p.write) return;
-    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;  // lanes of a bf16 row
-    const int sub = lane % kLanes;
-    for (SpanWalk w(a, blockIdx.x); w.live(); w.next()) {
-      const int p0 = w.item.p0;
-      const SpanTiles tiles(p0, p0 + w.item.tokens - 1, a.window, a.sinks);
-      const int32_t* row = a.table + (int64_t)w.item.question * a.max_blocks;
-      for (int x0 = 0; x0 < 2 * w.item.tokens; x0 += kAtOnce) {
-        const int x = x0 + lane / kLanes, token = x >> 1, pos = p0 + token;
-        const bool is_v = x & 1;
-        // its tile's place on the work line: chunk positions lie in the tiles from lo on, or are sinks'
-        const int page = pos / kPage, j = page < tiles.ns ? page : tiles.ns + page - tiles.lo;
-        const bool mine = token < w.item.tokens && j >= w.j0 && j < w.j1;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (mine)
-          v = reinterpret_cast<const uint4*>(is_v ? a.v : a.k)[((int64_t)(w.item.row0 + token) * a.h_kv + w.head) * kLanes + sub];
-        const int64_t cell = mine ? ((int64_t)row[page] * a.h_kv + w.head) * kPage + pos % kPage : 0;
-        if (E == 2) {
-          if (mine) static_cast<uint4*>(is_v ? a.pool_v : a.pool_k)[cell * kLanes + sub] = v;
-        } else {
-          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-          float f[8], top = 0.f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            f[e] = __uint_as_float(e & 1 ? u[e / 2] & 0xffff0000u : u[e / 2] << 16);
-            top = nan_max(top, fabsf(f[e]));
-          }
-#pragma unroll
-          for (int o = kLanes / 2; o > 0; o >>= 1) top = nan_max(top, __shfl_xor_sync(0xffffffffu, top, o));
-          const float scale = top < INFINITY ? __fdiv_rn(top, 448.f) : __int_as_float(0x7fffffff);
-          uint32_t c[2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float y[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = scale == 0.f ? 0.f : __fdiv_rn(f[4 * i + e], scale);
-            c[i] = e4m3x2(y[0], y[1]) | e4m3x2(y[2], y[3]) << 16;
-          }
-          if (mine) {
-            *reinterpret_cast<uint2*>(static_cast<unsigned char*>(is_v ? a.pool_v : a.pool_k) + cell * D + sub * 8) =
-                make_uint2(c[0], c[1]);
-            if (sub == 0) (is_v ? a.scale_v : a.scale_k)[cell] = scale;
-          }
+    }
+  } else if (warp == kJoinWarp) {
+    // -------------------------------------------------------------------- joins, of all units but the last
+    uint32_t joins = 0;
+    bool ok = true;
+    for (SpanWalk w(a, blockIdx.x); ok && w.live() && !w.ends(); w.next()) {
+      const int rows = w.item.tokens * a.group;
+      const bool whole = w.whole();
+      const int64_t slot = w.slot(blockIdx.x) * a.layout.rows;
+      for (int nt = 0; nt < NT; ++nt, ++joins) {
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars->join_full, joins & 1, abort_flag, budget)))) break;
+#pragma unroll 2
+        for (int r = 0; r < 8; ++r) {
+          if (nt * 8 + r >= rows) break;
+          float acc[D / 32], top, sum;
+          join_warps<D, E>(join, join_ml, r, acc, top, sum);
+          if (whole) store_row<D>(a, w.item, w.head, nt * 8 + r, acc, sum);
+          else store_piece<D>(a, slot + nt * 8 + r, acc, top, sum);
         }
+        mbar_arrive_warp(&bars->join_empty);
+      }
+      if (ok && !whole) {  // the warp that finishes a row's last piece joins them all, in their order
+        const int first = w.first(), parts = w.parts();
+        int32_t* arrived = reinterpret_cast<int32_t*>(a.ws + a.layout.arrived) + first * kSpanRows;
+        __threadfence();
+        __syncwarp();
+        uint32_t all = __ballot_sync(0xffffffffu, lane < rows && atomicAdd(arrived + min(lane, kSpanRows - 1), lane < rows) == parts - 1);
+        __threadfence();
+        for (; all; all &= all - 1) join_pieces<D>(a, w.item, w.head, __ffs(all) - 1, first, parts);
       }
     }
-    __threadfence();
-    asm volatile("fence.proxy.async;" ::: "memory");  // before the copies of these pages, which the other warp issues
-    mbar_arrive_warp(&bars->written);
+    if (!ok && lane == 0) timeout();
   } else {
     // -------------------------------------------------------------------- attention
     span_zero_gaps(a, kWarps * 32);
@@ -295,37 +380,90 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
     constexpr int kTiles = D / 16;             // 16-dim tiles of O^T
     const int g = lane >> 2, c = lane & 3;
     const uint32_t smem0 = smem_u32(smem);
-    float* join = reinterpret_cast<float*>(smem + L::kJoin);
-    float2* join_ml = reinterpret_cast<float2*>(smem + L::kMl);
     // swizzled address of 16-byte chunk ch of row r
     auto at = [&](uint32_t tile, int r, int ch) {
       if (L::kPitch == 128)
         return tile + (ch >> 3) * (L::kKeys * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
       return tile + r * 64 + ((ch ^ (r >> 1 & 3)) << 4);
     };
-    uint32_t seq = 0;
+    // a new token's K and V rows: into row r of the loaded tiles and into the cache, a lane per 1/32
+    auto put_rows = [&](int64_t src, int64_t cell, uint32_t tk, uint32_t tv, int r) {
+      constexpr int kN = D / 32;  // elements of a lane
+      uint32_t in[2][kN / 2];
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const uint32_t* from = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(v ? a.v : a.k) + src) + lane * (kN / 2);
+        if (kN == 4) {
+          const uint2 x = *reinterpret_cast<const uint2*>(from);
+          in[v][0] = x.x;
+          in[v][kN / 2 - 1] = x.y;
+        } else {
+          in[v][0] = *from;
+        }
+      }
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const int at_byte = lane * kN * E;  // of the row
+        const uint32_t to = at(v ? tv : tk, r, at_byte / 16) + at_byte % 16;
+        unsigned char* dst = static_cast<unsigned char*>(v ? a.pool_v : a.pool_k) + cell * L::kRow + at_byte;
+        if (E == 2) {
+#pragma unroll
+          for (int e = 0; e < kN / 2; ++e) {
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + 4 * e), "r"(in[v][e]) : "memory");
+            reinterpret_cast<uint32_t*>(dst)[e] = in[v][e];
+          }
+        } else {
+          float f[kN], top = 0.f;
+#pragma unroll
+          for (int e = 0; e < kN; ++e) {
+            f[e] = __uint_as_float(e & 1 ? in[v][e / 2] & 0xffff0000u : in[v][e / 2] << 16);
+            top = nan_max(top, fabsf(f[e]));
+          }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) top = nan_max(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const float scale = top < INFINITY ? __fdiv_rn(top, 448.f) : __int_as_float(0x7fffffff);
+#pragma unroll
+          for (int e = 0; e < kN; ++e) f[e] = scale == 0.f ? 0.f : __fdiv_rn(f[e], scale);
+          const uint32_t lo = e4m3x2(f[0], f[1]);
+          if (kN == 4) {
+            const uint32_t code = lo | e4m3x2(f[kN - 2], f[kN - 1]) << 16;
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(code) : "memory");
+            *reinterpret_cast<uint32_t*>(dst) = code;
+          } else {
+            asm volatile("st.shared.b16 [%0], %1;" ::"r"(to), "h"((uint16_t)lo) : "memory");
+            *reinterpret_cast<uint16_t*>(dst) = (uint16_t)lo;
+          }
+          if (lane == 0) {
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(tk + 2 * L::kTile + (v * L::kKeys + r) * 4), "f"(scale) : "memory");
+            (v ? a.scale_v : a.scale_k)[cell] = scale;
+          }
+        }
+      }
+    };
+    uint32_t seq = 0, n = 0, joins = 0;
     bool ok = true;
-    for (SpanWalk w(a, blockIdx.x); w.live(); w.next()) {
+    for (SpanWalk w(a, blockIdx.x); ok && w.live(); w.next()) {
       const int p0 = w.item.p0, p1 = p0 + w.item.tokens - 1, rows = w.item.tokens * a.group;
       const SpanTiles tiles(p0, p1, a.window, a.sinks);
       // q as the B operand: row nt * 8 + g, the dims of this lane's chunks
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_full[n & 1], (n / 2) & 1, abort_flag, budget)))) break;
       uint32_t q[NT][kChunks * kSteps][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int r = nt * 8 + g;
-        const uint32_t* src = reinterpret_cast<const uint32_t*>(
-            static_cast<const __nv_bfloat16*>(a.q) +
-            ((int64_t)(w.item.row0 + (r < rows ? r / a.group : 0)) * a.h_q + w.head * a.group + (r < rows ? r % a.group : 0)) * D);
+        const uint32_t src = smem0 + L::kQ + (n & 1) * L::kQBytes + r * L::kQPitch;
 #pragma unroll
         for (int i = 0; i < kChunks; ++i)
 #pragma unroll
           for (int h = 0; h < kSteps; ++h) {
             const int dim = (E == 2 ? 8 : 16) * (c + 4 * i) + 4 * h;
-            const uint2 x = r < rows ? *reinterpret_cast<const uint2*>(src + dim / 2) : make_uint2(0u, 0u);
+            const uint2 x = r < rows ? lds64(src + 2 * dim) : make_uint2(0u, 0u);
             q[nt][i * kSteps + h][0] = x.x;
             q[nt][i * kSteps + h][1] = x.y;
           }
       }
+      mbar_arrive_warp(&bars->q_empty[n & 1]);
+      ++n;
       // fp16 has no exponents to spare: a row of q is scaled by a power of two that puts its largest element
       // in [2^14, 2^15) -- exact down to 2^-29 of it, and off by at most 2^-40 of it below -- and the
       // scores by its inverse
@@ -371,18 +509,28 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
 #pragma unroll
           for (int x = 0; x < 4; ++x) o[mt][nt][x] = 0.f;
 
-      for (int j = w.j0; j < w.j1; ++j)
-      for (int half = 0; half < L::kHalves; ++half) {
+      for (int x = w.j0 * L::kHalves; x < w.j1 * L::kHalves; ++x) {
+        const int j = x / L::kHalves, half = x % L::kHalves;
         const int h0 = tiles.at(j) * kPage + half * L::kKeys;
         if (L::kHalves > 1 && !group_seen<L::kKeys>(a, h0, p0, p1)) continue;
         const uint32_t here = seq++;
         if (L::kHalves > 1 && (here & 1) != warp / L::kStageWarps) continue;  // the other warps' turn
         const int s = here % L::kStages;
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->full[s], (here / L::kStages) & 1, abort_flag, budget));
-        if (!ok) continue;
+        if (!ok) break;
         const int k0 = warp % L::kStageWarps * 16, u0 = h0 + k0;  // this warp's 16 positions of the stage
         if (group_seen(a, u0, p0, p1)) {
           const uint32_t tk = smem0 + s * L::kStageBytes, tv = tk + L::kTile;
+          if (p.write && u0 + 15 >= p0) {  // positions of the chunk among them
+#pragma unroll 1
+            for (int t = max(0, u0 - p0); t < w.item.tokens && p0 + t < u0 + 16; ++t) {
+              const int64_t src = ((int64_t)(w.item.row0 + t) * a.h_kv + w.head) * D, cell =
+                  ((int64_t)a.table[(int64_t)w.item.question * a.max_blocks + tiles.at(j)] * a.h_kv + w.head) * kPage + (p0 + t) % kPage;
+              put_rows(src, cell, tk, tv, k0 + p0 + t - u0);
+            }
+            __syncwarp();
+            fence_proxy_async_smem();  // before the slot's next load
+          }
           const int r0 = k0 + perm(g);  // slots g and g + 8
           float z[NT][4];
 #pragma unroll
@@ -597,11 +745,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
         mbar_arrive_warp(&bars->empty[s]);
       }
 
-      // ------------------------------------------------------------------ the eight warps' results, joined
-      const bool whole = w.whole();
-      const int64_t slot = w.slot(blockIdx.x) * a.layout.rows;
+      // leave the results to the joining warp, 8 rows at a time
+      const bool ends = w.ends();
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+      for (int nt = 0; nt < NT; ++nt, ++joins) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           float t = l[nt][x];
@@ -610,7 +757,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
           t += __shfl_xor_sync(0xffffffffu, t, 16);
           l[nt][x] = t;
         }
-        asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");  // the buffers are free
+        if (ok && ends && nt > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars->join_empty8, 0, abort_flag, budget));
+        else if (ok && joins > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars->join_empty, (joins - 1) & 1, abort_flag, budget));
+        if (!ok) break;
         float* mine = join + warp * 8 * L::kPad;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -622,82 +771,30 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
                 E == 1 ? make_float2(o[mt][nt][x] * unit, o[mt][nt][2 + x] * unit)
                        : make_float2(o[mt][nt][x], o[mt][nt][2 + x]);
         }
-        asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
-        // a warp per row, D / 32 consecutive dims per lane
+        mbar_arrive_warp(&bars->join_full);
+        if (!ends) continue;
+        // The part's last unit: nothing else to do here, so a warp per row, without the joining warp
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars->join_full, joins & 1, abort_flag, budget)))) break;
         const int row = nt * 8 + warp;
-        if (row < rows && ok) {
-          constexpr int kD = D / 32;
-          float top = -INFINITY, sum = 0.f, acc[kD] = {};
-#pragma unroll
-          for (int v = 0; v < kWarps; ++v) top = fmaxf(top, join_ml[v * 8 + warp].x);
-          const float ref = top == -INFINITY ? 0.f : top;
-#pragma unroll
-          for (int v = 0; v < kWarps; ++v) {
-            const float2 y = join_ml[v * 8 + warp];
-            const float f = ex2_approx(y.x - ref);
-            sum = fmaf(y.y, f, sum);
-#pragma unroll
-            for (int e = 0; e < kD; e += 2) {
-              const int dim = lane * kD + e;  // held by group gg in its tile mt
-              const int gg = E == 1 ? dim / (D / 8) : dim / 8 % 8, mt = E == 1 ? dim % (D / 8) / 2 : dim / 64 * 4 + dim % 8 / 2;
-              const float2 z = *reinterpret_cast<const float2*>(join + (v * 8 + warp) * L::kPad + mt * 16 + 2 * gg);
-              acc[e] = fmaf(z.x, f, acc[e]);
-              acc[e + 1] = fmaf(z.y, f, acc[e + 1]);
-            }
-          }
-          if (whole) {
-            const float inv = 1.f / sum;
-            uint32_t* dst = reinterpret_cast<uint32_t*>(
-                static_cast<__nv_bfloat16*>(a.out) +
-                ((int64_t)(w.item.row0 + row / a.group) * a.h_q + w.head * a.group + row % a.group) * D + lane * kD);
-#pragma unroll
-            for (int e = 0; e < kD; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+        if (row < rows) {
+          float acc[D / 32], top, sum;
+          join_warps<D, E>(join, join_ml, warp, acc, top, sum);
+          if (w.whole()) {
+            store_row<D>(a, w.item, w.head, row, acc, sum);
           } else {
-            float* dst = reinterpret_cast<float*>(a.ws + a.layout.part_o) + (slot + row) * D + lane * kD;
-#pragma unroll
-            for (int e = 0; e < kD; ++e) dst[e] = acc[e];
-            if (lane == 0) reinterpret_cast<float2*>(a.ws + a.layout.part_ml)[slot + row] = make_float2(top, sum);
-          }
-        }
-      }
-      if (!whole) {
-        // The CTA that finishes the last piece joins them all, in their order.
-        __threadfence();
-        asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
-        if (threadIdx.x == 0) {
-          int32_t* arrived = reinterpret_cast<int32_t*>(a.ws + a.layout.arrived) + 2 * w.first();
-          bars->last = ok && atomicAdd(arrived, 1) == w.parts() - 1;
-          __threadfence();
-        }
-        asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
-        if (bars->last) {
-          constexpr int kD = D / 32;
-          const float2* ml = reinterpret_cast<const float2*>(a.ws + a.layout.part_ml);
-          const float* po = reinterpret_cast<const float*>(a.ws + a.layout.part_o);
-          const int first = w.first(), parts = w.parts();
-          for (int row = warp; row < rows; row += kWarps) {
-            auto piece = [&](int i) { return (2 * (int64_t)(first + i) + (i == 0)) * a.layout.rows + row; };
-            float top = -INFINITY;
-            for (int i = lane; i < parts; i += 32) top = fmaxf(top, __ldcg(ml + piece(i)).x);
-            top = warp_max(top);
-            const float ref = top == -INFINITY ? 0.f : top;
-            float sum = 0.f, acc[kD] = {};
-#pragma unroll 4
-            for (int i = 0; i < parts; ++i) {
-              const float2 y = __ldcg(ml + piece(i));
-              const float f = ex2_approx(y.x - ref);
-              sum = fmaf(y.y, f, sum);
-#pragma unroll
-              for (int e = 0; e < kD; ++e) acc[e] = fmaf(__ldcg(po + piece(i) * D + lane * kD + e), f, acc[e]);
+            store_piece<D>(a, w.slot(blockIdx.x) * a.layout.rows + row, acc, top, sum);
+            __threadfence();
+            __syncwarp();
+            int before = 0;
+            if (lane == 0)
+              before = atomicAdd(reinterpret_cast<int32_t*>(a.ws + a.layout.arrived) + w.first() * kSpanRows + row, 1);
+            if (__shfl_sync(0xffffffffu, before, 0) == w.parts() - 1) {
+              __threadfence();
+              join_pieces<D>(a, w.item, w.head, row, w.first(), w.parts());
             }
-            const float inv = 1.f / sum;
-            uint32_t* dst = reinterpret_cast<uint32_t*>(
-                static_cast<__nv_bfloat16*>(a.out) +
-                ((int64_t)(w.item.row0 + row / a.group) * a.h_q + w.head * a.group + row % a.group) * D + lane * kD);
-#pragma unroll
-            for (int e = 0; e < kD; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
           }
         }
+        if (NT > 1) mbar_arrive_warp(&bars->join_empty8);
       }
     }
     if (!ok && lane == 0) timeout();
