@@ -29,6 +29,7 @@ struct SpanHeader {
   int32_t n_items;
   int32_t n_gaps;
   int32_t n_new;  // tokens in questions
+  int32_t n_joins;
 };
 
 struct alignas(16) SpanItem {
@@ -57,7 +58,8 @@ struct SpanLayout {
   size_t cuts;     // SpanCut[kSpanMaxCtas + 1]
   size_t arrived;  // int32[kSpanMaxCtas][kSpanRows] finished pieces of the unit that begins in part c and goes on
   size_t part_ml;  // float2[2 * kSpanMaxCtas][rows] running maximum (log2 units) and sum
-  size_t part_o;   // float[2 * kSpanMaxCtas][rows][d]
+  size_t part_o;   // float[2 * kSpanMaxCtas][d / 8][rows][8] (few rows: [rows][d])
+  size_t joins;    // int32[kSpanMaxCtas] cuts of the units that the merge kernel joins
   size_t total;
   int32_t rows;    // rows of a partial result
   int64_t max_items;
@@ -84,6 +86,7 @@ inline SpanLayout span_layout(int32_t n, int32_t T, int32_t group, int32_t d) {
   L.arrived = take(sizeof(int32_t) * kSpanRows * kSpanMaxCtas);
   L.part_ml = take(sizeof(float2) * 2 * kSpanMaxCtas * (size_t)L.rows);
   L.part_o = take(sizeof(float) * 2 * kSpanMaxCtas * (size_t)L.rows * d);
+  L.joins = take(sizeof(int32_t) * kSpanMaxCtas);
   L.total = off;
   return L;
 }
@@ -113,6 +116,7 @@ struct SpanArgs {
   int32_t tile_tokens;    // floor(M / group)
   int32_t item_tiles;     // row tiles of an item
   int32_t ctas;           // parts of the work line
+  int32_t join_from;      // units of so many pieces or more are joined by the merge kernel
   int32_t unit_cost;      // what a unit costs beside its key tiles, in key tiles
   int32_t attend;         // 0: cache write or read only (no items)
   char* ws;
@@ -192,6 +196,11 @@ struct SpanWalk {
     j1 = last();
   }
 };
+
+// Place of elements 8 c .. 8 c + 7 of a row in the partial results (neighbouring rows side by side).
+__device__ __forceinline__ int64_t span_part(const SpanArgs& a, int64_t slot, int c, int row) {
+  return ((slot * (a.d / 8) + c) * a.layout.rows + row) * 8;
+}
 
 // Is position u visible to the token at position p?
 __device__ __forceinline__ bool span_sees(int p, int u, int window, int sinks) {

@@ -93,6 +93,7 @@ kev_status span_attend(SpanArgs* a, bool write, cudaStream_t s) {
     const int ctas = rows <= 8 ? 2 * sms : sms;
     span_tiling(a, rows <= 8 ? 8 : 16, 1, ctas < kSpanMaxCtas ? ctas : kSpanMaxCtas);
     a->unit_cost = 1;
+    a->join_from = kSpanMaxCtas + 1;  // none: the kernel joins its own
     cudaError_t e = launch_span_plan(*a, s);
     if (e == cudaSuccess) e = launch_span_rows(*a, write, s);
     return from_cuda(e);
@@ -103,6 +104,7 @@ kev_status span_attend(SpanArgs* a, bool write, cudaStream_t s) {
   // measured: a unit of two row tiles costs 1.8 us a key tile and 3.3 us beside them (loading q, the
   // masks of its first and last tiles, the epilogue)
   a->unit_cost = tc ? 2 : 0;
+  a->join_from = tc ? 3 : 2;
   cudaError_t e = launch_span_plan(*a, s);
   if (e == cudaSuccess && write) e = launch_span_write(*a, sms, s);
   if (e == cudaSuccess) e = tc ? launch_span_tc(*a, s) : launch_span_simt(*a, s);

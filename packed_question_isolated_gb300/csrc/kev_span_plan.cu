@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(SpanArgs a) {
   extern __shared__ unsigned long long dyn[];  // intervals, prefixes; sort keys, bit map of used blocks or tile counts
   __shared__ Scan s_scan[33];
   __shared__ long long s_sum[33];
-  __shared__ int s_err;
+  __shared__ int s_err, s_joins;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, n = a.n;
   kev_interval* iv = reinterpret_cast<kev_interval*>(dyn);
   int* pre = reinterpret_cast<int*>(iv + n);
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(SpanArgs a) {
   unsigned long long* area = dyn + (16 * (size_t)n + 8 + 7) / 8;
   unsigned* used = reinterpret_cast<unsigned*>(area);
   const int words = a.pool_elem ? (a.n_blocks + 31) / 32 : 0;
-  if (t == 0) s_err = 0;
+  if (t == 0) s_err = s_joins = 0;
   for (int i = t; i < words; i += kThreads) used[i] = 0u;
   pdl_wait();
   pdl_trigger();
@@ -288,6 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(SpanArgs a) {
   // and then its tiles; a cut in the fixed cost moves to the unit's beginning
   SpanCut* cuts = reinterpret_cast<SpanCut*>(a.ws + a.layout.cuts);
   int32_t* arrived = reinterpret_cast<int32_t*>(a.ws + a.layout.arrived);
+  int32_t* joins = reinterpret_cast<int32_t*>(a.ws + a.layout.joins);
   for (int x = t; x < a.ctas * kSpanRows; x += kThreads) arrived[x] = 0;
   const long long total = run;
   const int parts = total < a.ctas ? (int)total : a.ctas;
@@ -315,10 +316,13 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(SpanArgs a) {
         const long long begin = w - cut.tile, end = w - at + size;  // its tiles
         cut.first = part_of(begin);
         cut.parts = part_of(end - 1) - cut.first + 1;
+        if (cut.first == c - 1 && cut.parts >= a.join_from) joins[atomicAdd(&s_joins, 1)] = c;
       }
     }
     cuts[c] = cut;
   }
+  __syncthreads();
+  if (t == 0) hdr->n_joins = s_joins;
 }
 
 }  // namespace

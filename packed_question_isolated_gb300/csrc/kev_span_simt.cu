@@ -166,9 +166,10 @@ __global__ void __launch_bounds__(kThreads, 2) span_simt_kernel(SpanArgs a) {
 #pragma unroll
         for (int e = 0; e < kDims; ++e) static_cast<float*>(a.out)[at + e] = o[r][e] * inv;
       } else {
-        const int64_t slot = walk.slot(blockIdx.x) * a.layout.rows + row;
-        float* dst = reinterpret_cast<float*>(a.ws + a.layout.part_o) + slot * D + lane * kV;
-        if (lane == 0) reinterpret_cast<float2*>(a.ws + a.layout.part_ml)[slot] = make_float2(m[r], sum);
+        const int64_t slot = walk.slot(blockIdx.x);
+        const int dim = lane * kV;
+        float* dst = reinterpret_cast<float*>(a.ws + a.layout.part_o) + span_part(a, slot, dim / 8, row) + dim % 8;
+        if (lane == 0) reinterpret_cast<float2*>(a.ws + a.layout.part_ml)[slot * a.layout.rows + row] = make_float2(m[r], sum);
 #pragma unroll
         for (int e = 0; e < kDims; ++e) dst[e] = o[r][e];
       }
@@ -176,49 +177,56 @@ __global__ void __launch_bounds__(kThreads, 2) span_simt_kernel(SpanArgs a) {
   }
 }
 
-// Joins the pieces of the units that a cut goes through: a warp per row, weights exp2(m_i - max m).
+// Joins the pieces of the units that the plan lists: a thread per row and 8 dims, weights exp2(m_i - max m).
 template <typename T, int D>
 __global__ void __launch_bounds__(256) span_merge_kernel(SpanArgs a) {
   pdl_wait();
   pdl_trigger();
   const SpanHeader* h = reinterpret_cast<const SpanHeader*>(a.ws);
   if (h->status != ST_OK) return;
-  const SpanItem* items = reinterpret_cast<const SpanItem*>(a.ws + a.layout.items);
   const SpanCut* cuts = reinterpret_cast<const SpanCut*>(a.ws + a.layout.cuts);
+  const int32_t* joins = reinterpret_cast<const int32_t*>(a.ws + a.layout.joins);
   const float2* ml = reinterpret_cast<const float2*>(a.ws + a.layout.part_ml);
   const float* po = reinterpret_cast<const float*>(a.ws + a.layout.part_o);
-  const int lane = threadIdx.x & 31;
-  constexpr int kDims = D / 32;
-  const int unit_rows = a.tile_rows * a.item_tiles;
-  const int64_t todo = (int64_t)(a.ctas - 1) * unit_rows;
-  for (int64_t x = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); x < todo; x += (int64_t)gridDim.x * 8) {
-    const int c = 1 + (int)(x / unit_rows), row = (int)(x % unit_rows);
-    const SpanCut cut = cuts[c];
-    if (cut.tile == 0 || cut.first != c - 1) continue;
-    const SpanItem w = items[cut.item];
+  const int per = a.layout.rows * (D / 8);
+  const int64_t todo = (int64_t)h->n_joins * per;
+  for (int64_t x = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; x < todo; x += (int64_t)gridDim.x * blockDim.x) {
+    const SpanCut& cut = cuts[joins[x / per]];
+    const int row = (int)(x % per) % a.layout.rows, c = (int)(x % per) / a.layout.rows;
     const int rr = row % a.tile_rows, token = row / a.tile_rows * a.tile_tokens + rr / a.group;
-    if (rr >= a.tile_tokens * a.group || token >= w.tokens) continue;
-    // part i's piece: slot 1 of the part the unit begins in, slot 0 of the later ones
-    auto slot = [&](int i) { return (2 * (int64_t)(cut.first + i) + (i == 0)) * a.layout.rows + row; };
+    if (rr >= a.tile_tokens * a.group || token >= cut.record.tokens) continue;
+    // piece i: slot 1 of the part the unit begins in, slot 0 of the later ones
+    auto slot = [&](int i) { return 2 * (int64_t)(cut.first + i) + (i == 0); };
     float top = -INFINITY;
-    for (int i = lane; i < cut.parts; i += 32) top = fmaxf(top, ml[slot(i)].x);
-    top = warp_max(top);
+#pragma unroll 4
+    for (int i = 0; i < cut.parts; ++i) top = fmaxf(top, ml[slot(i) * a.layout.rows + row].x);
     const float base = top == -INFINITY ? 0.f : top;
-    float l = 0.f, o[kDims] = {};
+    float l = 0.f, o[8] = {};
+#pragma unroll 4
     for (int i = 0; i < cut.parts; ++i) {
-      const float2 p = ml[slot(i)];
-      const float wgt = exp2f(p.x - base);
+      const float2 p = ml[slot(i) * a.layout.rows + row];
+      const float4* src = reinterpret_cast<const float4*>(po + span_part(a, slot(i), c, row));
+      const float4 u = src[0], v = src[1];
+      const float wgt = exp2f(p.x - base), y[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
       l = fmaf(p.y, wgt, l);
-      const float* src = po + slot(i) * D + lane * kDims;
 #pragma unroll
-      for (int e = 0; e < kDims; ++e) o[e] = fmaf(src[e], wgt, o[e]);
+      for (int e = 0; e < 8; ++e) o[e] = fmaf(y[e], wgt, o[e]);
     }
     const float inv = 1.f / l;
     T* dst = static_cast<T*>(a.out) +
-             ((int64_t)(w.row0 + token) * a.h_q + cut.head * a.group + rr % a.group) * D +
-             lane * kDims;
+             ((int64_t)(cut.record.row0 + token) * a.h_q + cut.head * a.group + rr % a.group) * D + c * 8;
+    if (sizeof(T) == 2) {
+      uint32_t y[4];
 #pragma unroll
-    for (int e = 0; e < kDims; ++e) dst[e] = from_f32<T>(o[e] * inv);
+      for (int e = 0; e < 4; ++e) {
+        const __nv_bfloat162 z = __floats2bfloat162_rn(o[2 * e] * inv, o[2 * e + 1] * inv);
+        y[e] = *reinterpret_cast<const uint32_t*>(&z);
+      }
+      *reinterpret_cast<uint4*>(dst) = make_uint4(y[0], y[1], y[2], y[3]);
+    } else {
+      reinterpret_cast<float4*>(dst)[0] = make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+      reinterpret_cast<float4*>(dst)[1] = make_float4(o[4] * inv, o[5] * inv, o[6] * inv, o[7] * inv);
+    }
   }
 }
 
@@ -239,7 +247,7 @@ cudaError_t launch_span_simt(const SpanArgs& a, cudaStream_t s) {
 cudaError_t launch_span_merge(const SpanArgs& a, int num_sms, cudaStream_t s) {
   auto kern = a.elem == 2 ? (a.d == 64 ? span_merge_kernel<__nv_bfloat16, 64> : span_merge_kernel<__nv_bfloat16, 128>)
                           : (a.d == 64 ? span_merge_kernel<float, 64> : span_merge_kernel<float, 128>);
-  return launch_pdl(kern, dim3(8 * num_sms), dim3(256), 0, s, a);
+  return launch_pdl(kern, dim3(4 * num_sms), dim3(256), 0, s, a);
 }
 
 }  // namespace kev

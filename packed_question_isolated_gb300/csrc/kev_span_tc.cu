@@ -24,6 +24,7 @@
 // Bound by the tensor pipe beside the shared-memory reads of its operands for many rows, by HBM
 // for few.  Every wait is bounded, as in the other tensor-core kernels.
 #include <cuda.h>
+#include <cuda_fp16.h>
 
 #include "kev_sm100.cuh"
 #include "kev_span.cuh"
@@ -104,13 +105,16 @@ __device__ __forceinline__ bool edge_tile(const SpanArgs& a, int u0, int p0, int
   return !(u1 <= p0 && (a.window == 0 || p1 - u0 < a.window || u1 < a.sinks));
 }
 
-// four e4m3 codes as bf16 pairs, exactly: sign, 4 exponent and 3 mantissa bits at their places in
-// bf16, times 2^120 for the difference of the exponent biases (subnormals come out right too)
+// four e4m3 codes as bf16 pairs, exactly: by way of fp16 and fp32 (placing the bits takes four integer
+// operations per pair, on the pipe that the softmax needs most)
 __device__ __forceinline__ void e4m3_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  const uint32_t a = __byte_perm(w, 0u, 0x1404), b = __byte_perm(w, 0u, 0x3424);
-  const uint32_t x = ((a >> 4) & 0x07f007f0u) | (a & 0x80008000u), y = ((b >> 4) & 0x07f007f0u) | (b & 0x80008000u);
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(x), "r"(0x7b807b80u));
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(y), "r"(0x7b807b80u));
+  uint32_t a, b;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(a), "=r"(b)
+      : "r"(w));
+  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a)), y = __half22float2(*reinterpret_cast<const __half2*>(&b));
+  lo = pack_bf16x2(x.x, x.y);
+  hi = pack_bf16x2(y.x, y.y);
 }
 
 __device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
@@ -358,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // warps), and the epilogue of unit n - 4 has read it (its PV came before the V slots of n - 1)
         if (x == 0) *reinterpret_cast<volatile int*>(&bars->bad[(n + 4) & 7]) = 0;
         for (int j = w.j0; ok && j < w.j1; ++j, ++tiles_done) {
-          const bool edge = !Q8 && edge_tile(a, tiles.at(j) * kBN, p0, p1);
+          const bool edge = edge_tile(a, tiles.at(j) * kBN, p0, p1);
           for (int is_v = 0; is_v < 2; ++is_v, ++seq) {
             const int s = seq % L::kRing;
             unsigned char* tile = smem + L::kKv + s * L::kTile;
@@ -408,7 +412,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 4
               for (int e = 0; e < kBN * kGroups / 128; ++e) {
                 const int at = e * 128 + x, r = at / kGroups, g = at % kGroups;
-                const uint4 c = codes[at];
+                uint4 c = codes[at];
+                if (is_v && edge) {  // NaN codes of masked positions; rows that see one have its NaN scale in P
+                  uint32_t* u = reinterpret_cast<uint32_t*>(&c);
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) u[i] &= ~(((((u[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xffu);
+                }
                 uint32_t o[8];
                 e4m3_to_bf16(c.x, o[0], o[1]);
                 e4m3_to_bf16(c.y, o[2], o[3]);
@@ -505,6 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               const uint32_t seen = seen_bits(c, hi, lo, below);
+              if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;  // a warp's few tokens agree on most keys
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 if (!(seen >> e & 1u)) sr[c][e] = __float_as_uint(-INFINITY);
@@ -533,6 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               const uint32_t seen = Q8 && edge ? seen_bits(c, hi, lo, below) : 0xffffffffu;
+              const bool cut = Q8 && edge && __any_sync(0xffffffffu, seen != 0xffffffffu);
               uint32_t pk[16];
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
@@ -545,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const float2 xy = unpack2(mul2(f2pack(x, y), f2pack(v.x, v.y)));
                   x = xy.x;
                   y = xy.y;
-                  if (edge) {  // a masked row's scale may be anything
+                  if (cut) {  // a masked row's scale may be anything
                     if (!(seen >> (2 * e) & 1u)) x = 0.f;
                     if (!(seen >> (2 * e + 1) & 1u)) y = 0.f;
                   }
@@ -637,8 +648,55 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (!row_ok) continue;
-        if (w.whole()) {
+        if (!warp_ok) continue;
+        if (!w.whole()) {
+          // A piece of a unit.  Of two, the warp that comes second joins both, its own from registers and in
+          // the order of the pieces; more are left to the merge kernel.
+          const int first = w.first(), parts = w.parts(), row = t * kBM + r;
+          const bool mine_first = w.j0 == 0;
+          float* po = reinterpret_cast<float*>(a.ws + a.layout.part_o);
+          float2* ml = reinterpret_cast<float2*>(a.ws + a.layout.part_ml);
+          int32_t* arrived = reinterpret_cast<int32_t*>(a.ws + a.layout.arrived) + first * kSpanRows + warp;
+          int there = 0;
+          if (parts == 2) {
+            if (lane == 0) asm volatile("ld.acquire.gpu.b32 %0, [%1];" : "=r"(there) : "l"(arrived) : "memory");
+            there = __shfl_sync(0xffffffffu, there, 0);
+          }
+          if (!there) {
+            const int64_t slot = w.slot(blockIdx.x);
+            if (row_ok) {
+              ml[slot * a.layout.rows + row] = make_float2(m_run, l_run);
+#pragma unroll
+              for (int c = 0; c < D / 8; ++c) st_global_v8(po + span_part(a, slot, c, row), &o[c / 4][c % 4 * 8]);
+            }
+            if (parts == 2) {
+              __threadfence();
+              __syncwarp();
+              if (lane == 0) there = atomicAdd(arrived, 1);
+              there = __shfl_sync(0xffffffffu, there, 0);
+            }
+          }
+          if (!there) continue;
+          __threadfence();
+          if (row_ok) {
+            const int64_t slot = mine_first ? 2 * (int64_t)(first + 1) : 2 * (int64_t)first + 1;  // the other's
+            const float2 y = __ldcg(ml + slot * a.layout.rows + row);
+            const float top = fmaxf(m_run, y.x), ref = top == -INFINITY ? 0.f : top;
+            const float f = ex2_approx(m_run - ref), g = ex2_approx(y.x - ref);
+            l_run = mine_first ? fmaf(y.y, g, l_run * f) : fmaf(l_run, f, y.y * g);
+#pragma unroll
+            for (int c = 0; c < D / 4; ++c) {
+              const float4 z = __ldcg(reinterpret_cast<const float4*>(po + span_part(a, slot, c / 2, row)) + c % 2);
+              const float zs[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float x = __uint_as_float(o[c / 8][c % 8 * 4 + e]);
+                o[c / 8][c % 8 * 4 + e] = __float_as_uint(mine_first ? fmaf(zs[e], g, x * f) : fmaf(x, f, zs[e] * g));
+              }
+            }
+          }
+        }
+        if (row_ok) {
           const float inv = 1.f / l_run;
           __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) +
                                ((int64_t)(w.item.row0 + token) * a.h_q + w.head * a.group + r % a.group) * D;
@@ -658,14 +716,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 reinterpret_cast<uint4*>(dst + c * 32)[e] = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
             }
           }
-        } else {
-          const int64_t slot = w.slot(blockIdx.x) * a.layout.rows + t * kBM + r;
-          float* dst = reinterpret_cast<float*>(a.ws + a.layout.part_o) + slot * D;
-          reinterpret_cast<float2*>(a.ws + a.layout.part_ml)[slot] = make_float2(m_run, l_run);
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c)
-#pragma unroll
-            for (int e = 0; e < 32; e += 8) st_global_v8(dst + c * 32 + e, &o[c][e]);
         }
       }
       if (!ok && lane == 0) raise_timeout(p, bars);
