@@ -71,7 +71,7 @@ struct Bars {
   uint32_t tmem;
   int abort;
   int never;
-  int bad[8];  // unit u % 8 has NaN or infinities in V at tiles with masked keys
+  int bad[8];  // unit u % 8 has NaN or infinities in V (e4m3: in its scales) at tiles with masked keys
 };
 static_assert(sizeof(Bars) <= 1024, "barriers");
 
@@ -372,25 +372,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
               }
               if (is_v && edge) {
+                uint4* at = reinterpret_cast<uint4*>(tile) + x;
+                // a half with all exponent bits carries into its top bit
+                auto bad_bits = [](uint32_t u) { return ((u & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
                 uint32_t any = 0;
+#pragma unroll 8
                 for (int e = 0; e < L::kTile / 16 / 128; ++e) {
-                  uint4* at = reinterpret_cast<uint4*>(tile) + e * 128 + x;
-                  uint4 v = *at;
-                  uint32_t* u = reinterpret_cast<uint32_t*>(&v);
-                  uint32_t bad = 0;
-#pragma unroll
-                  for (int i = 0; i < 4; ++i)  // a half with all exponent bits carries into its top bit
-                    bad |= ((u[i] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
-                  if (bad) {
+                  const uint4 v = at[e * 128];
+                  any |= bad_bits(v.x) | bad_bits(v.y) | bad_bits(v.z) | bad_bits(v.w);
+                }
+                if (any) {
+#pragma unroll 1
+                  for (int e = 0; e < L::kTile / 16 / 128; ++e) {
+                    uint4 v = at[e * 128];
+                    uint32_t* u = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                      const uint32_t b = ((u[i] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+                      const uint32_t b = bad_bits(u[i]);
                       if (b & 0x8000u) u[i] &= 0xffff0000u;
                       if (b & 0x80000000u) u[i] &= 0x0000ffffu;
                     }
-                    *at = v;
+                    at[e * 128] = v;
                   }
-                  any |= bad;
                 }
                 if (__any_sync(0xffffffffu, any != 0)) {
                   if (lane == 0) *reinterpret_cast<volatile int*>(&bars->bad[n & 7]) = 1;
@@ -405,7 +408,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = false;
                 break;
               }
-              if (!is_v) mbar_arrive_warp(&bars->sc_full[tiles_done % kScaleSlots]);
+              if (!is_v) {
+                // This thread's key: K's factor with the softmax's (1 for a row of zeros, whose scores are 0;
+                // a row with a NaN scale has NaN codes), and V's, where a NaN at a tile with masked keys
+                // becomes 0: the epilogue puts it back for the rows that see it
+                float* sc = reinterpret_cast<float*>(smem + L::kScale) + tiles_done % kScaleSlots * (2 * kBN) + x;
+                const float k = sc[0], v = sc[kBN];
+                sc[0] = k > 0.f ? k * p.scale_log2 : 1.f;
+                if (edge && !(v <= 3.4028235e38f)) {
+                  sc[kBN] = 0.f;
+                  *reinterpret_cast<volatile int*>(&bars->bad[n & 7]) = 1;
+                }
+                mbar_arrive_warp(&bars->sc_full[tiles_done % kScaleSlots]);
+              }
               const uint4* codes = reinterpret_cast<const uint4*>(smem + L::kStage + st * L::kCodes);
               const uint32_t dst = smem_u32(tile);
               constexpr int kGroups = D / 16;  // 16-code groups of a row
@@ -413,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int e = 0; e < kBN * kGroups / 128; ++e) {
                 const int at = e * 128 + x, r = at / kGroups, g = at % kGroups;
                 uint4 c = codes[at];
-                if (is_v && edge) {  // NaN codes of masked positions; rows that see one have its NaN scale in P
+                if (is_v && edge) {  // and NaN codes become 0
                   uint32_t* u = reinterpret_cast<uint32_t*>(&c);
 #pragma unroll
                   for (int i = 0; i < 4; ++i) u[i] &= ~(((((u[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xffu);
@@ -453,8 +468,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int t = warp >> 2, r = (warp & 3) * 32 + lane;  // row tile, row (a warp reaches TMEM lanes 32 (warp % 4) ..)
       const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
       const uint32_t tm_s = tmem + t * kBN + lane_off, tm_o = tmem + 256 + t * D + lane_off;
-      const float sl2 = Q8 ? 1.f : p.scale_log2;  // e4m3: folded into the key's factor below
-      const unsigned long long sl2x2 = f2pack(sl2, sl2), kfac = f2pack(p.scale_log2, p.scale_log2);
+      const float sl2 = Q8 ? 1.f : p.scale_log2;  // e4m3: in the keys' factors
+      const unsigned long long sl2x2 = f2pack(sl2, sl2);
       const int tok = r / a.group;  // token of the tile
       uint32_t s_cnt = 0, o_cnt = 0, n = 0, tiles_done = 0;
       bool ok = true;
@@ -493,28 +508,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < 4; ++c) tmem_ld32(tm_s + c * 32, sr[c]);
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_ld_wait(sr[c]);
-          if (Q8) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                const float4 k = sc[c * 8 + e / 4];
-                const float2 x = unpack2(mul2((unsigned long long)sr[c][e] | (unsigned long long)sr[c][e + 1] << 32,
-                                              mul2(f2pack(k.x, k.y), kfac)));
-                const float2 y = unpack2(mul2((unsigned long long)sr[c][e + 2] | (unsigned long long)sr[c][e + 3] << 32,
-                                              mul2(f2pack(k.z, k.w), kfac)));
-                sr[c][e] = __float_as_uint(x.x);
-                sr[c][e + 1] = __float_as_uint(x.y);
-                sr[c][e + 2] = __float_as_uint(y.x);
-                sr[c][e + 3] = __float_as_uint(y.y);
-              }
-          }
-          const int hi = pos - u0, lo = a.window ? hi - a.window + 1 : 0, below = a.sinks - u0;
           if (edge) {
+            // Keys this row sees, as bits.  A warp's few tokens agree on most words of 32 keys.
+            const int hi = pos - u0, lo = a.window ? hi - a.window + 1 : 0, below = a.sinks - u0;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               const uint32_t seen = seen_bits(c, hi, lo, below);
-              if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;  // a warp's few tokens agree on most keys
+              if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 if (!(seen >> e & 1u)) sr[c][e] = __float_as_uint(-INFINITY);
@@ -523,17 +523,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           auto row_max = [&]() -> float {
             float mp[8];
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-              mp[q] = fmax3(__uint_as_float(sr[q >> 1][(q & 1) * 16]), __uint_as_float(sr[q >> 1][(q & 1) * 16 + 1]),
-                            __uint_as_float(sr[q >> 1][(q & 1) * 16 + 2]));
+            for (int q = 0; q < 8; ++q) mp[q] = -INFINITY;
 #pragma unroll
-            for (int e = 3; e < 15; e += 2)
+            for (int c = 0; c < 4; ++c)
 #pragma unroll
-              for (int q = 0; q < 8; ++q)
-                mp[q] = fmax3(mp[q], __uint_as_float(sr[q >> 1][(q & 1) * 16 + e]),
-                              __uint_as_float(sr[q >> 1][(q & 1) * 16 + e + 1]));
-#pragma unroll
-            for (int q = 0; q < 8; ++q) mp[q] = fmaxf(mp[q], __uint_as_float(sr[q >> 1][(q & 1) * 16 + 15]));
+              for (int e = 0; e < 32; e += 4) {
+                float4 k = make_float4(1.f, 1.f, 1.f, 1.f);
+                if (Q8) k = sc[c * 8 + e / 4];
+                const int q = e / 4;
+                mp[q] = fmax3(mp[q], __uint_as_float(sr[c][e]) * k.x, __uint_as_float(sr[c][e + 1]) * k.y);
+                mp[q] = fmax3(mp[q], __uint_as_float(sr[c][e + 2]) * k.z, __uint_as_float(sr[c][e + 3]) * k.w);
+              }
             return fmax3(fmax3(mp[0], mp[1], mp[2]), fmax3(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7])) * sl2;
           };
           // P into the first 64 columns of S_t; returns the row's sum of the weights
@@ -542,26 +542,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             unsigned long long accs[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              const uint32_t seen = Q8 && edge ? seen_bits(c, hi, lo, below) : 0xffffffffu;
-              const bool cut = Q8 && edge && __any_sync(0xffffffffu, seen != 0xffffffffu);
               uint32_t pk[16];
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
                 const unsigned long long sv = (unsigned long long)sr[c][2 * e] | ((unsigned long long)sr[c][2 * e + 1] << 32);
-                const float2 z = unpack2(Q8 ? add2(sv, negm) : fma2(sv, sl2x2, negm));
-                float x = ex2_approx(z.x), y = ex2_approx(z.y);
-                accs[e & 3] = add2(accs[e & 3], f2pack(x, y));
-                if (Q8) {
-                  const float2 v = reinterpret_cast<const float2*>(sc)[kBN / 2 + c * 16 + e];
-                  const float2 xy = unpack2(mul2(f2pack(x, y), f2pack(v.x, v.y)));
-                  x = xy.x;
-                  y = xy.y;
-                  if (cut) {  // a masked row's scale may be anything
-                    if (!(seen >> (2 * e) & 1u)) x = 0.f;
-                    if (!(seen >> (2 * e + 1) & 1u)) y = 0.f;
-                  }
-                }
-                pk[e] = pack_bf16x2(x, y);
+                const unsigned long long k = Q8 ? reinterpret_cast<const unsigned long long*>(sc)[c * 16 + e] : sl2x2;
+                const float2 z = unpack2(fma2(sv, k, negm));
+                unsigned long long w = f2pack(ex2_approx(z.x), ex2_approx(z.y));
+                accs[e & 3] = add2(accs[e & 3], w);
+                if (Q8) w = mul2(w, reinterpret_cast<const unsigned long long*>(sc)[kBN / 2 + c * 16 + e]);  // V's scales
+                const float2 x = unpack2(w);
+                pk[e] = pack_bf16x2(x.x, x.y);
               }
               tmem_st16(tm_s + c * 16, pk);
             }
@@ -615,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < D / 32; ++c) tmem_ld32(tm_o + c * 32, o[c]);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) tmem_ld_wait(o[c]);
-        const bool bad = !Q8 && *reinterpret_cast<volatile int*>(&bars->bad[n & 7]);
+        const bool bad = *reinterpret_cast<volatile int*>(&bars->bad[n & 7]);
         tc_fence_before();
         mbar_arrive_warp(&bars->o_free[t]);
         if (bad && row_ok) {
@@ -626,6 +617,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!edge_tile(a, u0, p0, p1)) continue;
             for (int u = u0; u < u0 + kBN && u <= pos; ++u) {
               if (!span_sees(pos, u, a.window, a.sinks)) continue;
+              if (Q8) {
+                const int64_t cell =
+                    ((int64_t)a.table[(int64_t)w.item.question * a.max_blocks + u / kPage] * a.h_kv + w.head) * kPage + u % kPage;
+                if (!(a.scale_v[cell] <= 3.4028235e38f)) l_run = __int_as_float(0x7fffffff);
+                continue;
+              }
               const uint4* v = reinterpret_cast<const uint4*>(
                   a.table ? static_cast<const __nv_bfloat16*>(a.pool_v) +
                                 (((int64_t)a.table[(int64_t)w.item.question * a.max_blocks + u / kPage] * a.h_kv + w.head) * kPage +
