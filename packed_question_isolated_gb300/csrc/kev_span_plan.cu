@@ -292,10 +292,19 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(SpanArgs a) {
   for (int x = t; x < a.ctas * kSpanRows; x += kThreads) arrived[x] = 0;
   const long long total = run;
   const int parts = total < a.ctas ? (int)total : a.ctas;
+  // place(c) without 64-bit divisions per thread; the part that holds a place by an estimate and steps
+  const long long q = parts ? total / parts : 0;
+  const unsigned r = parts ? (unsigned)(total - q * parts) : 0u;
+  auto place = [&](int c) { return c * q + (unsigned)c * r / (unsigned)parts; };
+  const float per_place = total ? (float)parts / (float)total : 0.f;
+  auto part_of = [&](long long x) {
+    int c = min(parts - 1, (int)((float)x * per_place));
+    while (c > 0 && place(c) > x) --c;
+    while (c + 1 < parts && place(c + 1) <= x) ++c;
+    return c;
+  };
   for (int c = t; c <= a.ctas; c += kThreads) {
-    // part c begins at c * total / parts; the part that holds place x is ((x + 1) * parts - 1) / total
-    auto part_of = [&](long long x) { return (int)(((x + 1) * parts - 1) / total); };
-    const long long w = c < parts ? c * total / parts : total;
+    const long long w = c < parts ? place(c) : total;
     SpanCut cut = {};
     cut.item = n_items;
     if (w < total) {
@@ -305,11 +314,11 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(SpanArgs a) {
         if (cum[mid] <= w) lo = mid;
         else hi = mid - 1;
       }
-      const int size = (int)(((lo + 1 < n_items ? cum[lo + 1] : total) - cum[lo]) / a.h_kv);
-      const long long in = w - cum[lo];
       cut.item = lo;
       cut.record = record(lo);
-      cut.head = (int)(in / size);
+      const int size = cut.record.tiles + a.unit_cost;
+      const long long in = w - cum[lo];
+      cut.head = in < 0x7fffffffll ? (int)in / size : (int)(in / size);
       const int at = (int)(in - (long long)cut.head * size);
       cut.tile = max(0, at - a.unit_cost);
       if (cut.tile > 0) {
