@@ -202,6 +202,30 @@ __device__ __forceinline__ int64_t span_part(const SpanArgs& a, int64_t slot, in
   return ((slot * (a.d / 8) + c) * a.layout.rows + row) * 8;
 }
 
+// A row's quantisation: scale = top / 448 (a NaN for a row that holds a NaN or an infinity), and its
+// elements' quotients x / scale, both the correctly rounded ones.  The quotients take the residual
+// correction of Markstein (1990): with r the correctly rounded reciprocal and q = x r, the fused
+// q + (x - q scale) r is the correctly rounded quotient -- as long as the residual is exact, so far
+// from the subnormals; smaller scales divide.  (The divisions were three quarters of the write's
+// instructions.)
+__device__ __forceinline__ float span_scale(float top) {
+  return top < INFINITY ? __fdiv_rn(top, 448.f) : __int_as_float(0x7fffffff);
+}
+template <int N>
+__device__ __forceinline__ void span_quotients(float (&f)[N], float scale) {
+  if (scale >= 8.2718061e-25f) {  // 2^-80
+    const float r = __frcp_rn(scale);
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const float q = f[e] * r;
+      f[e] = fmaf(fmaf(-q, scale, f[e]), r, q);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e) f[e] = scale == 0.f ? 0.f : __fdiv_rn(f[e], scale);
+  }
+}
+
 // Is position u visible to the token at position p?
 __device__ __forceinline__ bool span_sees(int p, int u, int window, int sinks) {
   return u <= p && (window == 0 || p - u < window || u < sinks);

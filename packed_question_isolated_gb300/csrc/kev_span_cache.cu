@@ -130,15 +130,11 @@ __global__ void __launch_bounds__(kThreads) span_write_kernel(SpanArgs a) {
           for (int i = 0; i < V::n; ++i) top = nan_max(top, fabsf(f[i]));
 #pragma unroll
           for (int o = kLanes / 2; o > 0; o >>= 1) top = nan_max(top, __shfl_xor_sync(0xffffffffu, top, o));
-          const float scale = top < INFINITY ? __fdiv_rn(top, 448.f) : __int_as_float(0x7fffffff);
+          const float scale = span_scale(top);
+          span_quotients(f, scale);
           uint32_t c[V::n / 4];
 #pragma unroll
-          for (int i = 0; i < V::n / 4; ++i) {
-            float y[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) y[j] = scale == 0.f ? 0.f : __fdiv_rn(f[4 * i + j], scale);
-            c[i] = e4m3x2(y[0], y[1]) | e4m3x2(y[2], y[3]) << 16;
-          }
+          for (int i = 0; i < V::n / 4; ++i) c[i] = e4m3x2(f[4 * i], f[4 * i + 1]) | e4m3x2(f[4 * i + 2], f[4 * i + 3]) << 16;
           if (g < a.h_kv) {
             unsigned char* dst = static_cast<unsigned char*>(is_v ? a.pool_v : a.pool_k) + cell * D + sub * V::n;
             if (V::n == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(c[0], c[V::n / 4 - 1]);

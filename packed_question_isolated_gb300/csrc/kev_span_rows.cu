@@ -421,9 +421,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
           }
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) top = nan_max(top, __shfl_xor_sync(0xffffffffu, top, o));
-          const float scale = top < INFINITY ? __fdiv_rn(top, 448.f) : __int_as_float(0x7fffffff);
-#pragma unroll
-          for (int e = 0; e < kN; ++e) f[e] = scale == 0.f ? 0.f : __fdiv_rn(f[e], scale);
+          const float scale = span_scale(top);
+          span_quotients(f, scale);
           const uint32_t lo = e4m3x2(f[0], f[1]);
           if (kN == 4) {
             const uint32_t code = lo | e4m3x2(f[kN - 2], f[kN - 1]) << 16;
