@@ -209,6 +209,10 @@ __device__ __forceinline__ int64_t span_part(const SpanArgs& a, int64_t slot, in
 // from the subnormals; smaller scales divide.  (The divisions were three quarters of the write's
 // instructions.)
 __device__ __forceinline__ float span_scale(float top) {
+  if (top >= 7.8886091e-31f && top < INFINITY) {  // 2^-100
+    const float r = 1.f / 448.f, q = top * r;
+    return fmaf(fmaf(-q, 448.f, top), r, q);
+  }
   return top < INFINITY ? __fdiv_rn(top, 448.f) : __int_as_float(0x7fffffff);
 }
 template <int N>

@@ -6,11 +6,12 @@
 // an e4m3 step of its size (relative 2^-4, or 2^-10 s below the normal range).  A row of zeros has
 // s = 0 and codes 0; a row that holds a NaN or an infinity has a NaN for its scale and reads
 // back as NaN throughout.  Reading gives c_e * s, rounded once to the output type.  Both
-// divisions are IEEE: the codes do not depend on the kernel's shape.
+// quotients are the correctly rounded ones: the codes do not depend on the kernel's shape.
 //
 // Bound by memory: 2 T H_kv (d elem + d + 4) bytes each way for an e4m3 cache.  A warp takes one
-// token's K or V rows of all kv heads: one search for the token's question and one page look-up,
-// then 16-byte loads with up to 4 in flight per lane (8 heads of 128 bf16: exactly 4).
+// token's K and V rows of all kv heads: one search for the token's question (in shared memory) and
+// one page look-up, then 16-byte loads with up to 8 in flight per lane (8 heads of 128 bf16: exactly
+// 8; with 4, and the search in L2, the chain of look-ups held the copy to 60 % of the bandwidth).
 #include <cuda_fp8.h>
 
 #include "kev_span.cuh"
@@ -19,6 +20,15 @@ namespace kev {
 namespace {
 
 constexpr int kThreads = 256;
+
+// The prefix sums of the questions' lengths into shared memory, by the whole CTA.
+__device__ __forceinline__ const int32_t* share_cu(const SpanArgs& a) {
+  extern __shared__ int32_t s_cu[];
+  const int32_t* cu = reinterpret_cast<const int32_t*>(a.ws + a.layout.cu);
+  for (int i = threadIdx.x; i < a.n; i += kThreads) s_cu[i] = cu[i];
+  __syncthreads();
+  return s_cu;
+}
 
 // the question of new token x: the last i with cu[i] <= x (empty questions share their successor's value)
 __device__ __forceinline__ int question_of(const int32_t* cu, int n, int x) {
@@ -43,6 +53,12 @@ __device__ __forceinline__ Place place_of(const SpanArgs& a, const int32_t* cu, 
   return {a.intervals[i].begin + j, a.table[(int64_t)i * a.max_blocks + p / kPage], p % kPage};
 }
 
+// max |x| that keeps NaN
+__device__ __forceinline__ float nan_max(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 template <int E> struct Vec;  // 16 bytes of a row as floats
 template <> struct Vec<4> {
   static constexpr int n = 4;
@@ -52,12 +68,26 @@ template <> struct Vec<4> {
     f[2] = __uint_as_float(w.z);
     f[3] = __uint_as_float(w.w);
   }
+  static __device__ float top(uint4 w) {  // the largest magnitude, or NaN
+    return nan_max(nan_max(fabsf(__uint_as_float(w.x)), fabsf(__uint_as_float(w.y))),
+                   nan_max(fabsf(__uint_as_float(w.z)), fabsf(__uint_as_float(w.w))));
+  }
   static __device__ uint4 put(const float (&f)[4]) {
     return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
   }
 };
 template <> struct Vec<2> {
   static constexpr int n = 8;
+  static __device__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  static __device__ float top(uint4 w) {  // two elements at a time
+    constexpr uint32_t kAbs = 0x7fff7fffu;
+    const uint32_t m = max2(max2(w.x & kAbs, w.y & kAbs), max2(w.z & kAbs, w.w & kAbs));
+    return nan_max(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  }
   static __device__ void get(uint4 w, float (&f)[8]) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -77,12 +107,6 @@ template <> struct Vec<2> {
   }
 };
 
-// max |x| that keeps NaN
-__device__ __forceinline__ float nan_max(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
 // two e4m3 codes, the first in the low byte
 __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
   uint16_t r;
@@ -100,49 +124,58 @@ __global__ void __launch_bounds__(kThreads) span_write_kernel(SpanArgs a) {
   pdl_trigger();
   const SpanHeader* h = reinterpret_cast<const SpanHeader*>(a.ws);
   if (h->status != ST_OK) return;
-  const int32_t* cu = reinterpret_cast<const int32_t*>(a.ws + a.layout.cu);
+  const int32_t* cu = share_cu(a);
   const int lane = threadIdx.x & 31, sub = lane % kLanes, r0 = lane / kLanes;
   const int warps = gridDim.x * (kThreads / 32);
-  const int64_t todo = 2 * (int64_t)h->n_new;
-  for (int64_t w = blockIdx.x * (kThreads / 32) + threadIdx.x / 32; w < todo; w += warps) {
-    const Place at = place_of(a, cu, (int)(w >> 1));
-    const bool is_v = w & 1;
-    const uint4* src = static_cast<const uint4*>(is_v ? a.v : a.k) + (int64_t)at.token * a.h_kv * kLanes;
+  const int n_new = h->n_new;
+  // few tokens: a warp for each of K and V
+  const int split = 2 * (int64_t)n_new <= warps;
+  int x = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+  const int side = x & 1;
+  if (split) x >>= 1;
+  Place next = x < n_new ? place_of(a, cu, x) : Place{};
+  for (; x < n_new; x += warps) {
+    const Place at = next;  // looked up one token ahead
+    if (x + warps < n_new) next = place_of(a, cu, x + warps);
     const int64_t cell0 = at.block * a.h_kv * kPage + at.row;  // + head * kPage: the cached row
     for (int g0 = 0; g0 < a.h_kv; g0 += kRows * kFlight) {
-      uint4 x[kFlight];
+      uint4 w[2][kFlight];
 #pragma unroll
-      for (int e = 0; e < kFlight; ++e) {
-        const int g = g0 + e * kRows + r0;
-        if (g < a.h_kv) x[e] = src[g * kLanes + sub];
-      }
+      for (int v = 0; v < 2; ++v)
 #pragma unroll
-      for (int e = 0; e < kFlight; ++e) {
-        const int g = g0 + e * kRows + r0;
-        const int64_t cell = cell0 + (int64_t)g * kPage;
-        if (!Q8) {
-          if (g < a.h_kv) static_cast<uint4*>(is_v ? a.pool_v : a.pool_k)[cell * kLanes + sub] = x[e];
-        } else {
-          float f[V::n], top = 0.f;
-          if (g >= a.h_kv) x[e] = make_uint4(0u, 0u, 0u, 0u);
-          V::get(x[e], f);
+        for (int e = 0; e < kFlight; ++e) {
+          if (split && v != side) continue;
+          const int g = g0 + e * kRows + r0;
+          w[v][e] = g < a.h_kv ? static_cast<const uint4*>(v ? a.v : a.k)[((int64_t)at.token * a.h_kv + g) * kLanes + sub]
+                               : make_uint4(0u, 0u, 0u, 0u);
+        }
 #pragma unroll
-          for (int i = 0; i < V::n; ++i) top = nan_max(top, fabsf(f[i]));
+      for (int v = 0; v < 2; ++v)
 #pragma unroll
-          for (int o = kLanes / 2; o > 0; o >>= 1) top = nan_max(top, __shfl_xor_sync(0xffffffffu, top, o));
-          const float scale = span_scale(top);
-          span_quotients(f, scale);
-          uint32_t c[V::n / 4];
+        for (int e = 0; e < kFlight; ++e) {
+          if (split && v != side) continue;
+          const int g = g0 + e * kRows + r0;
+          const int64_t cell = cell0 + (int64_t)g * kPage;
+          if (!Q8) {
+            if (g < a.h_kv) static_cast<uint4*>(v ? a.pool_v : a.pool_k)[cell * kLanes + sub] = w[v][e];
+          } else {
+            float f[V::n], top = V::top(w[v][e]);
+            V::get(w[v][e], f);
 #pragma unroll
-          for (int i = 0; i < V::n / 4; ++i) c[i] = e4m3x2(f[4 * i], f[4 * i + 1]) | e4m3x2(f[4 * i + 2], f[4 * i + 3]) << 16;
-          if (g < a.h_kv) {
-            unsigned char* dst = static_cast<unsigned char*>(is_v ? a.pool_v : a.pool_k) + cell * D + sub * V::n;
-            if (V::n == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(c[0], c[V::n / 4 - 1]);
-            else *reinterpret_cast<uint32_t*>(dst) = c[0];
-            if (sub == 0) (is_v ? a.scale_v : a.scale_k)[cell] = scale;
+            for (int o = kLanes / 2; o > 0; o >>= 1) top = nan_max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float scale = span_scale(top);
+            span_quotients(f, scale);
+            uint32_t c[V::n / 4];
+#pragma unroll
+            for (int i = 0; i < V::n / 4; ++i) c[i] = e4m3x2(f[4 * i], f[4 * i + 1]) | e4m3x2(f[4 * i + 2], f[4 * i + 3]) << 16;
+            if (g < a.h_kv) {
+              unsigned char* dst = static_cast<unsigned char*>(v ? a.pool_v : a.pool_k) + cell * D + sub * V::n;
+              if (V::n == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(c[0], c[V::n / 4 - 1]);
+              else *reinterpret_cast<uint32_t*>(dst) = c[0];
+              if (sub == 0) (v ? a.scale_v : a.scale_k)[cell] = scale;
+            }
           }
         }
-      }
     }
   }
 }
@@ -155,61 +188,73 @@ __global__ void __launch_bounds__(kThreads) span_read_kernel(SpanArgs a, void* k
   pdl_trigger();
   const SpanHeader* h = reinterpret_cast<const SpanHeader*>(a.ws);
   if (h->status != ST_OK) return;
-  const int32_t* cu = reinterpret_cast<const int32_t*>(a.ws + a.layout.cu);
+  const int32_t* cu = share_cu(a);
   const int lane = threadIdx.x & 31, sub = lane % kLanes, r0 = lane / kLanes;
   const int warps = gridDim.x * (kThreads / 32);
-  const int64_t todo = 2 * (int64_t)h->n_new;
-  for (int64_t w = blockIdx.x * (kThreads / 32) + threadIdx.x / 32; w < todo; w += warps) {
-    const Place at = place_of(a, cu, (int)(w >> 1));
-    const bool is_v = w & 1;
-    uint4* dst = static_cast<uint4*>(is_v ? v_out : k_out) + (int64_t)at.token * a.h_kv * kLanes;
+  const int n_new = h->n_new;
+  // few tokens: a warp for each of K and V
+  const int split = 2 * (int64_t)n_new <= warps;
+  int x = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+  const int side = x & 1;
+  if (split) x >>= 1;
+  Place next = x < n_new ? place_of(a, cu, x) : Place{};
+  for (; x < n_new; x += warps) {
+    const Place at = next;  // looked up one token ahead
+    if (x + warps < n_new) next = place_of(a, cu, x + warps);
     const int64_t cell0 = at.block * a.h_kv * kPage + at.row;
     for (int g0 = 0; g0 < a.h_kv; g0 += kRows * kFlight) {
-      uint4 x[kFlight];
-      float s[kFlight];
+      uint4 w[2][kFlight];
+      float s[2][kFlight];
 #pragma unroll
-      for (int e = 0; e < kFlight; ++e) {
-        const int g = g0 + e * kRows + r0;
-        const int64_t cell = cell0 + (int64_t)g * kPage;
-        if (g >= a.h_kv) continue;
-        if (Q8) {
-          const unsigned char* src = static_cast<const unsigned char*>(is_v ? a.pool_v : a.pool_k) + cell * D + sub * V::n;
-          if (V::n == 8) {
-            const uint2 c = *reinterpret_cast<const uint2*>(src);
-            x[e] = make_uint4(c.x, c.y, 0u, 0u);
+      for (int v = 0; v < 2; ++v)
+#pragma unroll
+        for (int e = 0; e < kFlight; ++e) {
+          if (split && v != side) continue;
+          const int g = g0 + e * kRows + r0;
+          const int64_t cell = cell0 + (int64_t)g * kPage;
+          if (g >= a.h_kv) continue;
+          if (Q8) {
+            const unsigned char* src = static_cast<const unsigned char*>(v ? a.pool_v : a.pool_k) + cell * D + sub * V::n;
+            if (V::n == 8) {
+              const uint2 c = *reinterpret_cast<const uint2*>(src);
+              w[v][e] = make_uint4(c.x, c.y, 0u, 0u);
+            } else {
+              w[v][e].x = *reinterpret_cast<const uint32_t*>(src);
+            }
+            s[v][e] = (v ? a.scale_v : a.scale_k)[cell];
           } else {
-            x[e].x = *reinterpret_cast<const uint32_t*>(src);
+            w[v][e] = static_cast<const uint4*>(v ? a.pool_v : a.pool_k)[cell * kLanes + sub];
           }
-          s[e] = (is_v ? a.scale_v : a.scale_k)[cell];
-        } else {
-          x[e] = static_cast<const uint4*>(is_v ? a.pool_v : a.pool_k)[cell * kLanes + sub];
         }
-      }
 #pragma unroll
-      for (int e = 0; e < kFlight; ++e) {
-        const int g = g0 + e * kRows + r0;
-        if (g >= a.h_kv) continue;
-        if (Q8) {
-          const uint32_t c[2] = {x[e].x, x[e].y};
-          float f[V::n];
+      for (int v = 0; v < 2; ++v)
 #pragma unroll
-          for (int i = 0; i < V::n; i += 2) {
-            uint32_t half2;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(half2) : "h"((uint16_t)(c[i / 4] >> (i % 4 * 8))));
-            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&half2));
-            f[i] = v.x * s[e];
-            f[i + 1] = v.y * s[e];
+        for (int e = 0; e < kFlight; ++e) {
+          if (split && v != side) continue;
+          const int g = g0 + e * kRows + r0;
+          if (g >= a.h_kv) continue;
+          uint4* dst = static_cast<uint4*>(v ? v_out : k_out) + ((int64_t)at.token * a.h_kv + g) * kLanes + sub;
+          if (Q8) {
+            const uint32_t c[2] = {w[v][e].x, w[v][e].y};
+            float f[V::n];
+#pragma unroll
+            for (int i = 0; i < V::n; i += 2) {
+              uint32_t half2;
+              asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(half2) : "h"((uint16_t)(c[i / 4] >> (i % 4 * 8))));
+              const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&half2));
+              f[i] = y.x * s[v][e];
+              f[i + 1] = y.y * s[v][e];
+            }
+            *dst = V::put(f);
+          } else {
+            *dst = w[v][e];
           }
-          dst[g * kLanes + sub] = V::put(f);
-        } else {
-          dst[g * kLanes + sub] = x[e];
         }
-      }
     }
   }
 }
 
-int grid_of(const SpanArgs& a, int num_sms) {  // one warp per token and side, 8 CTAs of 8 warps per SM at most
+int grid_of(const SpanArgs& a, int num_sms) {  // two warps per token, 8 CTAs of 8 warps per SM at most
   const int64_t ctas = (2 * (int64_t)a.T + kThreads / 32 - 1) / (kThreads / 32);
   return (int)(ctas < 8 * num_sms ? ctas : 8 * num_sms);
 }
@@ -223,7 +268,7 @@ cudaError_t launch_span_write(const SpanArgs& a, int num_sms, cudaStream_t s) {
                                        : (q8 ? span_write_kernel<2, 128, true> : span_write_kernel<2, 128, false>))
                           : (a.d == 64 ? (q8 ? span_write_kernel<4, 64, true> : span_write_kernel<4, 64, false>)
                                        : (q8 ? span_write_kernel<4, 128, true> : span_write_kernel<4, 128, false>));
-  return launch_pdl(kern, dim3(grid_of(a, num_sms)), dim3(kThreads), 0, s, a);
+  return launch_pdl(kern, dim3(grid_of(a, num_sms)), dim3(kThreads), sizeof(int32_t) * (size_t)a.n, s, a);
 }
 
 cudaError_t launch_span_read(const SpanArgs& a, void* k_out, void* v_out, int num_sms, cudaStream_t s) {
@@ -233,7 +278,7 @@ cudaError_t launch_span_read(const SpanArgs& a, void* k_out, void* v_out, int nu
                                        : (q8 ? span_read_kernel<2, 128, true> : span_read_kernel<2, 128, false>))
                           : (a.d == 64 ? (q8 ? span_read_kernel<4, 64, true> : span_read_kernel<4, 64, false>)
                                        : (q8 ? span_read_kernel<4, 128, true> : span_read_kernel<4, 128, false>));
-  return launch_pdl(kern, dim3(grid_of(a, num_sms)), dim3(kThreads), 0, s, a, k_out, v_out);
+  return launch_pdl(kern, dim3(grid_of(a, num_sms)), dim3(kThreads), sizeof(int32_t) * (size_t)a.n, s, a, k_out, v_out);
 }
 
 }  // namespace kev
