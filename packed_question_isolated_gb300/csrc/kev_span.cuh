@@ -26,7 +26,6 @@ constexpr int kSpanMaxBlocks = 1 << 20;  // pool blocks: the plan marks used blo
 
 struct SpanHeader {
   int32_t status;
-  int32_t n_items;
   int32_t n_gaps;
   int32_t n_new;  // tokens in questions
   int32_t n_joins;
@@ -50,16 +49,21 @@ struct alignas(16) SpanCut {
   int32_t pad[3];
 };
 
-struct SpanLayout {
-  size_t cu;       // int32[n + 1] prefix sums of the lengths, in question order
-  size_t gaps;     // int2[n + 1] token ranges of no question
+// A work line in the workspace.
+struct SpanLine {
   size_t items;    // SpanItem[max_items]
   size_t cum;      // int64[max_items + 1] key tiles (over all kv heads) before each item
   size_t cuts;     // SpanCut[kSpanMaxCtas + 1]
   size_t arrived;  // int32[kSpanMaxCtas][kSpanRows] finished pieces of the unit that begins in part c and goes on
+  size_t joins;    // int32[kSpanMaxCtas] cuts of the units that the merge kernel joins
+};
+
+struct SpanLayout {
+  size_t cu;       // int32[n + 1] prefix sums of the lengths, in question order
+  size_t gaps;     // int2[n + 1] token ranges of no question
+  SpanLine line[2];
   size_t part_ml;  // float2[2 * kSpanMaxCtas][rows] running maximum (log2 units) and sum
   size_t part_o;   // float[2 * kSpanMaxCtas][d / 8][rows][8] (few rows: [rows][d])
-  size_t joins;    // int32[kSpanMaxCtas] cuts of the units that the merge kernel joins
   size_t total;
   int32_t rows;    // rows of a partial result
   int64_t max_items;
@@ -80,13 +84,15 @@ inline SpanLayout span_layout(int32_t n, int32_t T, int32_t group, int32_t d) {
   };
   L.cu = take(sizeof(int32_t) * ((size_t)n + 1));
   L.gaps = take(sizeof(int2) * ((size_t)n + 1));
-  L.items = take(sizeof(SpanItem) * (size_t)L.max_items);
-  L.cum = take(sizeof(int64_t) * ((size_t)L.max_items + 1));
-  L.cuts = take(sizeof(SpanCut) * (kSpanMaxCtas + 1));
-  L.arrived = take(sizeof(int32_t) * kSpanRows * kSpanMaxCtas);
+  for (SpanLine& l : L.line) {
+    l.items = take(sizeof(SpanItem) * (size_t)L.max_items);
+    l.cum = take(sizeof(int64_t) * ((size_t)L.max_items + 1));
+    l.cuts = take(sizeof(SpanCut) * (kSpanMaxCtas + 1));
+    l.arrived = take(sizeof(int32_t) * kSpanRows * kSpanMaxCtas);
+    l.joins = take(sizeof(int32_t) * kSpanMaxCtas);
+  }
   L.part_ml = take(sizeof(float2) * 2 * kSpanMaxCtas * (size_t)L.rows);
   L.part_o = take(sizeof(float) * 2 * kSpanMaxCtas * (size_t)L.rows * d);
-  L.joins = take(sizeof(int32_t) * kSpanMaxCtas);
   L.total = off;
   return L;
 }
@@ -112,13 +118,15 @@ struct SpanArgs {
   int32_t max_blocks, n_blocks;
   int32_t window, sinks;  // window 0: every earlier position
   int32_t max_chunk;      // no question has more tokens
+  // The work line of this launch: the questions of min_tokens .. max_tokens tokens
+  SpanLine line;
+  int32_t min_tokens, max_tokens;
   int32_t tile_rows;      // M: rows of a row tile (128, 64 or 16)
   int32_t tile_tokens;    // floor(M / group)
   int32_t item_tiles;     // row tiles of an item
   int32_t ctas;           // parts of the work line
   int32_t join_from;      // units of so many pieces or more are joined by the merge kernel
   int32_t unit_cost;      // what a unit costs beside its key tiles, in key tiles
-  int32_t attend;         // 0: cache write or read only (no items)
   char* ws;
   SpanLayout layout;
   int32_t* dev_status;
@@ -127,7 +135,9 @@ struct SpanArgs {
 // tensor maps (kev_span_tc.cu): `rank` dimensions, innermost first and contiguous, of `elem`-byte elements
 bool span_tensor_map(CUtensorMap* m, const void* base, int elem, int rank, const cuuint64_t* dims, const cuuint32_t* box,
                      CUtensorMapSwizzle swizzle);
-cudaError_t launch_span_plan(const SpanArgs& a, cudaStream_t s);
+// The checks of a call, and the work lines of its attention launches: none for a cache write or read,
+// or one or two (same call, other line) whose questions between them are all that have tokens
+cudaError_t launch_span_plan(const SpanArgs& a, int lines, const SpanArgs* line0, const SpanArgs* line1, cudaStream_t s);
 cudaError_t launch_span_write(const SpanArgs& a, int num_sms, cudaStream_t s);
 cudaError_t launch_span_read(const SpanArgs& a, void* k_out, void* v_out, int num_sms, cudaStream_t s);
 cudaError_t launch_span_simt(const SpanArgs& a, cudaStream_t s);  // fp32
@@ -155,8 +165,8 @@ struct SpanWalk {
   SpanCut to;
   int from_first, from_parts, it, head, h_kv, j0, j1;
   __device__ __forceinline__ SpanWalk(const SpanArgs& a, int part) {
-    items = reinterpret_cast<const SpanItem*>(a.ws + a.layout.items);
-    const SpanCut* cuts = reinterpret_cast<const SpanCut*>(a.ws + a.layout.cuts);
+    items = reinterpret_cast<const SpanItem*>(a.ws + a.line.items);
+    const SpanCut* cuts = reinterpret_cast<const SpanCut*>(a.ws + a.line.cuts);
     const SpanCut from = cuts[part];
     to = cuts[part + 1];
     from_first = from.first;

@@ -75,40 +75,71 @@ kev_status span_cache(SpanArgs* a, const kev_attn_shape* shape, const int32_t* p
   return KEV_OK;
 }
 
-void span_tiling(SpanArgs* a, int rows, int tiles, int ctas) {
-  a->attend = 1;
-  a->tile_rows = rows;
-  a->tile_tokens = rows / a->group;
-  a->item_tiles = tiles;
-  a->ctas = ctas;
+// The launch of a kernel with row tiles of `rows` rows, `tiles` of them an item, on `ctas` CTAs.
+SpanArgs span_line(const SpanArgs& call, int line, int rows, int tiles, int ctas) {
+  SpanArgs a = call;
+  a.line = call.layout.line[line];
+  a.min_tokens = 1;
+  a.max_tokens = call.max_chunk;
+  a.tile_rows = rows;
+  a.tile_tokens = rows / a.group;
+  a.item_tiles = tiles;
+  a.ctas = ctas < kSpanMaxCtas ? ctas : kSpanMaxCtas;
+  return a;
 }
 
-kev_status span_attend(SpanArgs* a, bool write, cudaStream_t s) {
+// Every cached row meets at most 8 or 16 rows, which the register kernel takes at memory speed; it
+// joins its own pieces.
+SpanArgs span_few_rows(const SpanArgs& call, int line, int rows, int sms) {
+  SpanArgs a = span_line(call, line, rows, 1, rows == 8 ? 2 * sms : sms);
+  a.unit_cost = 2;  // measured beside 0 and 1: decode of 32 questions 31.4 us against 42.6 and 33.6
+  a.join_from = kSpanMaxCtas + 1;
+  return a;
+}
+
+kev_status span_attend(const SpanArgs& call, bool write, cudaStream_t s) {
   const int sms = sms_of_current_device();
   if (sms <= 0) return KEV_ERR_CUDA;
-  // Few rows per question, and the caller said so: every cached row meets at most 16 rows, which the
-  // register kernel takes at memory speed; it writes the new rows itself and joins its own pieces.
-  const int64_t rows = (int64_t)a->max_chunk * a->group;
-  if (a->elem == 2 && a->pool_elem && rows <= 16) {
-    const int ctas = rows <= 8 ? 2 * sms : sms;
-    span_tiling(a, rows <= 8 ? 8 : 16, 1, ctas < kSpanMaxCtas ? ctas : kSpanMaxCtas);
-    a->unit_cost = 2;  // measured beside 0 and 1: decode of 32 questions 31.4 us against 42.6 and 33.6
-    a->join_from = kSpanMaxCtas + 1;  // none: the kernel joins its own
-    cudaError_t e = launch_span_plan(*a, s);
-    if (e == cudaSuccess) e = launch_span_rows(*a, write, s);
+  cudaError_t e;
+  if (call.elem == 4) {
+    SpanArgs a = span_line(call, 0, 64, 1, 2 * sms);
+    a.join_from = 2;
+    e = launch_span_plan(call, 1, &a, nullptr, s);
+    if (e == cudaSuccess && write) e = launch_span_write(a, sms, s);
+    if (e == cudaSuccess) e = launch_span_simt(a, s);
+    if (e == cudaSuccess) e = launch_span_merge(a, sms, s);
     return from_cuda(e);
   }
-  const bool tc = a->elem == 2;
-  const int ctas = tc ? sms : 2 * sms;
-  span_tiling(a, tc ? 128 : 64, tc ? 2 : 1, ctas < kSpanMaxCtas ? ctas : kSpanMaxCtas);
+  const int64_t rows = (int64_t)call.max_chunk * call.group;
+  if (call.pool_elem && rows <= 16) {  // few rows per question, and the caller said so
+    const SpanArgs a = span_few_rows(call, 0, rows <= 8 ? 8 : 16, sms);
+    e = launch_span_plan(call, 1, &a, nullptr, s);
+    if (e == cudaSuccess) e = launch_span_rows(a, write, s);
+    return from_cuda(e);
+  }
+  SpanArgs a = span_line(call, 0, 128, 2, sms);
   // measured: a unit of two row tiles costs 1.8 us a key tile and 3.3 us beside them (loading q, the
   // masks of its first and last tiles, the epilogue)
-  a->unit_cost = tc ? 2 : 0;
-  a->join_from = tc ? 3 : 2;
-  cudaError_t e = launch_span_plan(*a, s);
-  if (e == cudaSuccess && write) e = launch_span_write(*a, sms, s);
-  if (e == cudaSuccess) e = tc ? launch_span_tc(*a, s) : launch_span_simt(*a, s);
-  if (e == cudaSuccess) e = launch_span_merge(*a, sms, s);
+  a.unit_cost = 2;
+  a.join_from = 3;
+  // Over an e4m3 cache, where an average question fills no row tile, most have one token or two: these go
+  // to the kernel for few rows, the others to the tensor cores.  Measured on 4 chunks of 256 to 512 tokens
+  // beside 60 single ones: 132 us, in one kernel 171 (the tensor-core kernel's conversion costs a page
+  // as much for 4 rows as for 256); over a bf16 cache it is the other way round, 122 against 111.
+  const bool split = call.pool_elem == 1 && (int64_t)call.T * call.group <= 128 * (int64_t)call.n;
+  if (split) {
+    SpanArgs b = span_few_rows(call, 1, call.group <= 8 ? 8 : 16, sms);
+    b.max_tokens = b.tile_tokens;
+    a.min_tokens = b.max_tokens + 1;
+    e = launch_span_plan(call, 2, &a, &b, s);
+    if (e == cudaSuccess && write) e = launch_span_write(call, sms, s);
+    if (e == cudaSuccess) e = launch_span_rows(b, false, s);
+  } else {
+    e = launch_span_plan(call, 1, &a, nullptr, s);
+    if (e == cudaSuccess && write) e = launch_span_write(call, sms, s);
+  }
+  if (e == cudaSuccess) e = launch_span_tc(a, s);
+  if (e == cudaSuccess) e = launch_span_merge(a, sms, s);
   return from_cuda(e);
 }
 
@@ -134,7 +165,7 @@ kev_status kev_paged_write(const void* k, const void* v, int32_t total_tokens, c
   if (sms <= 0) return KEV_ERR_CUDA;
   a.k = k;
   a.v = v;
-  cudaError_t e = launch_span_plan(a, (cudaStream_t)stream);
+  cudaError_t e = launch_span_plan(a, 0, nullptr, nullptr, (cudaStream_t)stream);
   if (e == cudaSuccess) e = launch_span_write(a, sms, (cudaStream_t)stream);
   return from_cuda(e);
 }
@@ -149,7 +180,7 @@ kev_status kev_paged_read(void* k, void* v, int32_t total_tokens, const kev_inte
   if (total_tokens > 0 && (!k || !v || !aligned(k, 16) || !aligned(v, 16))) return KEV_ERR_INVALID_ARG;
   const int sms = sms_of_current_device();
   if (sms <= 0) return KEV_ERR_CUDA;
-  cudaError_t e = launch_span_plan(a, (cudaStream_t)stream);
+  cudaError_t e = launch_span_plan(a, 0, nullptr, nullptr, (cudaStream_t)stream);
   if (e == cudaSuccess) e = launch_span_read(a, k, v, sms, (cudaStream_t)stream);
   return from_cuda(e);
 }
@@ -173,7 +204,7 @@ kev_status kev_chunk_attn_paged(const void* q, const void* k, const void* v, int
   a.window = window;
   a.sinks = sinks;
   if (max_chunk > 0 && max_chunk < a.max_chunk) a.max_chunk = max_chunk;
-  return span_attend(&a, k != nullptr, (cudaStream_t)stream);
+  return span_attend(a, k != nullptr, (cudaStream_t)stream);
 }
 
 kev_status kev_prefill_attn_window(const void* q, const void* k, const void* v, int32_t total_tokens,
@@ -193,7 +224,7 @@ kev_status kev_prefill_attn_window(const void* q, const void* k, const void* v, 
   a.out = out;
   a.window = window;
   a.sinks = sinks;
-  return span_attend(&a, false, (cudaStream_t)stream);
+  return span_attend(a, false, (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -18,17 +18,30 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kCumSmem = 4096;  // items whose tile counts are searched in shared memory
 
-// What the checks and the work line scan over the questions: end of the intervals so far, new
-// tokens, items, gaps.
+// What of a work line the plan needs.
+struct PlanLine {
+  SpanLine at;
+  int32_t item_tokens, min_tokens, max_tokens, ctas, unit_cost, join_from;
+};
+struct PlanArgs {
+  SpanArgs a;
+  int32_t lines;
+  PlanLine line[2];
+};
+
+// What the checks and the work lines scan over the questions: end of the intervals so far, new
+// tokens, items of both lines, gaps.
 struct Scan {
-  int end, tokens, items, gaps;
+  int end, tokens, items[2], gaps;
 };
 __device__ __forceinline__ Scan join(const Scan& a, const Scan& b) {
-  return {max(a.end, b.end), a.tokens + b.tokens, a.items + b.items, a.gaps + b.gaps};
+  return {max(a.end, b.end), a.tokens + b.tokens, {a.items[0] + b.items[0], a.items[1] + b.items[1]}, a.gaps + b.gaps};
 }
 __device__ __forceinline__ Scan up(const Scan& x, int o) {
-  return {__shfl_up_sync(0xffffffffu, x.end, o), __shfl_up_sync(0xffffffffu, x.tokens, o),
-          __shfl_up_sync(0xffffffffu, x.items, o), __shfl_up_sync(0xffffffffu, x.gaps, o)};
+  return {__shfl_up_sync(0xffffffffu, x.end, o),
+          __shfl_up_sync(0xffffffffu, x.tokens, o),
+          {__shfl_up_sync(0xffffffffu, x.items[0], o), __shfl_up_sync(0xffffffffu, x.items[1], o)},
+          __shfl_up_sync(0xffffffffu, x.gaps, o)};
 }
 __device__ __forceinline__ long long join(long long a, long long b) { return a + b; }
 __device__ __forceinline__ long long up(long long x, int o) { return __shfl_up_sync(0xffffffffu, x, o); }
@@ -63,7 +76,8 @@ __device__ T block_scan(T v, T zero, T* tmp /* [33] */, T* total) {
   return join(tmp[warp], before);
 }
 
-__global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(SpanArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(const __grid_constant__ PlanArgs p) {
+  const SpanArgs& a = p.a;
   extern __shared__ unsigned long long dyn[];  // intervals, prefixes; sort keys, bit map of used blocks or tile counts
   __shared__ Scan s_scan[33];
   __shared__ long long s_sum[33];
@@ -71,8 +85,9 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(SpanArgs a) {
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, n = a.n;
   kev_interval* iv = reinterpret_cast<kev_interval*>(dyn);
   int* pre = reinterpret_cast<int*>(iv + n);
-  int* base = pre + n;  // first item of each question
-  unsigned long long* area = dyn + (16 * (size_t)n + 8 + 7) / 8;
+  int* base0 = pre + n;  // first item of each question, in each line
+  int* base1 = base0 + n + 1;
+  unsigned long long* area = dyn + (20 * (size_t)n + 8 + 7) / 8;  // 8 + 4 + 4 + 4 bytes a question, and the two ends
   unsigned* used = reinterpret_cast<unsigned*>(area);
   const int words = a.pool_elem ? (a.n_blocks + 31) / 32 : 0;
   if (t == 0) s_err = s_joins = 0;
@@ -85,32 +100,35 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(SpanArgs a) {
   int2* gaps = reinterpret_cast<int2*>(a.ws + a.layout.gaps);
   // error ranks: intervals, prefix, overflow, slot -- the first that applies is reported
   auto error = [&](int rank) { atomicMax(&s_err, 8 - rank); };
-  const int item_tokens = a.tile_tokens * a.item_tiles;
+  auto items_of = [&](int l, int L) {
+    return l < p.lines && L >= p.line[l].min_tokens && L <= p.line[l].max_tokens ? (L + p.line[l].item_tokens - 1) / p.line[l].item_tokens : 0;
+  };
 
   // A thread's questions: `per` consecutive ones.
   const int per = (n + kThreads - 1) / kThreads;
-  Scan mine = {0, 0, 0, 0};
+  Scan mine = {};
 #pragma unroll 1
   for (int e = 0; e < per; ++e) {
     const int i = t * per + e;
     if (i >= n) break;
     const kev_interval v = a.intervals[i];
-    const int p = a.prefix ? a.prefix[i] : 0;
+    const int first = a.prefix ? a.prefix[i] : 0;
     iv[i] = v;
-    pre[i] = p;
+    pre[i] = first;
     if (v.begin < 0 || v.end < v.begin || v.end > a.T || v.end - v.begin > a.max_chunk) {
       error(0);
     } else if (v.end > v.begin) {
       const int L = v.end - v.begin;
-      if (p < 0) error(1);
-      else if (a.pool_elem && (int64_t)p + L > (int64_t)a.max_blocks * kPage) error(2);
+      if (first < 0) error(1);
+      else if (a.pool_elem && (int64_t)first + L > (int64_t)a.max_blocks * kPage) error(2);
       mine.end = max(mine.end, v.end);
       mine.tokens += L;
-      if (a.attend) mine.items += (L + item_tokens - 1) / item_tokens;
+      mine.items[0] += items_of(0, L);
+      mine.items[1] += items_of(1, L);
     }
   }
   Scan all;
-  const Scan before = block_scan(mine, Scan{0, 0, 0, 0}, s_scan, &all);
+  const Scan before = block_scan(mine, Scan{}, s_scan, &all);
 
   const bool clean = s_err == 0;  // the checks of single questions passed
   __syncthreads();
@@ -119,25 +137,28 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(SpanArgs a) {
   // beginning and looked at again.
   bool ok = true;
   if (clean) {
-    int end = before.end, tokens = before.tokens, items = before.items;
+    int end = before.end, tokens = before.tokens, items0 = before.items[0], items1 = before.items[1];
 #pragma unroll 1
     for (int e = 0; e < per; ++e) {
       const int i = t * per + e;
       if (i >= n) break;
       const int L = iv[i].end - iv[i].begin;
       cu[i] = tokens;
-      base[i] = items;
+      base0[i] = items0;
+      base1[i] = items1;
       if (L > 0) {
         ok = ok && iv[i].begin >= end;
         mine.gaps += iv[i].begin > end;
         end = max(end, iv[i].end);
         tokens += L;
-        if (a.attend) items += (L + item_tokens - 1) / item_tokens;
+        items0 += items_of(0, L);
+        items1 += items_of(1, L);
       }
     }
     if (t == 0) {
       cu[n] = all.tokens;
-      base[n] = all.items;
+      base0[n] = all.items[0];
+      base1[n] = all.items[1];
     }
     if (words) {  // pages: one or more warps per question, a lane per page; a block's bit may be set once
       const int slices = n < kThreads / 32 ? kThreads / 32 / n : 1;
@@ -148,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(SpanArgs a) {
         if (L <= 0) continue;
         const int p0 = pre[i], p1 = p0 + L - 1;
         int ns = 0, lo = p0 / kPage;
-        if (a.attend) {
+        if (p.lines) {
           const SpanTiles s(p0, p1, a.window, a.sinks);
           ns = s.ns;
           lo = s.lo;
@@ -179,12 +200,12 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(SpanArgs a) {
 #pragma unroll 1
       for (int j = k >> 1; j > 0; j >>= 1) {
         for (int i = t; i < n2; i += kThreads) {
-          const int p = i ^ j;
-          if (p > i) {
-            const unsigned long long x = area[i], y = area[p];
+          const int other = i ^ j;
+          if (other > i) {
+            const unsigned long long x = area[i], y = area[other];
             if ((x > y) == ((i & k) == 0)) {
               area[i] = y;
-              area[p] = x;
+              area[other] = x;
             }
           }
         }
@@ -193,12 +214,12 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(SpanArgs a) {
   }
   // gaps between the intervals in order
   auto find_gaps = [&](auto get, bool check) {
-    Scan v = {0, 0, 0, 0}, total;
+    Scan v = {}, total;
     for (int e = 0; e < per; ++e) {
       const int i = t * per + e;
       if (i < n && get(i).end > get(i).begin) v.end = max(v.end, get(i).end);
     }
-    const int first = block_scan(v, Scan{0, 0, 0, 0}, s_scan, &total).end;
+    const int first = block_scan(v, Scan{}, s_scan, &total).end;
     int end = first;
     for (int e = 0; e < per; ++e) {
       const int i = t * per + e;
@@ -209,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(SpanArgs a) {
       }
     }
     __syncthreads();  // the scan's scratch is free
-    int at = block_scan(v, Scan{0, 0, 0, 0}, s_scan, &total).gaps;
+    int at = block_scan(v, Scan{}, s_scan, &total).gaps;
     end = first;
     for (int e = 0; e < per; ++e) {
       const int i = t * per + e;
@@ -225,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(SpanArgs a) {
   };
   if (clean) {
     if (!sorted) find_gaps(ordered, true);
-    else if (a.attend && all.tokens < a.T) find_gaps(interval, false);
+    else if (p.lines && all.tokens < a.T) find_gaps(interval, false);
     else if (t == 0) hdr->n_gaps = 0;
     __syncthreads();
   }
@@ -239,121 +260,132 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(SpanArgs a) {
     return;
   }
   if (t == 0) {
-    hdr->n_items = all.items;
     hdr->n_new = all.tokens;
     hdr->status = ST_OK;
     if (a.dev_status) *a.dev_status = ST_OK;
   }
-  if (!a.attend) return;
 
-  // items and the key tiles before each
-  SpanItem* out = reinterpret_cast<SpanItem*>(a.ws + a.layout.items);
-  const int n_items = all.items;
-  long long* cum = n_items <= kCumSmem ? reinterpret_cast<long long*>(area)
-                                       : reinterpret_cast<long long*>(a.ws + a.layout.cum);
-  auto record = [&](int x) {
-    int lo = 0, hi = n - 1;  // the last question whose first item is at or before x
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (base[mid] <= x) lo = mid;
-      else hi = mid - 1;
-    }
-    SpanItem w = {};
-    const int token0 = (x - base[lo]) * item_tokens;
-    w.question = lo;
-    w.row0 = iv[lo].begin + token0;
-    w.tokens = min(item_tokens, iv[lo].end - w.row0);
-    w.p0 = pre[lo] + token0;
-    w.tiles = SpanTiles(w.p0, w.p0 + w.tokens - 1, a.window, a.sinks).n;
-    return w;
-  };
-  long long run = 0;
 #pragma unroll 1
-  for (int first = 0; first < n_items; first += kThreads) {
-    const int x = first + t;
-    long long tiles = 0;
-    if (x < n_items) {
-      const SpanItem w = record(x);
-      out[x] = w;
-      tiles = (long long)(w.tiles + a.unit_cost) * a.h_kv;
-    }
-    long long sum;
-    const long long at = block_scan(tiles, 0ll, s_sum, &sum);
-    if (x < n_items) cum[x] = run + at;
-    run += sum;
-    __syncthreads();
-  }
-
-  // cuts: part c begins at place floor(c * total / parts) of the line, where a unit is its fixed cost
-  // and then its tiles; a cut in the fixed cost moves to the unit's beginning
-  SpanCut* cuts = reinterpret_cast<SpanCut*>(a.ws + a.layout.cuts);
-  int32_t* arrived = reinterpret_cast<int32_t*>(a.ws + a.layout.arrived);
-  int32_t* joins = reinterpret_cast<int32_t*>(a.ws + a.layout.joins);
-  for (int x = t; x < a.ctas * kSpanRows; x += kThreads) arrived[x] = 0;
-  const long long total = run;
-  const int parts = total < a.ctas ? (int)total : a.ctas;
-  // place(c) without 64-bit divisions per thread; the part that holds a place by an estimate and steps
-  const long long q = parts ? total / parts : 0;
-  const unsigned r = parts ? (unsigned)(total - q * parts) : 0u;
-  auto place = [&](int c) { return c * q + (unsigned)c * r / (unsigned)parts; };
-  const float per_place = total ? (float)parts / (float)total : 0.f;
-  auto part_of = [&](long long x) {
-    int c = min(parts - 1, (int)((float)x * per_place));
-    while (c > 0 && place(c) > x) --c;
-    while (c + 1 < parts && place(c + 1) <= x) ++c;
-    return c;
-  };
-  for (int c = t; c <= a.ctas; c += kThreads) {
-    const long long w = c < parts ? place(c) : total;
-    SpanCut cut = {};
-    cut.item = n_items;
-    if (w < total) {
-      int lo = 0, hi = n_items - 1;
+  for (int l = 0; l < p.lines; ++l) {
+    const PlanLine& line = p.line[l];
+    const int* base = l ? base1 : base0;
+    // items and the key tiles before each
+    SpanItem* out = reinterpret_cast<SpanItem*>(a.ws + line.at.items);
+    const int n_items = base[n];
+    long long* cum = n_items <= kCumSmem ? reinterpret_cast<long long*>(area)
+                                         : reinterpret_cast<long long*>(a.ws + line.at.cum);
+    auto record = [&](int x) {
+      int lo = 0, hi = n - 1;  // the last question whose first item is at or before x
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (cum[mid] <= w) lo = mid;
+        if (base[mid] <= x) lo = mid;
         else hi = mid - 1;
       }
-      cut.item = lo;
-      cut.record = record(lo);
-      const int size = cut.record.tiles + a.unit_cost;
-      const long long in = w - cum[lo];
-      cut.head = in < 0x7fffffffll ? (int)in / size : (int)(in / size);
-      const int at = (int)(in - (long long)cut.head * size);
-      cut.tile = max(0, at - a.unit_cost);
-      if (cut.tile > 0) {
-        const long long begin = w - cut.tile, end = w - at + size;  // its tiles
-        cut.first = part_of(begin);
-        cut.parts = part_of(end - 1) - cut.first + 1;
-        if (cut.first == c - 1 && cut.parts >= a.join_from) joins[atomicAdd(&s_joins, 1)] = c;
+      SpanItem w = {};
+      const int token0 = (x - base[lo]) * line.item_tokens;
+      w.question = lo;
+      w.row0 = iv[lo].begin + token0;
+      w.tokens = min(line.item_tokens, iv[lo].end - w.row0);
+      w.p0 = pre[lo] + token0;
+      w.tiles = SpanTiles(w.p0, w.p0 + w.tokens - 1, a.window, a.sinks).n;
+      return w;
+    };
+    long long run = 0;
+#pragma unroll 1
+    for (int first = 0; first < n_items; first += kThreads) {
+      const int x = first + t;
+      long long tiles = 0;
+      if (x < n_items) {
+        const SpanItem w = record(x);
+        out[x] = w;
+        tiles = (long long)(w.tiles + line.unit_cost) * a.h_kv;
       }
+      long long sum;
+      const long long at = block_scan(tiles, 0ll, s_sum, &sum);
+      if (x < n_items) cum[x] = run + at;
+      run += sum;
+      __syncthreads();
     }
-    cuts[c] = cut;
+
+    // cuts: part c begins at place floor(c * total / parts) of the line, where a unit is its fixed cost
+    // and then its tiles; a cut in the fixed cost moves to the unit's beginning
+    SpanCut* cuts = reinterpret_cast<SpanCut*>(a.ws + line.at.cuts);
+    int32_t* arrived = reinterpret_cast<int32_t*>(a.ws + line.at.arrived);
+    int32_t* joins = reinterpret_cast<int32_t*>(a.ws + line.at.joins);
+    for (int x = t; x < line.ctas * kSpanRows; x += kThreads) arrived[x] = 0;
+    const long long total = run;
+    const int parts = total < line.ctas ? (int)total : line.ctas;
+    // place(c) without 64-bit divisions per thread; the part that holds a place by an estimate and steps
+    const long long q = parts ? total / parts : 0;
+    const unsigned r = parts ? (unsigned)(total - q * parts) : 0u;
+    auto place = [&](int c) { return c * q + (unsigned)c * r / (unsigned)parts; };
+    const float per_place = total ? (float)parts / (float)total : 0.f;
+    auto part_of = [&](long long x) {
+      int c = min(parts - 1, (int)((float)x * per_place));
+      while (c > 0 && place(c) > x) --c;
+      while (c + 1 < parts && place(c + 1) <= x) ++c;
+      return c;
+    };
+    for (int c = t; c <= line.ctas; c += kThreads) {
+      const long long w = c < parts ? place(c) : total;
+      SpanCut cut = {};
+      cut.item = n_items;
+      if (w < total) {
+        int lo = 0, hi = n_items - 1;
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (cum[mid] <= w) lo = mid;
+          else hi = mid - 1;
+        }
+        cut.item = lo;
+        cut.record = record(lo);
+        const int size = cut.record.tiles + line.unit_cost;
+        const long long in = w - cum[lo];
+        cut.head = in < 0x7fffffffll ? (int)in / size : (int)(in / size);
+        const int at = (int)(in - (long long)cut.head * size);
+        cut.tile = max(0, at - line.unit_cost);
+        if (cut.tile > 0) {
+          const long long begin = w - cut.tile, end = w - at + size;  // its tiles
+          cut.first = part_of(begin);
+          cut.parts = part_of(end - 1) - cut.first + 1;
+          if (cut.first == c - 1 && cut.parts >= line.join_from) joins[atomicAdd(&s_joins, 1)] = c;
+        }
+      }
+      cuts[c] = cut;
+    }
+    __syncthreads();
   }
-  __syncthreads();
   if (t == 0) hdr->n_joins = s_joins;
 }
 
 }  // namespace
 
-cudaError_t launch_span_plan(const SpanArgs& a, cudaStream_t s) {
+cudaError_t launch_span_plan(const SpanArgs& a, int lines, const SpanArgs* line0, const SpanArgs* line1, cudaStream_t s) {
+  PlanArgs p = {};
+  p.a = a;
+  p.lines = lines;
   // intervals, prefixes and first items of the questions, and beside them the largest of: the sort
   // keys, the bit map of the blocks, the tile counts of the items
   size_t area = 8;
   while (area < 8 * (size_t)a.n) area <<= 1;
   const size_t map = a.pool_elem ? ((size_t)a.n_blocks + 63) / 64 * 8 : 0;
-  const int64_t items = a.attend ? (int64_t)a.T / (a.tile_tokens * a.item_tiles) + a.n : 0;
-  const size_t cum = items < kCumSmem ? 8 * (size_t)items : 8 * kCumSmem;
   area = area > map ? area : map;
-  area = area > cum ? area : cum;
-  const size_t smem = 16 * (size_t)a.n + 16 + area;
-  constexpr int kMost = 16 * kMaxQuestions + 16 + kSpanMaxBlocks / 8;
+  for (int l = 0; l < lines; ++l) {
+    const SpanArgs& x = l ? *line1 : *line0;
+    const int item_tokens = x.tile_tokens * x.item_tiles;
+    p.line[l] = {x.line, item_tokens, x.min_tokens, x.max_tokens, x.ctas, x.unit_cost, x.join_from};
+    const int64_t items = (int64_t)a.T / item_tokens + a.n;
+    const size_t cum = items < kCumSmem ? 8 * (size_t)items : 8 * kCumSmem;
+    area = area > cum ? area : cum;
+  }
+  const size_t smem = 20 * (size_t)a.n + 24 + area;
+  constexpr int kMost = 20 * kMaxQuestions + 24 + kSpanMaxBlocks / 8;
   static_assert(kMost <= 220 * 1024, "shared memory of the plan");
   if (smem > 40 * 1024) {  // always the same limit: calls from several threads do not lower each other's
     const cudaError_t e = cudaFuncSetAttribute(span_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
     if (e != cudaSuccess) return e;
   }
-  return launch_pdl(span_plan_kernel, dim3(1), dim3(kThreads), smem, s, a);
+  return launch_pdl(span_plan_kernel, dim3(1), dim3(kThreads), smem, s, p);
 }
 
 }  // namespace kev

@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
       }
       if (ok && !whole) {  // the warp that finishes a row's last piece joins them all, in their order
         const int first = w.first(), parts = w.parts();
-        int32_t* arrived = reinterpret_cast<int32_t*>(a.ws + a.layout.arrived) + first * kSpanRows;
+        int32_t* arrived = reinterpret_cast<int32_t*>(a.ws + a.line.arrived) + first * kSpanRows;
         __threadfence();
         __syncwarp();
         uint32_t all = __ballot_sync(0xffffffffu, lane < rows && atomicAdd(arrived + min(lane, kSpanRows - 1), lane < rows) == parts - 1);
@@ -786,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
             __syncwarp();
             int before = 0;
             if (lane == 0)
-              before = atomicAdd(reinterpret_cast<int32_t*>(a.ws + a.layout.arrived) + w.first() * kSpanRows + row, 1);
+              before = atomicAdd(reinterpret_cast<int32_t*>(a.ws + a.line.arrived) + w.first() * kSpanRows + row, 1);
             if (__shfl_sync(0xffffffffu, before, 0) == w.parts() - 1) {
               __threadfence();
               join_pieces<D>(a, w.item, w.head, row, w.first(), w.parts());

@@ -184,8 +184,8 @@ __global__ void __launch_bounds__(256) span_merge_kernel(SpanArgs a) {
   pdl_trigger();
   const SpanHeader* h = reinterpret_cast<const SpanHeader*>(a.ws);
   if (h->status != ST_OK) return;
-  const SpanCut* cuts = reinterpret_cast<const SpanCut*>(a.ws + a.layout.cuts);
-  const int32_t* joins = reinterpret_cast<const int32_t*>(a.ws + a.layout.joins);
+  const SpanCut* cuts = reinterpret_cast<const SpanCut*>(a.ws + a.line.cuts);
+  const int32_t* joins = reinterpret_cast<const int32_t*>(a.ws + a.line.joins);
   const float2* ml = reinterpret_cast<const float2*>(a.ws + a.layout.part_ml);
   const float* po = reinterpret_cast<const float*>(a.ws + a.layout.part_o);
   const int per = a.layout.rows * (D / 8);

@@ -653,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool mine_first = w.j0 == 0;
           float* po = reinterpret_cast<float*>(a.ws + a.layout.part_o);
           float2* ml = reinterpret_cast<float2*>(a.ws + a.layout.part_ml);
-          int32_t* arrived = reinterpret_cast<int32_t*>(a.ws + a.layout.arrived) + first * kSpanRows + warp;
+          int32_t* arrived = reinterpret_cast<int32_t*>(a.ws + a.line.arrived) + first * kSpanRows + warp;
           int there = 0;
           if (parts == 2) {
             if (lane == 0) asm volatile("ld.acquire.gpu.b32 %0, [%1];" : "=r"(there) : "l"(arrived) : "memory");

@@ -164,6 +164,19 @@ def test_decode_steps_with_max_chunk(dtype, pool, h_q, h_kv, d, mask):
     b.check(*_kv(b.caches()), *mask)
 
 
+@pytest.mark.parametrize("pool", ["bf16", "e4m3"])
+@pytest.mark.parametrize("h_q,h_kv,d,mask", [(8, 2, 128, (0, 0)), (28, 4, 128, (150, 3)), (16, 1, 64, (0, 0)), (4, 4, 64, (64, 1))])
+def test_mixed_rounds_of_chunks_and_single_tokens(pool, h_q, h_kv, d, mask):
+    """A scheduler's round: many questions with one or two tokens beside a few longer chunks and an empty one."""
+    r = np.random.default_rng(h_q)
+    lens = [1] * 30 + [150, 2, 0, 40, 3]
+    prefix = r.integers(0, 700, len(lens)).tolist()
+    b = Span(70 + h_q, lens, prefix, h_q, h_kv, d, "bf16", pool, gaps=1, order=r.permutation(len(lens)).tolist())
+    b.chunk(*mask)
+    b.ok()
+    b.check(*_kv(b.caches()), *mask)
+
+
 @pytest.mark.parametrize("n,prefix", [(1, 30000), (2, 9000), (300, 40)])
 @pytest.mark.parametrize("pool", ["bf16", "e4m3"])
 def test_one_long_cache_is_split_and_many_short_ones_are_not(n, prefix, pool):
