@@ -151,10 +151,25 @@ def _ptr(x) -> Optional[int]:
     return x.data_ptr()
 
 
+def _current_stream() -> int:
+    """torch's current stream on the current device (the raw handle where torch hands it out: a Stream
+    object costs a call 3 us on the host, more than its launches)."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    raw = getattr(_torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None or not _torch.cuda.is_initialized():
+        return _torch.cuda.current_stream().cuda_stream
+    return raw(_torch.cuda.current_device())
+
+
+_torch = None
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
