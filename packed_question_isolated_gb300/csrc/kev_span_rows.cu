@@ -15,12 +15,13 @@
 //   warp 8      loads pages into a ring: TMA boxes of 16 positions, only those that some row sees
 //   warps 0-7   a warp takes 16 of a page's 128 positions, with a running reference maximum, sum and
 //               accumulator of its own, which it leaves in shared memory when the unit ends
-//               A warp that comes to positions of the chunk itself takes their K/V rows from the inputs:
-//               into the loaded page, and (quantised for e4m3) into the cache.  Every (unit, tile) has
-//               one owner, so a row is written once, and nobody waits for the write
-//   warp 9      joins the eight warps' results while they work on the next unit, and the pieces of a
-//               unit that a cut goes through, if its own piece is the last one done -- in the order of
-//               the pieces, so the result does not depend on which CTA that is
+//               A warp that comes to positions of the chunk itself puts their K/V rows into the loaded page
+//   warp 9      prepares those rows, up to two units ahead: from the inputs, quantised for e4m3, into the
+//               cache and into shared memory.  Every (unit, tile) has one owner, so a row is written
+//               once, and nobody waits for the write.  Between that it joins the eight warps' results
+//               while they work on the next unit, and the pieces of a unit that a cut goes through, if
+//               its own piece is the last one done -- in the order of the pieces, so the result does not
+//               depend on which CTA that is
 //
 // Registers instead of ldmatrix: the contraction index of an MMA may be permuted freely, so a lane
 // takes whole 16-byte chunks of a row (8 bf16 or 16 codes) as its share of several k-steps.  For K,
@@ -58,20 +59,25 @@ struct Smem {
   static constexpr int kJoinBytes = kWarps * 8 * kPad * 4;  // float [8 warps][8 rows][kPad]
   static constexpr int kQPitch = 2 * D + 16;                // bytes of a staged q row
   static constexpr int kQBytes = NT * 8 * kQPitch;          // q rows of a unit
-  static constexpr int kRoom = (kCtas == 2 ? 113 * 1024 : 226 * 1024) - 2048 - kJoinBytes - kWarps * 64 - 2 * kQBytes;
+  static constexpr int kNewRows = NT * 8;                   // new tokens of a unit at most
+  static constexpr int kNewBytes = kNewRows * (2 * kRow + 16);  // their K and V rows and scales
+  static constexpr int kRoom =
+      (kCtas == 2 ? 113 * 1024 : 226 * 1024) - 2048 - kJoinBytes - kWarps * 64 - 2 * kQBytes - 2 * kNewBytes;
   // A warp waits for the stages of its own turns only, so each stage has to belong to one set of warps
   // (a phase it did not wait for would pass for the one before): an even number with half pages.
   static constexpr int kStages = (kRoom / kStageBytes < 8 ? kRoom / kStageBytes : 8) / kHalves * kHalves;
   static constexpr int kJoin = kStages * kStageBytes;
   static constexpr int kMl = kJoin + kJoinBytes;            // float2 [8 warps][8 rows]
   static constexpr int kQ = kMl + kWarps * 64;              // two units' q rows
-  static constexpr int kBar = kQ + 2 * kQBytes;
+  static constexpr int kNew = kQ + 2 * kQBytes;             // two units' new rows
+  static constexpr int kBar = kNew + 2 * kNewBytes;
   static constexpr int kBytes = kBar + 256 + 1024;
 };
 
 struct Bars {
   uint64_t full[8], empty[8];
   uint64_t q_full[2], q_empty[2];
+  uint64_t new_full[2], new_empty[2];
   uint64_t join_full, join_empty;
   uint64_t join_empty8;  // the last unit's first 8 rows are joined
   int abort;
@@ -263,6 +269,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
     for (int u = 0; u < 2; ++u) {
       mbar_init(&bars->q_full[u], 1);
       mbar_init(&bars->q_empty[u], kWarps);
+      mbar_init(&bars->new_full[u], 1);
+      mbar_init(&bars->new_empty[u], kWarps);
     }
     mbar_init(&bars->join_full, kWarps);
     mbar_init(&bars->join_empty, 1);
@@ -342,9 +350,68 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
         mbar_wait(&bars->full[q % L::kStages], (q / L::kStages) & 1, never, kDrainBudget);
     }
   } else if (warp == kJoinWarp) {
+    // -------------------------------------------------------------------- new rows
+    bool ok = true;
+    uint32_t made = 0;
+    SpanWalk ahead(a, blockIdx.x);
+    auto new_rows = [&]() {  // of the next unit
+      if (!p.write || !ok || !ahead.live()) return;
+      if (made >= 2) ok = __all_sync(0xffffffffu, mbar_wait(&bars->new_empty[made & 1], (made / 2 - 1) & 1, abort_flag, budget));
+      if (!ok) return;
+      constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;  // lanes of a bf16 row
+      const int sub = lane % kLanes, p0 = ahead.item.p0, tokens = ahead.item.tokens;
+      const SpanTiles tiles(p0, p0 + tokens - 1, a.window, a.sinks);
+      const int32_t* row = a.table + (int64_t)ahead.item.question * a.max_blocks;
+      unsigned char* base = smem + L::kNew + (made & 1) * L::kNewBytes;
+      for (int x0 = 0; x0 < 2 * tokens; x0 += kAtOnce) {
+        const int x = x0 + lane / kLanes, token = x >> 1, pos = p0 + token, is_v = x & 1;
+        const int j = tiles.ns + pos / kPage - tiles.lo;  // its tile of the unit
+        const bool mine = token < tokens && j >= ahead.j0 && j < ahead.j1;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        int64_t cell = 0;
+        if (mine) {
+          v = reinterpret_cast<const uint4*>(is_v ? a.v : a.k)[((int64_t)(ahead.item.row0 + token) * a.h_kv + ahead.head) * kLanes + sub];
+          cell = ((int64_t)row[pos / kPage] * a.h_kv + ahead.head) * kPage + pos % kPage;
+        }
+        unsigned char* here = base + x * L::kRow;  // [token][K, V][kRow]
+        unsigned char* dst = static_cast<unsigned char*>(is_v ? a.pool_v : a.pool_k) + cell * L::kRow;
+        if (E == 2) {
+          if (mine) {
+            reinterpret_cast<uint4*>(here)[sub] = v;
+            reinterpret_cast<uint4*>(dst)[sub] = v;
+          }
+        } else {
+          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+          float f[8], top = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            f[e] = __uint_as_float(e & 1 ? u[e / 2] & 0xffff0000u : u[e / 2] << 16);
+            top = nan_max(top, fabsf(f[e]));
+          }
+#pragma unroll
+          for (int o = kLanes / 2; o > 0; o >>= 1) top = nan_max(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const float scale = span_scale(top);
+          span_quotients(f, scale);
+          const uint2 code = make_uint2(e4m3x2(f[0], f[1]) | e4m3x2(f[2], f[3]) << 16, e4m3x2(f[4], f[5]) | e4m3x2(f[6], f[7]) << 16);
+          if (mine) {
+            reinterpret_cast<uint2*>(here)[sub] = code;
+            reinterpret_cast<uint2*>(dst)[sub] = code;
+            if (sub == 0) {
+              reinterpret_cast<float*>(base + 2 * L::kNewRows * L::kRow)[x] = scale;
+              (is_v ? a.scale_v : a.scale_k)[cell] = scale;
+            }
+          }
+        }
+      }
+      mbar_arrive_warp(&bars->new_full[made & 1]);
+      ++made;
+      ahead.next();
+    };
+    new_rows();
+    new_rows();
+
     // -------------------------------------------------------------------- joins, of all units but the last
     uint32_t joins = 0;
-    bool ok = true;
     for (SpanWalk w(a, blockIdx.x); ok && w.live() && !w.ends(); w.next()) {
       const int rows = w.item.tokens * a.group;
       const bool whole = w.whole();
@@ -370,6 +437,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
         __threadfence();
         for (; all; all &= all - 1) join_pieces<D>(a, w.item, w.head, __ffs(all) - 1, first, parts);
       }
+      new_rows();
     }
     if (!ok && lane == 0) timeout();
   } else {
@@ -385,59 +453,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
       if (L::kPitch == 128)
         return tile + (ch >> 3) * (L::kKeys * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
       return tile + r * 64 + ((ch ^ (r >> 1 & 3)) << 4);
-    };
-    // a new token's K and V rows: into row r of the loaded tiles and into the cache, a lane per 1/32
-    auto put_rows = [&](int64_t src, int64_t cell, uint32_t tk, uint32_t tv, int r) {
-      constexpr int kN = D / 32;  // elements of a lane
-      uint32_t in[2][kN / 2];
-#pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        const uint32_t* from = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(v ? a.v : a.k) + src) + lane * (kN / 2);
-        if (kN == 4) {
-          const uint2 x = *reinterpret_cast<const uint2*>(from);
-          in[v][0] = x.x;
-          in[v][kN / 2 - 1] = x.y;
-        } else {
-          in[v][0] = *from;
-        }
-      }
-#pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        const int at_byte = lane * kN * E;  // of the row
-        const uint32_t to = at(v ? tv : tk, r, at_byte / 16) + at_byte % 16;
-        unsigned char* dst = static_cast<unsigned char*>(v ? a.pool_v : a.pool_k) + cell * L::kRow + at_byte;
-        if (E == 2) {
-#pragma unroll
-          for (int e = 0; e < kN / 2; ++e) {
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + 4 * e), "r"(in[v][e]) : "memory");
-            reinterpret_cast<uint32_t*>(dst)[e] = in[v][e];
-          }
-        } else {
-          float f[kN], top = 0.f;
-#pragma unroll
-          for (int e = 0; e < kN; ++e) {
-            f[e] = __uint_as_float(e & 1 ? in[v][e / 2] & 0xffff0000u : in[v][e / 2] << 16);
-            top = nan_max(top, fabsf(f[e]));
-          }
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) top = nan_max(top, __shfl_xor_sync(0xffffffffu, top, o));
-          const float scale = span_scale(top);
-          span_quotients(f, scale);
-          const uint32_t lo = e4m3x2(f[0], f[1]);
-          if (kN == 4) {
-            const uint32_t code = lo | e4m3x2(f[kN - 2], f[kN - 1]) << 16;
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(code) : "memory");
-            *reinterpret_cast<uint32_t*>(dst) = code;
-          } else {
-            asm volatile("st.shared.b16 [%0], %1;" ::"r"(to), "h"((uint16_t)lo) : "memory");
-            *reinterpret_cast<uint16_t*>(dst) = (uint16_t)lo;
-          }
-          if (lane == 0) {
-            asm volatile("st.shared.f32 [%0], %1;" ::"r"(tk + 2 * L::kTile + (v * L::kKeys + r) * 4), "f"(scale) : "memory");
-            (v ? a.scale_v : a.scale_k)[cell] = scale;
-          }
-        }
-      }
     };
     uint32_t seq = 0, n = 0, joins = 0;
     bool ok = true;
@@ -520,12 +535,23 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
         const int k0 = warp % L::kStageWarps * 16, u0 = h0 + k0;  // this warp's 16 positions of the stage
         if (group_seen(a, u0, p0, p1)) {
           const uint32_t tk = smem0 + s * L::kStageBytes, tv = tk + L::kTile;
-          if (p.write && u0 + 15 >= p0) {  // positions of the chunk among them
+          if (p.write && u0 + 15 >= p0) {  // positions of the chunk among them: their rows, from shared memory
+            const uint32_t from = (n - 1) & 1;
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars->new_full[from], ((n - 1) / 2) & 1, abort_flag, budget));
+            if (!ok) break;
+            const uint32_t rows0 = smem0 + L::kNew + from * L::kNewBytes;
+            constexpr int kWords = L::kRow / 16;  // 16-byte chunks of a row; lanes beyond K's and V's have none
 #pragma unroll 1
             for (int t = max(0, u0 - p0); t < w.item.tokens && p0 + t < u0 + 16; ++t) {
-              const int64_t src = ((int64_t)(w.item.row0 + t) * a.h_kv + w.head) * D, cell =
-                  ((int64_t)a.table[(int64_t)w.item.question * a.max_blocks + tiles.at(j)] * a.h_kv + w.head) * kPage + (p0 + t) % kPage;
-              put_rows(src, cell, tk, tv, k0 + p0 + t - u0);
+              const int r = k0 + p0 + t - u0;
+              if (lane < 2 * kWords) {
+                const uint4 x = lds128(rows0 + (2 * t) * L::kRow + lane * 16);
+                st_shared_v4(at(lane < kWords ? tk : tv, r, lane % kWords), x.x, x.y, x.z, x.w);
+              }
+              if (E == 1 && lane < 2) {
+                const float x = lds32(rows0 + 2 * L::kNewRows * L::kRow + (2 * t + lane) * 4);
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(tk + 2 * L::kTile + (lane * L::kKeys + r) * 4), "f"(x) : "memory");
+              }
             }
             __syncwarp();
             fence_proxy_async_smem();  // before the slot's next load
@@ -744,6 +770,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
         mbar_arrive_warp(&bars->empty[s]);
       }
 
+      if (!ok) break;
+      if (p.write) {  // every warp sees every phase, or a later one could pass for it
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->new_full[(n - 1) & 1], ((n - 1) / 2) & 1, abort_flag, budget));
+        if (!ok) break;
+        mbar_arrive_warp(&bars->new_empty[(n - 1) & 1]);
+      }
       // leave the results to the joining warp, 8 rows at a time
       const bool ends = w.ends();
 #pragma unroll
