@@ -530,7 +530,10 @@ const char* kev_status_string(kev_status status);
  * segments, table check, attention, paged write), 10 = kv_write_paged (3), 11 =
  * decode_attn_paged (2), 12 = prefill_chunk (3: segments, slot write, attention), 13 =
  * sample (1), 14 = lora_apply (1), 15 = decode_step (2: decode + merge on the tensor cores,
- * decode + advance otherwise).  -1 for an unknown id. */
+ * decode + advance otherwise), 16 = paged_write (2), 17 = paged_read (2), 18 = chunk_attn_paged
+ * (plan and attention for few rows per question, 2 and before any call; else plan, cache write if
+ * k is given, attention -- two kernels in a mixed round over an e4m3 cache -- and merge), 19 =
+ * prefill_attn_window (3: plan, attention, merge).  -1 for an unknown id. */
 int32_t kev_launch_count(int32_t entry_point);
 
 #ifdef __cplusplus

@@ -1,11 +1,16 @@
 // Host side of the span operators of include/kev.h: argument checks and launches.
 #include <math.h>
 
+#include <atomic>
+
 #include "kev_span.cuh"
 
 using namespace kev;
 
 namespace {
+
+// kernel launches of the most recent successful kev_chunk_attn_paged
+std::atomic<int32_t> g_chunk_launches{2};
 
 bool aligned(const void* p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
 
@@ -97,10 +102,20 @@ SpanArgs span_few_rows(const SpanArgs& call, int line, int rows, int sms) {
   return a;
 }
 
-kev_status span_attend(const SpanArgs& call, bool write, cudaStream_t s) {
+// Windows are at most 2^30 long (a longer one sees everything: positions end there), and sinks as many.
+kev_status span_mask(SpanArgs* a, int32_t window, int32_t sinks) {
+  if (window < 0 || sinks < 0) return KEV_ERR_INVALID_ARG;
+  a->window = window > (1 << 30) ? 0 : window;
+  a->sinks = sinks > (1 << 30) ? 1 << 30 : sinks;
+  return KEV_OK;
+}
+
+// Launches the attention; *launches: how many kernels.
+kev_status span_attend(const SpanArgs& call, bool write, int32_t* launches, cudaStream_t s) {
   const int sms = sms_of_current_device();
   if (sms <= 0) return KEV_ERR_CUDA;
   cudaError_t e;
+  *launches = 3 + write;
   if (call.elem == 4) {
     SpanArgs a = span_line(call, 0, 64, 1, 2 * sms);
     a.join_from = 2;
@@ -113,6 +128,7 @@ kev_status span_attend(const SpanArgs& call, bool write, cudaStream_t s) {
   const int64_t rows = (int64_t)call.max_chunk * call.group;
   if (call.pool_elem && rows <= 16) {  // few rows per question, and the caller said so
     const SpanArgs a = span_few_rows(call, 0, rows <= 8 ? 8 : 16, sms);
+    *launches = 2;
     e = launch_span_plan(call, 1, &a, nullptr, s);
     if (e == cudaSuccess) e = launch_span_rows(a, write, s);
     return from_cuda(e);
@@ -128,6 +144,7 @@ kev_status span_attend(const SpanArgs& call, bool write, cudaStream_t s) {
   // as much for 4 rows as for 256); over a bf16 cache it is the other way round, 122 against 111.
   const bool split = call.pool_elem == 1 && (int64_t)call.T * call.group <= 128 * (int64_t)call.n;
   if (split) {
+    ++*launches;
     SpanArgs b = span_few_rows(call, 1, call.group <= 8 ? 8 : 16, sms);
     b.max_tokens = b.tile_tokens;
     a.min_tokens = b.max_tokens + 1;
@@ -144,6 +161,8 @@ kev_status span_attend(const SpanArgs& call, bool write, cudaStream_t s) {
 }
 
 }  // namespace
+
+int32_t kev::chunk_launches() { return g_chunk_launches.load(); }
 
 extern "C" {
 
@@ -194,17 +213,20 @@ kev_status kev_chunk_attn_paged(const void* q, const void* k, const void* v, int
   kev_status st = span_common(&a, total_tokens, intervals, n_questions, shape, workspace, workspace_bytes, dev_status);
   if (st == KEV_OK) st = span_cache(&a, shape, prefix_lens, cache);
   if (st != KEV_OK) return st;
-  if (window < 0 || sinks < 0 || max_chunk < 0) return KEV_ERR_INVALID_ARG;
+  if (max_chunk < 0) return KEV_ERR_INVALID_ARG;
+  st = span_mask(&a, window, sinks);
+  if (st != KEV_OK) return st;
   if ((k == nullptr) != (v == nullptr) || !aligned(k, 16) || !aligned(v, 16)) return KEV_ERR_INVALID_ARG;
   if (total_tokens > 0 && (!q || !out || !aligned(q, 16) || !aligned(out, 16))) return KEV_ERR_INVALID_ARG;
   a.q = q;
   a.k = k;
   a.v = v;
   a.out = out;
-  a.window = window;
-  a.sinks = sinks;
   if (max_chunk > 0 && max_chunk < a.max_chunk) a.max_chunk = max_chunk;
-  return span_attend(a, k != nullptr, (cudaStream_t)stream);
+  int32_t launches;
+  st = span_attend(a, k != nullptr, &launches, (cudaStream_t)stream);
+  if (st == KEV_OK) g_chunk_launches = launches;
+  return st;
 }
 
 kev_status kev_prefill_attn_window(const void* q, const void* k, const void* v, int32_t total_tokens,
@@ -212,19 +234,18 @@ kev_status kev_prefill_attn_window(const void* q, const void* k, const void* v, 
                                    void* out, const kev_attn_shape* shape, void* workspace, size_t workspace_bytes,
                                    int32_t* dev_status, kev_stream_t stream) {
   SpanArgs a;
-  const kev_status st =
-      span_common(&a, total_tokens, intervals, n_questions, shape, workspace, workspace_bytes, dev_status);
+  kev_status st = span_common(&a, total_tokens, intervals, n_questions, shape, workspace, workspace_bytes, dev_status);
   if (st != KEV_OK) return st;
-  if (window < 0 || sinks < 0) return KEV_ERR_INVALID_ARG;
+  st = span_mask(&a, window, sinks);
+  if (st != KEV_OK) return st;
   if (total_tokens > 0 && (!q || !k || !v || !out || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16)))
     return KEV_ERR_INVALID_ARG;
   a.q = q;
   a.k = k;
   a.v = v;
   a.out = out;
-  a.window = window;
-  a.sinks = sinks;
-  return span_attend(a, false, (cudaStream_t)stream);
+  int32_t launches;
+  return span_attend(a, false, &launches, (cudaStream_t)stream);
 }
 
 }  // extern "C"

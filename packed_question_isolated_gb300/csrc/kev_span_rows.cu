@@ -79,6 +79,7 @@ struct Bars {
   uint64_t q_full[2], q_empty[2];
   uint64_t new_full[2], new_empty[2];
   uint64_t join_full, join_empty;
+  uint64_t stall;        // timeout test hook: nothing ever arrives on it
   uint64_t join_empty8;  // the last unit's first 8 rows are joined
   int abort;
   int never;
@@ -89,7 +90,8 @@ struct RowsArgs {
   SpanArgs s;
   float scale_log2;
   long long wait_budget;
-  int write;
+  int32_t write;
+  int32_t test_stall;  // timeout test hook
 };
 
 __device__ __forceinline__ int perm(int s) {  // position of slot s: 0 5 2 7 4 1 6 3
@@ -275,6 +277,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
     mbar_init(&bars->join_full, kWarps);
     mbar_init(&bars->join_empty, 1);
     mbar_init(&bars->join_empty8, kWarps);
+    mbar_init(&bars->stall, 1);
     bars->abort = bars->never = 0;
     fence_mbar_init();
   }
@@ -302,7 +305,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
     constexpr int kBoxes = 2 * L::kSubs * L::kStageWarps;  // 16-position boxes of a stage: one per lane
     const int is_v = lane / (kBoxes / 2), sub = lane / L::kStageWarps % L::kSubs, grp = lane % L::kStageWarps;
     uint32_t seq = 0, n = 0;
-    bool ok = true;
+    bool ok = !(p.test_stall && blockIdx.x == 0) ||
+              __all_sync(0xffffffffu, mbar_wait(&bars->stall, 0, abort_flag, budget));
     for (SpanWalk w(a, blockIdx.x); ok && w.live(); w.next()) {
       const int p0 = w.item.p0, p1 = p0 + w.item.tokens - 1, rows = w.item.tokens * a.group;
       const SpanTiles tiles(p0, p1, a.window, a.sinks);
@@ -840,6 +844,7 @@ cudaError_t launch(const SpanArgs& a, bool write, cudaStream_t s) {
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.wait_budget = wait_budget_cycles();
   p.write = write;
+  p.test_stall = test_stall_requested();
   CUtensorMap mk, mv;
   const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)a.n_blocks * a.h_kv * kPage};
   const cuuint32_t box[2] = {(cuuint32_t)(L::kPitch / E), 16};

@@ -68,6 +68,7 @@ struct Bars {
   uint64_t sc_full[kScaleSlots];         // e4m3: scales of a key tile visible
   uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
   uint64_t drain[2];
+  uint64_t stall;  // timeout test hook: nothing ever arrives on it
   uint32_t tmem;
   int abort;
   int never;
@@ -79,6 +80,7 @@ struct TcArgs {
   SpanArgs s;
   float scale_log2;
   long long wait_budget;
+  int32_t test_stall;  // timeout test hook
 };
 
 __device__ __forceinline__ void raise_timeout(const TcArgs& p, Bars* b) {
@@ -163,6 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars->o_free[t], 4);
       mbar_init(&bars->drain[t], 1);
     }
+    mbar_init(&bars->stall, 1);
     bars->abort = 0;
     bars->never = 0;
     fence_mbar_init();
@@ -201,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint64_t* full = Q8 ? bars->st_full : bars->full;
         uint64_t* empty = Q8 ? bars->st_empty : bars->empty;
         uint32_t seq = 0, tiles_done = 0;
-        bool ok = true;
+        bool ok = !(p.test_stall && blockIdx.x == 0) || mbar_wait(&bars->stall, 0, abort_flag, budget);
         for (SpanWalk w(a, blockIdx.x); ok && w.live(); w.next()) {
           const SpanTiles tiles(w.item.p0, w.item.p0 + w.item.tokens - 1, a.window, a.sinks);
           const int32_t* row = a.table ? a.table + (int64_t)w.item.question * a.max_blocks : nullptr;
@@ -770,6 +773,7 @@ cudaError_t launch(const SpanArgs& a, cudaStream_t s) {
   p.s = a;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.wait_budget = wait_budget_cycles();
+  p.test_stall = test_stall_requested();
   CUtensorMap mq = {}, mk = {}, mv = {};
   const cuuint64_t q_dims[3] = {(cuuint64_t)D, (cuuint64_t)a.h_q, (cuuint64_t)a.T};
   const cuuint32_t q_box[3] = {64, (cuuint32_t)a.group, (cuuint32_t)a.tile_tokens};
