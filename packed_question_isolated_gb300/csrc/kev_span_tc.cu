@@ -494,6 +494,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int u0 = tiles.at(j) * kBN;
           const bool edge = edge_tile(a, u0, p0, p1);
           const float4* sc = reinterpret_cast<const float4*>(smem + L::kScale + tiles_done % kScaleSlots * (2 * kBN * 4));
+          // Keys this row sees, as bits.  A warp's few tokens agree on most words of 32 keys: bit c of `full` where
+          // all its rows see all of word c.
+          uint32_t seen[4], full = 0;
+          auto look = [&]() {
+            if (!edge) return;
+            const int hi = pos - u0, lo = a.window ? hi - a.window + 1 : 0, below = a.sinks - u0;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              seen[c] = seen_bits(c, hi, lo, below);
+              full |= (unsigned)__all_sync(0xffffffffu, seen[c] == 0xffffffffu) << c;
+            }
+          };
+          if (!Q8) look();  // while S is computed (over e4m3 the registers are short: 344 us against 339 so)
           if (!warp_wait(&bars->s_full[t], s_cnt & 1, abort_flag, budget) ||
               (Q8 && !warp_wait(&bars->sc_full[tiles_done % kScaleSlots], (tiles_done / kScaleSlots) & 1, abort_flag, budget))) {
             ok = false;
@@ -511,16 +524,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < 4; ++c) tmem_ld32(tm_s + c * 32, sr[c]);
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_ld_wait(sr[c]);
+          if (Q8) look();
           if (edge) {
-            // Keys this row sees, as bits.  A warp's few tokens agree on most words of 32 keys.
-            const int hi = pos - u0, lo = a.window ? hi - a.window + 1 : 0, below = a.sinks - u0;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              const uint32_t seen = seen_bits(c, hi, lo, below);
-              if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
+              if (full >> c & 1u) continue;
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if (!(seen >> e & 1u)) sr[c][e] = __float_as_uint(-INFINITY);
+                if (!(seen[c] >> e & 1u)) sr[c][e] = __float_as_uint(-INFINITY);
             }
           }
           auto row_max = [&]() -> float {
