@@ -10,8 +10,7 @@
 // tile (or an extra trip of the unpacked codes through shared memory, which at HBM speed is more than
 // shared memory carries); the matrix pipe stays below half its time.
 //
-// Two persistent CTAs per SM (one with 16 rows) walk their equal parts of the work line
-// (kev_span.cuh), so one's beginnings and ends of units lie beside the other's streaming:
+// One or two persistent CTAs per SM walk their equal parts of the work line (kev_span.cuh):
 //   warp 8      loads pages into a ring: TMA boxes of 16 positions, only those that some row sees
 //   warps 0-7   a warp takes 16 of a page's 128 positions, with a running reference maximum, sum and
 //               accumulator of its own, which it leaves in shared memory when the unit ends
@@ -37,23 +36,26 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kWarps = 8;  // of 16 positions each
+constexpr int kWarps = 8;  // of 16 positions each: a page
 constexpr int kThreads = (kWarps + 2) * 32;
 constexpr int kLoadWarp = kWarps, kJoinWarp = kWarps + 1;
 constexpr float kBig = 1.8446744e19f;  // 2^64: a weight above it moves the reference
 constexpr long long kDrainBudget = 4000000000ll;
 
+// CTAs per SM.  Two, so that one's beginnings and ends of units lie beside the other's streaming, where the
+// registers (8 rows) and the pages (at most 32 KB for K and V) let them: e4m3 decode of 16 long caches
+// 82 us against 94 with one.  A bf16 page at d = 128 takes 64 KB: one CTA with 3 pages in flight, 115 us for
+// 16 caches of 2 to 32 Ki positions against 121 with two and half pages.
+constexpr int few_rows_ctas(int d, int elem, int tiles) { return tiles == 1 && d * elem < 256 ? 2 : 1; }
+
 template <int D, int E, int NT>
 struct Smem {
-  static constexpr int kCtas = NT == 1 ? 2 : 1;             // per SM
-  static constexpr int kKeys = E == 2 ? 64 : 128;           // positions of a stage: half a page, or a page
-  static constexpr int kHalves = kPage / kKeys;
-  static constexpr int kStageWarps = kKeys / 16;            // a stage's warps; with half pages two sets take turns
+  static constexpr int kCtas = few_rows_ctas(D, E, NT);     // per SM
   static constexpr int kRow = D * E;                        // bytes of a cached row
   static constexpr int kPitch = kRow < 128 ? kRow : 128;    // row of a swizzled sub-tile
   static constexpr int kSubs = kRow / kPitch;
-  static constexpr int kTile = kKeys * kRow;                // K or V of a stage
-  static constexpr int kScales = E == 1 ? 2 * kKeys * 4 : 0;
+  static constexpr int kTile = kPage * kRow;                // K or V of a stage
+  static constexpr int kScales = E == 1 ? 2 * kPage * 4 : 0;
   static constexpr int kStageBytes = 2 * kTile + (kScales + 1023) / 1024 * 1024;
   static constexpr int kPad = D + 4;                        // floats of a row in the join buffer
   static constexpr int kJoinBytes = kWarps * 8 * kPad * 4;  // float [8 warps][8 rows][kPad]
@@ -63,9 +65,7 @@ struct Smem {
   static constexpr int kNewBytes = kNewRows * (2 * kRow + 16);  // their K and V rows and scales
   static constexpr int kRoom =
       (kCtas == 2 ? 113 * 1024 : 226 * 1024) - 2048 - kJoinBytes - kWarps * 64 - 2 * kQBytes - 2 * kNewBytes;
-  // A warp waits for the stages of its own turns only, so each stage has to belong to one set of warps
-  // (a phase it did not wait for would pass for the one before): an even number with half pages.
-  static constexpr int kStages = (kRoom / kStageBytes < 8 ? kRoom / kStageBytes : 8) / kHalves * kHalves;
+  static constexpr int kStages = kRoom / kStageBytes < 8 ? kRoom / kStageBytes : 8;
   static constexpr int kJoin = kStages * kStageBytes;
   static constexpr int kMl = kJoin + kJoinBytes;            // float2 [8 warps][8 rows]
   static constexpr int kQ = kMl + kWarps * 64;              // two units' q rows
@@ -161,10 +161,9 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
   return r;
 }
 
-// Some row of the item (tokens at p0 .. p1) sees one of positions u .. u + N - 1.
-template <int N = 16>
+// Some row of the item (tokens at p0 .. p1) sees one of positions u .. u + 15.
 __device__ __forceinline__ bool group_seen(const SpanArgs& a, int u, int p0, int p1) {
-  return u <= p1 && (a.window == 0 || p0 - (u + N - 1) < a.window || u < a.sinks);
+  return u <= p1 && (a.window == 0 || p0 - (u + 15) < a.window || u < a.sinks);
 }
 
 // A row of the output: D / 32 consecutive dims per lane.
@@ -253,7 +252,7 @@ __device__ __forceinline__ void store_piece(const SpanArgs& a, int64_t slot, con
 }
 
 template <int D, int E, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, few_rows_ctas(D, E, NT))
     span_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ RowsArgs p) {
   using L = Smem<D, E, NT>;
@@ -266,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < 8; ++s) {
       mbar_init(&bars->full[s], 1);
-      mbar_init(&bars->empty[s], L::kStageWarps);
+      mbar_init(&bars->empty[s], kWarps);
     }
     for (int u = 0; u < 2; ++u) {
       mbar_init(&bars->q_full[u], 1);
@@ -302,8 +301,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
 
   if (warp == kLoadWarp) {
     // -------------------------------------------------------------------- page loads
-    constexpr int kBoxes = 2 * L::kSubs * L::kStageWarps;  // 16-position boxes of a stage: one per lane
-    const int is_v = lane / (kBoxes / 2), sub = lane / L::kStageWarps % L::kSubs, grp = lane % L::kStageWarps;
+    constexpr int kBoxes = 2 * L::kSubs * kWarps;  // 16-position boxes of a page: one per lane
+    const int is_v = lane / (kBoxes / 2), sub = lane / kWarps % L::kSubs, grp = lane % kWarps;
     uint32_t seq = 0, n = 0;
     bool ok = !(p.test_stall && blockIdx.x == 0) ||
               __all_sync(0xffffffffu, mbar_wait(&bars->stall, 0, abort_flag, budget));
@@ -325,26 +324,23 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
       for (int j = w.j0; ok && j < w.j1; ++j) {
         if ((j - w.j0) % 32 == 0) ids = j + lane < w.j1 ? row[tiles.at(j + lane)] : 0;  // 32 pages ahead
         const int block = __shfl_sync(0xffffffffu, ids, (j - w.j0) % 32);
-        for (int half = 0; half < L::kHalves; ++half) {
-          const int u0 = tiles.at(j) * kPage + half * L::kKeys;
-          if (L::kHalves > 1 && !group_seen<L::kKeys>(a, u0, p0, p1)) continue;
-          const int s = seq % L::kStages;
-          if (seq >= L::kStages)
-            ok = __all_sync(0xffffffffu, mbar_wait(&bars->empty[s], (seq / L::kStages - 1) & 1, abort_flag, budget));
-          if (!ok) break;
-          const bool mine = lane < kBoxes && group_seen(a, u0 + grp * 16, p0, p1);
-          const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
-          const int cell = (block * a.h_kv + w.head) * kPage + half * L::kKeys;
-          unsigned char* dst = smem + s * L::kStageBytes;
-          if (lane == 0) mbar_arrive_expect_tx(&bars->full[s], boxes * 16 * L::kPitch + L::kScales);
-          __syncwarp();
-          if (mine)
-            tma_load_2d(dst + is_v * L::kTile + (sub * L::kKeys + grp * 16) * L::kPitch, is_v ? &tm_v : &tm_k,
-                        sub * L::kPitch / E, cell + grp * 16, &bars->full[s]);
-          if (E == 1 && lane < 2)
-            bulk_load(dst + 2 * L::kTile + lane * L::kKeys * 4, (lane ? a.scale_v : a.scale_k) + cell, L::kKeys * 4, &bars->full[s]);
-          ++seq;
-        }
+        const int u0 = tiles.at(j) * kPage;
+        const int s = seq % L::kStages;
+        if (seq >= L::kStages)
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars->empty[s], (seq / L::kStages - 1) & 1, abort_flag, budget));
+        if (!ok) break;
+        const bool mine = lane < kBoxes && group_seen(a, u0 + grp * 16, p0, p1);
+        const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
+        const int cell = (block * a.h_kv + w.head) * kPage;
+        unsigned char* dst = smem + s * L::kStageBytes;
+        if (lane == 0) mbar_arrive_expect_tx(&bars->full[s], boxes * 16 * L::kPitch + L::kScales);
+        __syncwarp();
+        if (mine)
+          tma_load_2d(dst + is_v * L::kTile + (sub * kPage + grp * 16) * L::kPitch, is_v ? &tm_v : &tm_k, sub * L::kPitch / E,
+                      cell + grp * 16, &bars->full[s]);
+        if (E == 1 && lane < 2)
+          bulk_load(dst + 2 * L::kTile + lane * kPage * 4, (lane ? a.scale_v : a.scale_k) + cell, kPage * 4, &bars->full[s]);
+        ++seq;
       }
     }
     if (!ok && lane == 0) timeout();
@@ -455,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
     // swizzled address of 16-byte chunk ch of row r
     auto at = [&](uint32_t tile, int r, int ch) {
       if (L::kPitch == 128)
-        return tile + (ch >> 3) * (L::kKeys * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+        return tile + (ch >> 3) * (kPage * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
       return tile + r * 64 + ((ch ^ (r >> 1 & 3)) << 4);
     };
     uint32_t seq = 0, n = 0, joins = 0;
@@ -527,16 +523,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
 #pragma unroll
           for (int x = 0; x < 4; ++x) o[mt][nt][x] = 0.f;
 
-      for (int x = w.j0 * L::kHalves; x < w.j1 * L::kHalves; ++x) {
-        const int j = x / L::kHalves, half = x % L::kHalves;
-        const int h0 = tiles.at(j) * kPage + half * L::kKeys;
-        if (L::kHalves > 1 && !group_seen<L::kKeys>(a, h0, p0, p1)) continue;
-        const uint32_t here = seq++;
-        if (L::kHalves > 1 && (here & 1) != warp / L::kStageWarps) continue;  // the other warps' turn
-        const int s = here % L::kStages;
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->full[s], (here / L::kStages) & 1, abort_flag, budget));
+      for (int j = w.j0; j < w.j1; ++j, ++seq) {
+        const int s = seq % L::kStages;
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->full[s], (seq / L::kStages) & 1, abort_flag, budget));
         if (!ok) break;
-        const int k0 = warp % L::kStageWarps * 16, u0 = h0 + k0;  // this warp's 16 positions of the stage
+        const int k0 = warp * 16, u0 = tiles.at(j) * kPage + k0;  // this warp's 16 positions
         if (group_seen(a, u0, p0, p1)) {
           const uint32_t tk = smem0 + s * L::kStageBytes, tv = tk + L::kTile;
           if (p.write && u0 + 15 >= p0) {  // positions of the chunk among them: their rows, from shared memory
@@ -554,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
               }
               if (E == 1 && lane < 2) {
                 const float x = lds32(rows0 + 2 * L::kNewRows * L::kRow + (2 * t + lane) * 4);
-                asm volatile("st.shared.f32 [%0], %1;" ::"r"(tk + 2 * L::kTile + (lane * L::kKeys + r) * 4), "f"(x) : "memory");
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(tk + 2 * L::kTile + (lane * kPage + r) * 4), "f"(x) : "memory");
               }
             }
             __syncwarp();
@@ -593,8 +584,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
             const uint32_t sc = tk + 2 * L::kTile + r0 * 4;
             kf0 = lds32(sc);
             kf1 = lds32(sc + 32);
-            vf0 = lds32(sc + L::kKeys * 4);
-            vf1 = lds32(sc + L::kKeys * 4 + 32);
+            vf0 = lds32(sc + kPage * 4);
+            vf1 = lds32(sc + kPage * 4 + 32);
           }
           // every row sees all 16 positions
           const bool edge = !(u0 + 15 <= p0 && (a.window == 0 || p1 - u0 < a.window || u0 + 15 < a.sinks));
@@ -851,7 +842,7 @@ cudaError_t launch(const SpanArgs& a, bool write, cudaStream_t s) {
   const CUtensorMapSwizzle swizzle = L::kPitch == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
   if (!span_tensor_map(&mk, a.pool_k, E, 2, dims, box, swizzle) || !span_tensor_map(&mv, a.pool_v, E, 2, dims, box, swizzle))
     return cudaErrorInvalidValue;
-  static_assert(L::kStages >= 2 && L::kStages % L::kHalves == 0 && L::kCtas * (L::kBytes + 1024) <= 228 * 1024, "shared memory");
+  static_assert(L::kStages >= 2 && L::kCtas * (L::kBytes + 1024) <= 228 * 1024, "shared memory");
   const cudaError_t e =
       cudaFuncSetAttribute(span_rows_kernel<D, E, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
   if (e != cudaSuccess) return e;
@@ -864,6 +855,8 @@ cudaError_t launch_nt(const SpanArgs& a, bool write, cudaStream_t s) {
 }
 
 }  // namespace
+
+int span_rows_ctas(int d, int pool_elem, int rows) { return few_rows_ctas(d, pool_elem, rows / 8); }
 
 cudaError_t launch_span_rows(const SpanArgs& a, bool write, cudaStream_t s) {
   if (a.T <= 0) return cudaSuccess;
