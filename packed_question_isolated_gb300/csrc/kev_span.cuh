@@ -143,7 +143,7 @@ cudaError_t launch_span_read(const SpanArgs& a, void* k_out, void* v_out, int nu
 cudaError_t launch_span_simt(const SpanArgs& a, cudaStream_t s);  // fp32
 cudaError_t launch_span_tc(const SpanArgs& a, cudaStream_t s);    // bf16
 cudaError_t launch_span_rows(const SpanArgs& a, bool write, cudaStream_t s);  // bf16, at most 16 rows a question
-int span_rows_ctas(int d, int pool_elem, int rows);  // CTAs per SM of that kernel for 8 or 16 rows
+int span_rows_ctas(int d, int rows);  // CTAs per SM of that kernel for 8 or 16 rows
 cudaError_t launch_span_merge(const SpanArgs& a, int num_sms, cudaStream_t s);
 
 // Key tiles of tokens at positions p0 .. p1: tile j holds positions 128 * at(j) ...

@@ -96,11 +96,10 @@ SpanArgs span_line(const SpanArgs& call, int line, int rows, int tiles, int ctas
 // Every cached row meets at most 8 or 16 rows, which the register kernel takes at memory speed; it
 // joins its own pieces.
 SpanArgs span_few_rows(const SpanArgs& call, int line, int rows, int sms) {
-  const int ctas = span_rows_ctas(call.d, call.pool_elem, rows);
-  SpanArgs a = span_line(call, line, rows, 1, ctas * sms);
-  // Measured: e4m3 decode of 32 questions 31.4 us with 2, 33.6 with 1, 42.6 with 0; bf16 pages at d = 128
-  // take longer each: 64 questions 44.7 us with 1, 46.3 with 2 (16 rows: 85.6 with 2, 90.1 with 1)
-  a.unit_cost = ctas == 1 && rows == 8 ? 1 : 2;
+  SpanArgs a = span_line(call, line, rows, 1, span_rows_ctas(call.d, rows) * sms);
+  // Measured: e4m3 decode of 32 questions 29.2 us with 2, 32.1 with 1; bf16 pages at d = 128 take longer
+  // each: 64 questions 44.7 us with 1, 46.3 with 2 (16 rows: 85.6 with 2, 90.1 with 1)
+  a.unit_cost = call.pool_elem == 2 && call.d == 128 && rows == 8 ? 1 : 2;
   a.join_from = kSpanMaxCtas + 1;
   return a;
 }

@@ -42,15 +42,15 @@ constexpr int kLoadWarp = kWarps, kJoinWarp = kWarps + 1;
 constexpr float kBig = 1.8446744e19f;  // 2^64: a weight above it moves the reference
 constexpr long long kDrainBudget = 4000000000ll;
 
-// CTAs per SM.  Two, so that one's beginnings and ends of units lie beside the other's streaming, where the
-// registers (8 rows) and the pages (at most 32 KB for K and V) let them: e4m3 decode of 16 long caches
-// 82 us against 94 with one.  A bf16 page at d = 128 takes 64 KB: one CTA with 3 pages in flight, 115 us for
-// 16 caches of 2 to 32 Ki positions against 121 with two and half pages.
-constexpr int few_rows_ctas(int d, int elem, int tiles) { return tiles == 1 && d * elem < 256 ? 2 : 1; }
+// CTAs per SM.  Two, so that one's beginnings and ends of units lie beside the other's streaming, where
+// registers and pages are small: d = 64 with 8 rows (32 bf16 caches of 2 to 32 Ki positions 146 us against
+// 159 with one).  At d = 128 one, with every register and three to five pages in flight: 16 such bf16 caches
+// 115 us against 121, e4m3 decode of 32 short ones 29.2 against 31.1 (of 16 long ones 84.7 against 81.8).
+constexpr int few_rows_ctas(int d, int tiles) { return tiles == 1 && d == 64 ? 2 : 1; }
 
 template <int D, int E, int NT>
 struct Smem {
-  static constexpr int kCtas = few_rows_ctas(D, E, NT);     // per SM
+  static constexpr int kCtas = few_rows_ctas(D, NT);     // per SM
   static constexpr int kRow = D * E;                        // bytes of a cached row
   static constexpr int kPitch = kRow < 128 ? kRow : 128;    // row of a swizzled sub-tile
   static constexpr int kSubs = kRow / kPitch;
@@ -252,7 +252,7 @@ __device__ __forceinline__ void store_piece(const SpanArgs& a, int64_t slot, con
 }
 
 template <int D, int E, int NT>
-__global__ void __launch_bounds__(kThreads, few_rows_ctas(D, E, NT))
+__global__ void __launch_bounds__(kThreads, few_rows_ctas(D, NT))
     span_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ RowsArgs p) {
   using L = Smem<D, E, NT>;
@@ -856,7 +856,7 @@ cudaError_t launch_nt(const SpanArgs& a, bool write, cudaStream_t s) {
 
 }  // namespace
 
-int span_rows_ctas(int d, int pool_elem, int rows) { return few_rows_ctas(d, pool_elem, rows / 8); }
+int span_rows_ctas(int d, int rows) { return few_rows_ctas(d, rows / 8); }
 
 cudaError_t launch_span_rows(const SpanArgs& a, bool write, cudaStream_t s) {
   if (a.T <= 0) return cudaSuccess;
