@@ -137,27 +137,31 @@ __global__ void __launch_bounds__(kThreads) span_write_kernel(SpanArgs a) {
   for (; x < n_new; x += warps) {
     const Place at = next;  // looked up one token ahead
     if (x + warps < n_new) next = place_of(a, cu, x + warps);
-    const int64_t cell0 = at.block * a.h_kv * kPage + at.row;  // + head * kPage: the cached row
+    // this lane's places at head r0: heads r0 + kRows e lie at fixed distances from them
+    const int64_t from = ((int64_t)at.token * a.h_kv + r0) * kLanes + sub;
+    const int64_t cell0 = (at.block * a.h_kv + r0) * kPage + at.row;
     for (int g0 = 0; g0 < a.h_kv; g0 += kRows * kFlight) {
+      const int heads = a.h_kv - g0 - r0;  // e * kRows < heads: a head of this lane's
       uint4 w[2][kFlight];
 #pragma unroll
-      for (int v = 0; v < 2; ++v)
+      for (int v = 0; v < 2; ++v) {
+        if (split && v != side) continue;
+        const uint4* src = static_cast<const uint4*>(v ? a.v : a.k) + from + g0 * kLanes;
+#pragma unroll
+        for (int e = 0; e < kFlight; ++e)
+          w[v][e] = e * kRows < heads ? src[e * kRows * kLanes] : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        if (split && v != side) continue;
+        const int64_t cell = cell0 + (int64_t)g0 * kPage;
+        unsigned char* dst = static_cast<unsigned char*>(v ? a.pool_v : a.pool_k) + cell * (D * (Q8 ? 1 : E)) + sub * (Q8 ? V::n : 16);
+        float* dst_scale = Q8 ? (v ? a.scale_v : a.scale_k) + cell : nullptr;
 #pragma unroll
         for (int e = 0; e < kFlight; ++e) {
-          if (split && v != side) continue;
-          const int g = g0 + e * kRows + r0;
-          w[v][e] = g < a.h_kv ? static_cast<const uint4*>(v ? a.v : a.k)[((int64_t)at.token * a.h_kv + g) * kLanes + sub]
-                               : make_uint4(0u, 0u, 0u, 0u);
-        }
-#pragma unroll
-      for (int v = 0; v < 2; ++v)
-#pragma unroll
-        for (int e = 0; e < kFlight; ++e) {
-          if (split && v != side) continue;
-          const int g = g0 + e * kRows + r0;
-          const int64_t cell = cell0 + (int64_t)g * kPage;
+          unsigned char* at_e = dst + e * kRows * kPage * D * (Q8 ? 1 : E);
           if (!Q8) {
-            if (g < a.h_kv) static_cast<uint4*>(v ? a.pool_v : a.pool_k)[cell * kLanes + sub] = w[v][e];
+            if (e * kRows < heads) *reinterpret_cast<uint4*>(at_e) = w[v][e];
           } else {
             float f[V::n], top = V::top(w[v][e]);
             V::get(w[v][e], f);
@@ -168,14 +172,14 @@ __global__ void __launch_bounds__(kThreads) span_write_kernel(SpanArgs a) {
             uint32_t c[V::n / 4];
 #pragma unroll
             for (int i = 0; i < V::n / 4; ++i) c[i] = e4m3x2(f[4 * i], f[4 * i + 1]) | e4m3x2(f[4 * i + 2], f[4 * i + 3]) << 16;
-            if (g < a.h_kv) {
-              unsigned char* dst = static_cast<unsigned char*>(v ? a.pool_v : a.pool_k) + cell * D + sub * V::n;
-              if (V::n == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(c[0], c[V::n / 4 - 1]);
-              else *reinterpret_cast<uint32_t*>(dst) = c[0];
-              if (sub == 0) (v ? a.scale_v : a.scale_k)[cell] = scale;
+            if (e * kRows < heads) {
+              if (V::n == 8) *reinterpret_cast<uint2*>(at_e) = make_uint2(c[0], c[V::n / 4 - 1]);
+              else *reinterpret_cast<uint32_t*>(at_e) = c[0];
+              if (sub == 0) dst_scale[e * kRows * kPage] = scale;
             }
           }
         }
+      }
     }
   }
 }
