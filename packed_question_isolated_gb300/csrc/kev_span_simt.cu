@@ -135,20 +135,26 @@ __global__ void __launch_bounds__(kThreads, 2) span_simt_kernel(SpanArgs a) {
         // a masked key's V may hold anything: its product is left out, not multiplied by zero
         const bool edge = __any_sync(0xffffffffu, seen != (1u << kWarpRows) - 1);
         __syncwarp();
-        for (int u = 0; u < kSub; ++u) {
-          const unsigned vis = edge ? __shfl_sync(0xffffffffu, seen, u) : 0xffu;
+        auto product = [&](int u, unsigned vis) {
           const float4 pa = *reinterpret_cast<const float4*>(&sm.p[warp][u][0]);
           const float4 pb = *reinterpret_cast<const float4*>(&sm.p[warp][u][4]);
           const float p[kWarpRows] = {pa.x, pa.y, pa.z, pa.w, pb.x, pb.y, pb.z, pb.w};
           float v[kDims];
 #pragma unroll
-          for (int e = 0; e < kDims; ++e) v[e] = sm.v[u][kV == 4 ? lane * 4 + e : lane * 2 + e];
+          for (int e = 0; e < kDims; ++e) v[e] = sm.v[u][lane * kV + e];
 #pragma unroll
           for (int r = 0; r < kWarpRows; ++r) {
             if (!(vis >> r & 1)) continue;
 #pragma unroll
             for (int e = 0; e < kDims; ++e) o[r][e] = fmaf(p[r], v[e], o[r][e]);
           }
+        };
+        if (edge) {
+#pragma unroll 1
+          for (int u = 0; u < kSub; ++u) product(u, __shfl_sync(0xffffffffu, seen, u));
+        } else {
+#pragma unroll 4
+          for (int u = 0; u < kSub; ++u) product(u, 0xffu);
         }
         __syncwarp();
       }
