@@ -11,7 +11,9 @@
 // Bound by memory: 2 T H_kv (d elem + d + 4) bytes each way for an e4m3 cache.  A warp takes one
 // token's K and V rows of all kv heads: one search for the token's question (in shared memory) and
 // one page look-up, then 16-byte loads with up to 8 in flight per lane (8 heads of 128 bf16: exactly
-// 8; with 4, and the search in L2, the chain of look-ups held the copy to 60 % of the bandwidth).
+// 8).  Measured: 97k tokens of 8 heads read back in 100 us (6.0 TB/s, 88 % of the measured copy rate);
+// 27k tokens written in 42 us (4.0 TB/s: neither fewer instructions nor more bytes in flight moved it; the
+// writes land 128 bytes at a time, 16 KB apart).
 #include <cuda_fp8.h>
 
 #include "kev_span.cuh"
