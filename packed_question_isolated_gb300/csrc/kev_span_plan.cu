@@ -8,7 +8,7 @@
 // sinks are neither checked nor read: a serving program may have given them back.
 //
 // One CTA.  Latency bound: a handful of dependent passes over n questions, their pages and their
-// items -- 5 us for a batch without a cache, 7 to 8 with 500 to 2000 pages to look at.  Disjointness is one
+// items -- 5 us for a batch without a cache, 6 to 8 with 500 to 2000 pages to look at.  Disjointness is one
 // prefix maximum of the interval ends when the intervals come in order, and a sort first when they do
 // not.  Equal parts by key tiles (and a fixed cost per unit) rather than whole units, longest first: a
 // decode step has fewer units than SMs or a few more, of lengths that differ by 30.
@@ -17,7 +17,6 @@
 namespace kev {
 namespace {
 
-constexpr int kThreads = 1024;
 constexpr int kCumSmem = 4096;  // items whose tile counts are searched in shared memory
 
 // What of a work line the plan needs.
@@ -49,7 +48,7 @@ __device__ __forceinline__ long long join(long long a, long long b) { return a +
 __device__ __forceinline__ long long up(long long x, int o) { return __shfl_up_sync(0xffffffffu, x, o); }
 
 // Exclusive scan in thread order; two barriers.
-template <typename T>
+template <int kThreads, typename T>
 __device__ T block_scan(T v, T zero, T* tmp /* [33] */, T* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   T x = v;
@@ -63,7 +62,7 @@ __device__ T block_scan(T v, T zero, T* tmp /* [33] */, T* total) {
   if (lane == 31) tmp[warp] = x;
   __syncthreads();
   if (warp == 0) {
-    T w = tmp[lane];
+    T w = lane < kThreads / 32 ? tmp[lane] : zero;
 #pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
       const T y = up(w, o);
@@ -78,6 +77,7 @@ __device__ T block_scan(T v, T zero, T* tmp /* [33] */, T* total) {
   return join(tmp[warp], before);
 }
 
+template <int kThreads>
 __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(const __grid_constant__ PlanArgs p) {
   const SpanArgs& a = p.a;
   extern __shared__ unsigned long long dyn[];  // intervals, prefixes; sort keys, bit map of used blocks or tile counts
@@ -96,6 +96,11 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(const __grid_con
   for (int i = t; i < words; i += kThreads) used[i] = 0u;
   pdl_wait();
   pdl_trigger();
+#pragma unroll 1
+  for (int l = 0; l < p.lines; ++l) {
+    uint4* arrived = reinterpret_cast<uint4*>(a.ws + p.line[l].at.arrived);
+    for (int x = t; x < p.line[l].ctas * (kSpanRows / 4); x += kThreads) arrived[x] = make_uint4(0u, 0u, 0u, 0u);
+  }
   __syncthreads();
   SpanHeader* hdr = reinterpret_cast<SpanHeader*>(a.ws);
   int32_t* cu = reinterpret_cast<int32_t*>(a.ws + a.layout.cu);
@@ -130,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(const __grid_con
     }
   }
   Scan all;
-  const Scan before = block_scan(mine, Scan{}, s_scan, &all);
+  const Scan before = block_scan<kThreads>(mine, Scan{}, s_scan, &all);
 
   const bool clean = s_err == 0;  // the checks of single questions passed
   __syncthreads();
@@ -221,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(const __grid_con
       const int i = t * per + e;
       if (i < n && get(i).end > get(i).begin) v.end = max(v.end, get(i).end);
     }
-    const int first = block_scan(v, Scan{}, s_scan, &total).end;
+    const int first = block_scan<kThreads>(v, Scan{}, s_scan, &total).end;
     int end = first;
     for (int e = 0; e < per; ++e) {
       const int i = t * per + e;
@@ -232,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(const __grid_con
       }
     }
     __syncthreads();  // the scan's scratch is free
-    int at = block_scan(v, Scan{}, s_scan, &total).gaps;
+    int at = block_scan<kThreads>(v, Scan{}, s_scan, &total).gaps;
     end = first;
     for (int e = 0; e < per; ++e) {
       const int i = t * per + e;
@@ -303,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(const __grid_con
         tiles = (long long)(w.tiles + line.unit_cost) * a.h_kv;
       }
       long long sum;
-      const long long at = block_scan(tiles, 0ll, s_sum, &sum);
+      const long long at = block_scan<kThreads>(tiles, 0ll, s_sum, &sum);
       if (x < n_items) cum[x] = run + at;
       run += sum;
       __syncthreads();
@@ -312,15 +317,15 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(const __grid_con
     // cuts: part c begins at place floor(c * total / parts) of the line, where a unit is its fixed cost
     // and then its tiles; a cut in the fixed cost moves to the unit's beginning
     SpanCut* cuts = reinterpret_cast<SpanCut*>(a.ws + line.at.cuts);
-    int32_t* arrived = reinterpret_cast<int32_t*>(a.ws + line.at.arrived);
     int32_t* joins = reinterpret_cast<int32_t*>(a.ws + line.at.joins);
-    for (int x = t; x < line.ctas * kSpanRows; x += kThreads) arrived[x] = 0;
     const long long total = run;
     const int parts = total < line.ctas ? (int)total : line.ctas;
     // place(c) without 64-bit divisions per thread; the part that holds a place by an estimate and steps
     const long long q = parts ? total / parts : 0;
     const unsigned r = parts ? (unsigned)(total - q * parts) : 0u;
-    auto place = [&](int c) { return c * q + (unsigned)c * r / (unsigned)parts; };
+    // x / parts for x < 2^17 and parts < 2^9, by a rounded-up reciprocal (its error times x stays below 2^32)
+    const unsigned per_part = parts ? 0xffffffffu / (unsigned)parts + 1u : 0u;
+    auto place = [&](int c) { return c * q + (parts == 1 ? 0u : __umulhi((unsigned)c * r, per_part)); };
     const float per_place = total ? (float)parts / (float)total : 0.f;
     auto part_of = [&](long long x) {
       int c = min(parts - 1, (int)((float)x * per_place));
@@ -383,11 +388,16 @@ cudaError_t launch_span_plan(const SpanArgs& a, int lines, const SpanArgs* line0
   const size_t smem = 20 * (size_t)a.n + 24 + area;
   constexpr int kMost = 20 * kMaxQuestions + 24 + kSpanMaxBlocks / 8;
   static_assert(kMost <= 220 * 1024, "shared memory of the plan");
+  // Few threads scan faster, many look at more pages at once.  Measured with 256 and 1024: 64 packed questions
+  // 59.0 and 60.1 us, one question after 100 positions 10.5 and 11.7; 64 windowed decode steps over tables of 136
+  // pages 40.0 and 36.4, 32 short ones 29.9 and 29.0
+  const bool wide = a.n > 512 || (a.pool_elem && (int64_t)a.n * a.max_blocks > 512);
+  auto kern = wide ? span_plan_kernel<1024> : span_plan_kernel<256>;
   if (smem > 40 * 1024) {  // always the same limit: calls from several threads do not lower each other's
-    const cudaError_t e = cudaFuncSetAttribute(span_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
     if (e != cudaSuccess) return e;
   }
-  return launch_pdl(span_plan_kernel, dim3(1), dim3(kThreads), smem, s, p);
+  return launch_pdl(kern, dim3(1), dim3(wide ? 1024 : 256), smem, s, p);
 }
 
 }  // namespace kev
