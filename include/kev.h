@@ -416,7 +416,7 @@ size_t kev_paged_workspace_size(int32_t n_questions, int32_t total_tokens, const
 
 /* Rows begin_i + j of k and v [T, H_kv, d_h] into positions P_i + j of the cache, in its type
  * (quantised as above, or a bit copy).  No other cached row is touched.  prefix_lens: device
- * int32[n_questions].  Two kernels. */
+ * int32[n_questions].  One kernel for up to 512 tokens and questions (and 2^18 blocks), else two. */
 kev_status kev_paged_write(const void* k, const void* v, int32_t total_tokens, const kev_interval* intervals,
                            int32_t n_questions, const int32_t* prefix_lens, const kev_paged_cache* cache,
                            const kev_attn_shape* shape, void* workspace, size_t workspace_bytes, int32_t* dev_status,
@@ -424,7 +424,7 @@ kev_status kev_paged_write(const void* k, const void* v, int32_t total_tokens, c
 
 /* The way back: positions P_i + j of the cache into rows begin_i + j of k and v [T, H_kv, d_h], in
  * the shape's type (c_e * s rounded once, or a bit copy).  Rows of tokens in no interval are not
- * touched.  Two kernels. */
+ * touched.  Kernels as for the write. */
 kev_status kev_paged_read(void* k, void* v, int32_t total_tokens, const kev_interval* intervals, int32_t n_questions,
                           const int32_t* prefix_lens, const kev_paged_cache* cache, const kev_attn_shape* shape,
                           void* workspace, size_t workspace_bytes, int32_t* dev_status, kev_stream_t stream);
@@ -435,8 +435,8 @@ kev_status kev_paged_read(void* k, void* v, int32_t total_tokens, const kev_inte
  * g = h / G.  Rows of tokens in no interval are written as zeros.  k and v NULL: the rows are in
  * the cache already.  max_chunk: no question brings more tokens (0: not known); a caller that
  * knows, above all of a decode step (1), gets the kernel for few rows.
- * Arithmetic: bf16 q: products on the tensor cores, fp32 accumulation, softmax weights rounded to
- * bf16 for the product with V; fp32 q: fp32 throughout.  What masked positions hold, NaN and
+ * Arithmetic: bf16 q: products on the tensor cores, fp32 accumulation, softmax weights rounded for
+ * the product with V, to bf16 or (few rows over KEV_E4M3) to fp16; fp32 q: fp32 throughout.  What masked positions hold, NaN and
  * infinities among it, does not reach the result. */
 kev_status kev_chunk_attn_paged(const void* q, const void* k, const void* v, int32_t total_tokens,
                                 const kev_interval* intervals, int32_t n_questions, const int32_t* prefix_lens,
@@ -530,10 +530,11 @@ const char* kev_status_string(kev_status status);
  * segments, table check, attention, paged write), 10 = kv_write_paged (3), 11 =
  * decode_attn_paged (2), 12 = prefill_chunk (3: segments, slot write, attention), 13 =
  * sample (1), 14 = lora_apply (1), 15 = decode_step (2: decode + merge on the tensor cores,
- * decode + advance otherwise), 16 = paged_write (2), 17 = paged_read (2), 18 = chunk_attn_paged
- * (plan and attention for few rows per question, 2 and before any call; else plan, cache write if
- * k is given, attention -- two kernels in a mixed round over an e4m3 cache -- and merge), 19 =
- * prefill_attn_window (3: plan, attention, merge).  -1 for an unknown id. */
+ * decode + advance otherwise), 16 = paged_write, 17 = paged_read (1 for
+ * small calls, else 2: plan, copy), 18 = chunk_attn_paged (plan and attention for few rows per
+ * question, 2; else plan, cache write if k is given, attention -- two kernels in a mixed round over an
+ * e4m3 cache -- and merge), 19 = prefill_attn_window (3: plan, attention, merge).  16 to 18: the most
+ * recent call's, 2 before any.  -1 for an unknown id. */
 int32_t kev_launch_count(int32_t entry_point);
 
 #ifdef __cplusplus

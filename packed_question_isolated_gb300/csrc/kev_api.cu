@@ -917,8 +917,8 @@ int32_t kev_launch_count(int32_t entry_point) {
     case 13: return 1;
     case 14: return 1;
     case 15: return g_step_launches.load();
-    case 16: return 2;
-    case 17: return 2;
+    case 16: return paged_write_launches();
+    case 17: return paged_read_launches();
     case 18: return chunk_launches();
     case 19: return 3;
   }

@@ -356,8 +356,10 @@ kev_status decode_check_args(const void* q_new, const void* k_new, const void* v
 DecodeLayout decode_layout_of(int32_t n_questions, int32_t slot_cap, const kev_attn_shape* shape);
 cudaError_t launch_decode(const DecodeArgs& a, int d, kev_dtype dt, int num_sms, cudaStream_t s);     // CUDA cores
 cudaError_t launch_decode_tc(const DecodeArgs& a, int num_sms, cudaStream_t s);                       // bf16, d = 128
-// kev_span_api.cu: kernels of the most recent kev_chunk_attn_paged
+// kev_span_api.cu: kernels of the most recent kev_chunk_attn_paged, kev_paged_write, kev_paged_read
 int32_t chunk_launches();
+int32_t paged_write_launches();
+int32_t paged_read_launches();
 // lens[i] += 1 for active i; with `code` (a device word), only if *code is ST_OK
 cudaError_t launch_advance(int32_t* lens, const uint8_t* active, int32_t n, cudaStream_t s,
                            const int32_t* code = nullptr);

@@ -138,8 +138,10 @@ bool span_tensor_map(CUtensorMap* m, const void* base, int elem, int rank, const
 // The checks of a call, and the work lines of its attention launches: none for a cache write or read,
 // or one or two (same call, other line) whose questions between them are all that have tokens
 cudaError_t launch_span_plan(const SpanArgs& a, int lines, const SpanArgs* line0, const SpanArgs* line1, cudaStream_t s);
-cudaError_t launch_span_write(const SpanArgs& a, int num_sms, cudaStream_t s);
-cudaError_t launch_span_read(const SpanArgs& a, void* k_out, void* v_out, int num_sms, cudaStream_t s);
+// checked: behind a plan; else a small call (span_small_copy), which checks for itself
+bool span_small_copy(const SpanArgs& a);
+cudaError_t launch_span_write(const SpanArgs& a, bool checked, int num_sms, cudaStream_t s);
+cudaError_t launch_span_read(const SpanArgs& a, void* k_out, void* v_out, bool checked, int num_sms, cudaStream_t s);
 cudaError_t launch_span_simt(const SpanArgs& a, cudaStream_t s);  // fp32
 cudaError_t launch_span_tc(const SpanArgs& a, cudaStream_t s);    // bf16
 cudaError_t launch_span_rows(const SpanArgs& a, bool write, cudaStream_t s);  // bf16, at most 16 rows a question

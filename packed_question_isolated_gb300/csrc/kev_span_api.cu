@@ -9,8 +9,8 @@ using namespace kev;
 
 namespace {
 
-// kernel launches of the most recent successful kev_chunk_attn_paged
-std::atomic<int32_t> g_chunk_launches{2};
+// kernel launches of the most recent successful call of each
+std::atomic<int32_t> g_chunk_launches{2}, g_write_launches{2}, g_read_launches{2};
 
 bool aligned(const void* p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
 
@@ -122,7 +122,7 @@ kev_status span_attend(const SpanArgs& call, bool write, int32_t* launches, cuda
     SpanArgs a = span_line(call, 0, 64, 1, 2 * sms);
     a.join_from = 2;
     e = launch_span_plan(call, 1, &a, nullptr, s);
-    if (e == cudaSuccess && write) e = launch_span_write(a, sms, s);
+    if (e == cudaSuccess && write) e = launch_span_write(a, true, sms, s);
     if (e == cudaSuccess) e = launch_span_simt(a, s);
     if (e == cudaSuccess) e = launch_span_merge(a, sms, s);
     return from_cuda(e);
@@ -151,11 +151,11 @@ kev_status span_attend(const SpanArgs& call, bool write, int32_t* launches, cuda
     b.max_tokens = b.tile_tokens;
     a.min_tokens = b.max_tokens + 1;
     e = launch_span_plan(call, 2, &a, &b, s);
-    if (e == cudaSuccess && write) e = launch_span_write(call, sms, s);
+    if (e == cudaSuccess && write) e = launch_span_write(call, true, sms, s);
     if (e == cudaSuccess) e = launch_span_rows(b, false, s);
   } else {
     e = launch_span_plan(call, 1, &a, nullptr, s);
-    if (e == cudaSuccess && write) e = launch_span_write(call, sms, s);
+    if (e == cudaSuccess && write) e = launch_span_write(call, true, sms, s);
   }
   if (e == cudaSuccess) e = launch_span_tc(a, s);
   if (e == cudaSuccess) e = launch_span_merge(a, sms, s);
@@ -165,6 +165,8 @@ kev_status span_attend(const SpanArgs& call, bool write, int32_t* launches, cuda
 }  // namespace
 
 int32_t kev::chunk_launches() { return g_chunk_launches.load(); }
+int32_t kev::paged_write_launches() { return g_write_launches.load(); }
+int32_t kev::paged_read_launches() { return g_read_launches.load(); }
 
 extern "C" {
 
@@ -186,8 +188,10 @@ kev_status kev_paged_write(const void* k, const void* v, int32_t total_tokens, c
   if (sms <= 0) return KEV_ERR_CUDA;
   a.k = k;
   a.v = v;
-  cudaError_t e = launch_span_plan(a, 0, nullptr, nullptr, (cudaStream_t)stream);
-  if (e == cudaSuccess) e = launch_span_write(a, sms, (cudaStream_t)stream);
+  const bool small = span_small_copy(a);
+  cudaError_t e = small ? cudaSuccess : launch_span_plan(a, 0, nullptr, nullptr, (cudaStream_t)stream);
+  if (e == cudaSuccess) e = launch_span_write(a, !small, sms, (cudaStream_t)stream);
+  if (e == cudaSuccess) g_write_launches = small ? 1 : 2;
   return from_cuda(e);
 }
 
@@ -201,8 +205,10 @@ kev_status kev_paged_read(void* k, void* v, int32_t total_tokens, const kev_inte
   if (total_tokens > 0 && (!k || !v || !aligned(k, 16) || !aligned(v, 16))) return KEV_ERR_INVALID_ARG;
   const int sms = sms_of_current_device();
   if (sms <= 0) return KEV_ERR_CUDA;
-  cudaError_t e = launch_span_plan(a, 0, nullptr, nullptr, (cudaStream_t)stream);
-  if (e == cudaSuccess) e = launch_span_read(a, k, v, sms, (cudaStream_t)stream);
+  const bool small = span_small_copy(a);
+  cudaError_t e = small ? cudaSuccess : launch_span_plan(a, 0, nullptr, nullptr, (cudaStream_t)stream);
+  if (e == cudaSuccess) e = launch_span_read(a, k, v, !small, sms, (cudaStream_t)stream);
+  if (e == cudaSuccess) g_read_launches = small ? 1 : 2;
   return from_cuda(e);
 }
 

@@ -12,7 +12,7 @@
 // token's K and V rows of all kv heads: one search for the token's question (in shared memory) and
 // one page look-up, then 16-byte loads with up to 8 in flight per lane (8 heads of 128 bf16: exactly
 // 8).  Measured: 97k tokens of 8 heads read back in 100 us (6.0 TB/s, 88 % of the measured copy rate);
-// 27k tokens written in 42 us (4.0 TB/s: neither fewer instructions nor more bytes in flight moved it; the
+// 27k tokens written in 42.6 us (4.0 TB/s: neither fewer instructions nor more bytes in flight moved it; the
 // writes land 128 bytes at a time, 16 KB apart).
 #include <cuda_fp8.h>
 
@@ -22,6 +22,7 @@ namespace kev {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kSmallThreads = 512, kSmall = 512;  // of the one kernel for small calls: threads, tokens and questions
 
 // The prefix sums of the questions' lengths into shared memory, by the whole CTA.
 __device__ __forceinline__ const int32_t* share_cu(const SpanArgs& a) {
@@ -116,69 +117,57 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
   return r;
 }
 
-template <int E, int D, bool Q8>
-__global__ void __launch_bounds__(kThreads) span_write_kernel(SpanArgs a) {
+// A warp's copy of one token's rows of all kv heads into the cache: K and V, or with kOne (or `split`) only
+// side `side` of them.
+template <int E, int D, bool Q8, bool kOne>
+__device__ __forceinline__ void write_token(const SpanArgs& a, const Place& at, bool split, int side) {
   using V = Vec<E>;
   constexpr int kLanes = D / V::n;       // lanes of a row: 8, 16 or 32
   constexpr int kRows = 32 / kLanes;     // rows a warp handles at once
   constexpr int kFlight = 4;             // of those in flight
-  pdl_wait();
-  pdl_trigger();
-  const SpanHeader* h = reinterpret_cast<const SpanHeader*>(a.ws);
-  if (h->status != ST_OK) return;
-  const int32_t* cu = share_cu(a);
+  constexpr int kSides = kOne ? 1 : 2;
   const int lane = threadIdx.x & 31, sub = lane % kLanes, r0 = lane / kLanes;
-  const int warps = gridDim.x * (kThreads / 32);
-  const int n_new = h->n_new;
-  // few tokens: a warp for each of K and V
-  const int split = 2 * (int64_t)n_new <= warps;
-  int x = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
-  const int side = x & 1;
-  if (split) x >>= 1;
-  Place next = x < n_new ? place_of(a, cu, x) : Place{};
-  for (; x < n_new; x += warps) {
-    const Place at = next;  // looked up one token ahead
-    if (x + warps < n_new) next = place_of(a, cu, x + warps);
-    // this lane's places at head r0: heads r0 + kRows e lie at fixed distances from them
-    const int64_t from = ((int64_t)at.token * a.h_kv + r0) * kLanes + sub;
-    const int64_t cell0 = (at.block * a.h_kv + r0) * kPage + at.row;
-    for (int g0 = 0; g0 < a.h_kv; g0 += kRows * kFlight) {
-      const int heads = a.h_kv - g0 - r0;  // e * kRows < heads: a head of this lane's
-      uint4 w[2][kFlight];
+  // this lane's places at head r0: heads r0 + kRows e lie at fixed distances from them
+  const int64_t from = ((int64_t)at.token * a.h_kv + r0) * kLanes + sub;
+  const int64_t cell0 = (at.block * a.h_kv + r0) * kPage + at.row;
+  for (int g0 = 0; g0 < a.h_kv; g0 += kRows * kFlight) {
+    const int heads = a.h_kv - g0 - r0;  // e * kRows < heads: a head of this lane's
+    uint4 w[kSides][kFlight];
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        if (split && v != side) continue;
-        const uint4* src = static_cast<const uint4*>(v ? a.v : a.k) + from + g0 * kLanes;
+    for (int i = 0; i < kSides; ++i) {
+      const int v = kOne ? side : i;
+      if (split && v != side) continue;
+      const uint4* src = static_cast<const uint4*>(v ? a.v : a.k) + from + g0 * kLanes;
 #pragma unroll
-        for (int e = 0; e < kFlight; ++e)
-          w[v][e] = e * kRows < heads ? src[e * kRows * kLanes] : make_uint4(0u, 0u, 0u, 0u);
-      }
+      for (int e = 0; e < kFlight; ++e)
+        w[i][e] = e * kRows < heads ? src[e * kRows * kLanes] : make_uint4(0u, 0u, 0u, 0u);
+    }
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        if (split && v != side) continue;
-        const int64_t cell = cell0 + (int64_t)g0 * kPage;
-        unsigned char* dst = static_cast<unsigned char*>(v ? a.pool_v : a.pool_k) + cell * (D * (Q8 ? 1 : E)) + sub * (Q8 ? V::n : 16);
-        float* dst_scale = Q8 ? (v ? a.scale_v : a.scale_k) + cell : nullptr;
+    for (int i = 0; i < kSides; ++i) {
+      const int v = kOne ? side : i;
+      if (split && v != side) continue;
+      const int64_t cell = cell0 + (int64_t)g0 * kPage;
+      unsigned char* dst = static_cast<unsigned char*>(v ? a.pool_v : a.pool_k) + cell * (D * (Q8 ? 1 : E)) + sub * (Q8 ? V::n : 16);
+      float* dst_scale = Q8 ? (v ? a.scale_v : a.scale_k) + cell : nullptr;
 #pragma unroll
-        for (int e = 0; e < kFlight; ++e) {
-          unsigned char* at_e = dst + e * kRows * kPage * D * (Q8 ? 1 : E);
-          if (!Q8) {
-            if (e * kRows < heads) *reinterpret_cast<uint4*>(at_e) = w[v][e];
-          } else {
-            float f[V::n], top = V::top(w[v][e]);
-            V::get(w[v][e], f);
+      for (int e = 0; e < kFlight; ++e) {
+        unsigned char* at_e = dst + e * kRows * kPage * D * (Q8 ? 1 : E);
+        if (!Q8) {
+          if (e * kRows < heads) *reinterpret_cast<uint4*>(at_e) = w[i][e];
+        } else {
+          float f[V::n], top = V::top(w[i][e]);
+          V::get(w[i][e], f);
 #pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) top = nan_max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const float scale = span_scale(top);
-            span_quotients(f, scale);
-            uint32_t c[V::n / 4];
+          for (int o = kLanes / 2; o > 0; o >>= 1) top = nan_max(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const float scale = span_scale(top);
+          span_quotients(f, scale);
+          uint32_t c[V::n / 4];
 #pragma unroll
-            for (int i = 0; i < V::n / 4; ++i) c[i] = e4m3x2(f[4 * i], f[4 * i + 1]) | e4m3x2(f[4 * i + 2], f[4 * i + 3]) << 16;
-            if (e * kRows < heads) {
-              if (V::n == 8) *reinterpret_cast<uint2*>(at_e) = make_uint2(c[0], c[V::n / 4 - 1]);
-              else *reinterpret_cast<uint32_t*>(at_e) = c[0];
-              if (sub == 0) dst_scale[e * kRows * kPage] = scale;
-            }
+          for (int j = 0; j < V::n / 4; ++j) c[j] = e4m3x2(f[4 * j], f[4 * j + 1]) | e4m3x2(f[4 * j + 2], f[4 * j + 3]) << 16;
+          if (e * kRows < heads) {
+            if (V::n == 8) *reinterpret_cast<uint2*>(at_e) = make_uint2(c[0], c[V::n / 4 - 1]);
+            else *reinterpret_cast<uint32_t*>(at_e) = c[0];
+            if (sub == 0) dst_scale[e * kRows * kPage] = scale;
           }
         }
       }
@@ -186,16 +175,73 @@ __global__ void __launch_bounds__(kThreads) span_write_kernel(SpanArgs a) {
   }
 }
 
-template <int E, int D, bool Q8>
-__global__ void __launch_bounds__(kThreads) span_read_kernel(SpanArgs a, void* k_out, void* v_out) {
+// and back
+template <int E, int D, bool Q8, bool kOne>
+__device__ __forceinline__ void read_token(const SpanArgs& a, void* k_out, void* v_out, const Place& at, bool split, int side) {
   using V = Vec<E>;
-  constexpr int kLanes = D / V::n, kRows = 32 / kLanes, kFlight = 4;
+  constexpr int kLanes = D / V::n, kRows = 32 / kLanes, kFlight = 4, kSides = kOne ? 1 : 2;
+  const int lane = threadIdx.x & 31, sub = lane % kLanes, r0 = lane / kLanes;
+  const int64_t cell0 = at.block * a.h_kv * kPage + at.row;
+  for (int g0 = 0; g0 < a.h_kv; g0 += kRows * kFlight) {
+    uint4 w[kSides][kFlight];
+    float s[kSides][kFlight];
+#pragma unroll
+    for (int i = 0; i < kSides; ++i)
+#pragma unroll
+      for (int e = 0; e < kFlight; ++e) {
+        const int v = kOne ? side : i;
+        if (split && v != side) continue;
+        const int g = g0 + e * kRows + r0;
+        const int64_t cell = cell0 + (int64_t)g * kPage;
+        if (g >= a.h_kv) continue;
+        if (Q8) {
+          const unsigned char* src = static_cast<const unsigned char*>(v ? a.pool_v : a.pool_k) + cell * D + sub * V::n;
+          if (V::n == 8) {
+            const uint2 c = *reinterpret_cast<const uint2*>(src);
+            w[i][e] = make_uint4(c.x, c.y, 0u, 0u);
+          } else {
+            w[i][e].x = *reinterpret_cast<const uint32_t*>(src);
+          }
+          s[i][e] = (v ? a.scale_v : a.scale_k)[cell];
+        } else {
+          w[i][e] = static_cast<const uint4*>(v ? a.pool_v : a.pool_k)[cell * kLanes + sub];
+        }
+      }
+#pragma unroll
+    for (int i = 0; i < kSides; ++i)
+#pragma unroll
+      for (int e = 0; e < kFlight; ++e) {
+        const int v = kOne ? side : i;
+        if (split && v != side) continue;
+        const int g = g0 + e * kRows + r0;
+        if (g >= a.h_kv) continue;
+        uint4* dst = static_cast<uint4*>(v ? v_out : k_out) + ((int64_t)at.token * a.h_kv + g) * kLanes + sub;
+        if (Q8) {
+          const uint32_t c[2] = {w[i][e].x, w[i][e].y};
+          float f[V::n];
+#pragma unroll
+          for (int j = 0; j < V::n; j += 2) {
+            uint32_t half2;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(half2) : "h"((uint16_t)(c[j / 4] >> (j % 4 * 8))));
+            const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&half2));
+            f[j] = y.x * s[i][e];
+            f[j + 1] = y.y * s[i][e];
+          }
+          *dst = V::put(f);
+        } else {
+          *dst = w[i][e];
+        }
+      }
+  }
+}
+
+template <int E, int D, bool Q8, bool kRead>
+__global__ void __launch_bounds__(kThreads) span_copy_kernel(SpanArgs a, void* k_out, void* v_out) {
   pdl_wait();
   pdl_trigger();
   const SpanHeader* h = reinterpret_cast<const SpanHeader*>(a.ws);
   if (h->status != ST_OK) return;
   const int32_t* cu = share_cu(a);
-  const int lane = threadIdx.x & 31, sub = lane % kLanes, r0 = lane / kLanes;
   const int warps = gridDim.x * (kThreads / 32);
   const int n_new = h->n_new;
   // few tokens: a warp for each of K and V
@@ -207,57 +253,72 @@ __global__ void __launch_bounds__(kThreads) span_read_kernel(SpanArgs a, void* k
   for (; x < n_new; x += warps) {
     const Place at = next;  // looked up one token ahead
     if (x + warps < n_new) next = place_of(a, cu, x + warps);
-    const int64_t cell0 = at.block * a.h_kv * kPage + at.row;
-    for (int g0 = 0; g0 < a.h_kv; g0 += kRows * kFlight) {
-      uint4 w[2][kFlight];
-      float s[2][kFlight];
-#pragma unroll
-      for (int v = 0; v < 2; ++v)
-#pragma unroll
-        for (int e = 0; e < kFlight; ++e) {
-          if (split && v != side) continue;
-          const int g = g0 + e * kRows + r0;
-          const int64_t cell = cell0 + (int64_t)g * kPage;
-          if (g >= a.h_kv) continue;
-          if (Q8) {
-            const unsigned char* src = static_cast<const unsigned char*>(v ? a.pool_v : a.pool_k) + cell * D + sub * V::n;
-            if (V::n == 8) {
-              const uint2 c = *reinterpret_cast<const uint2*>(src);
-              w[v][e] = make_uint4(c.x, c.y, 0u, 0u);
-            } else {
-              w[v][e].x = *reinterpret_cast<const uint32_t*>(src);
-            }
-            s[v][e] = (v ? a.scale_v : a.scale_k)[cell];
-          } else {
-            w[v][e] = static_cast<const uint4*>(v ? a.pool_v : a.pool_k)[cell * kLanes + sub];
-          }
-        }
-#pragma unroll
-      for (int v = 0; v < 2; ++v)
-#pragma unroll
-        for (int e = 0; e < kFlight; ++e) {
-          if (split && v != side) continue;
-          const int g = g0 + e * kRows + r0;
-          if (g >= a.h_kv) continue;
-          uint4* dst = static_cast<uint4*>(v ? v_out : k_out) + ((int64_t)at.token * a.h_kv + g) * kLanes + sub;
-          if (Q8) {
-            const uint32_t c[2] = {w[v][e].x, w[v][e].y};
-            float f[V::n];
-#pragma unroll
-            for (int i = 0; i < V::n; i += 2) {
-              uint32_t half2;
-              asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(half2) : "h"((uint16_t)(c[i / 4] >> (i % 4 * 8))));
-              const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&half2));
-              f[i] = y.x * s[v][e];
-              f[i + 1] = y.y * s[v][e];
-            }
-            *dst = V::put(f);
-          } else {
-            *dst = w[v][e];
-          }
-        }
+    if (kRead) read_token<E, D, Q8, false>(a, k_out, v_out, at, split, side);
+    else write_token<E, D, Q8, false>(a, at, split, side);
+  }
+}
+
+// The checks of the plan (kev_span_plan.cu) and the copy in one kernel, for small calls: every CTA makes all
+// the checks for itself, in shared memory, and comes to the same verdict, so none has to wait for another.
+// Overlapping intervals show as a token that is marked twice; the mark is also the token's question.  A warp
+// copies one token's K or V.  Measured for one token of each of 32 questions 3.6 us, with two kernels 7.0; at the
+// ends of what it takes, a chunk of 512 tokens 4.9 against 7.3 and 512 questions of one token 9.0 against 15.6.
+template <int E, int D, bool Q8, bool kRead>
+__global__ void __launch_bounds__(kSmallThreads) span_small_copy_kernel(SpanArgs a, void* k_out, void* v_out) {
+  extern __shared__ unsigned small_smem[];
+  unsigned* used = small_smem;  // a bit per block
+  const int words = (a.n_blocks + 31) / 32, t = threadIdx.x, warp = t / 32, lane = t & 31;
+  __shared__ int2 s_iv[kSmall];
+  __shared__ int s_prefix[kSmall], s_owner[kSmall], s_err;
+  if (t == 0) s_err = 0;
+  for (int i = t; i < words; i += kSmallThreads) used[i] = 0u;
+  for (int i = t; i < a.T; i += kSmallThreads) s_owner[i] = -1;
+  pdl_wait();
+  pdl_trigger();
+  __syncthreads();
+  auto error = [&](int rank) { atomicMax(&s_err, 8 - rank); };  // ranks as in the plan
+  for (int i = t; i < a.n; i += kSmallThreads) {
+    const kev_interval v = a.intervals[i];
+    const int first = a.prefix[i];
+    s_iv[i] = make_int2(v.begin, v.end);
+    s_prefix[i] = first;
+    if (v.begin < 0 || v.end < v.begin || v.end > a.T) {
+      error(0);
+    } else if (v.end > v.begin) {
+      if (first < 0) error(1);
+      else if ((int64_t)first + (v.end - v.begin) > (int64_t)a.max_blocks * kPage) error(2);
     }
   }
+  __syncthreads();
+  const bool clean = s_err == 0;
+  __syncthreads();
+  if (clean) {
+    for (int i = t; i < a.n; i += kSmallThreads) {  // pages; a block's bit may be set once
+      const int L = s_iv[i].y - s_iv[i].x;
+      if (L <= 0) continue;
+      for (int e = s_prefix[i] / kPage; e <= (s_prefix[i] + L - 1) / kPage; ++e) {
+        const int b = a.table[(int64_t)i * a.max_blocks + e];
+        const unsigned bit = 1u << (b & 31);
+        if (b < 0 || b >= a.n_blocks || atomicOr(&used[b >> 5], bit) & bit) error(3);
+      }
+    }
+    for (int i = warp; i < a.n; i += kSmallThreads / 32)
+      for (int x = s_iv[i].x + lane; x < s_iv[i].y; x += 32)
+        if (atomicExch(&s_owner[x], i) >= 0) error(0);
+  }
+  __syncthreads();
+  if (blockIdx.x == 0 && t == 0 && a.dev_status) {
+    const int rank = 8 - s_err;
+    *a.dev_status = s_err == 0 ? ST_OK : rank == 0 ? ST_INTERVALS : rank == 1 ? ST_PREFIX : rank == 2 ? ST_OVERFLOW : ST_SLOT;
+  }
+  if (s_err) return;
+  const int y = blockIdx.x * (kSmallThreads / 32) + warp, x = y >> 1;
+  const int i = x < a.T ? s_owner[x] : -1;
+  if (i < 0) return;
+  const int p = s_prefix[i] + x - s_iv[i].x;
+  const Place at = {x, a.table[(int64_t)i * a.max_blocks + p / kPage], p % kPage};
+  if (kRead) read_token<E, D, Q8, true>(a, k_out, v_out, at, true, y & 1);
+  else write_token<E, D, Q8, true>(a, at, true, y & 1);
 }
 
 int grid_of(const SpanArgs& a, int num_sms) {  // two warps per token, 8 CTAs of 8 warps per SM at most
@@ -265,26 +326,36 @@ int grid_of(const SpanArgs& a, int num_sms) {  // two warps per token, 8 CTAs of
   return (int)(ctas < 8 * num_sms ? ctas : 8 * num_sms);
 }
 
-}  // namespace
-
-cudaError_t launch_span_write(const SpanArgs& a, int num_sms, cudaStream_t s) {
-  if (a.T <= 0) return cudaSuccess;
+template <int E, int D, bool Q8, bool kRead>
+cudaError_t launch(const SpanArgs& a, void* k_out, void* v_out, bool checked, int num_sms, cudaStream_t s) {
+  if (checked) return launch_pdl(span_copy_kernel<E, D, Q8, kRead>, dim3(grid_of(a, num_sms)), dim3(kThreads),
+                                 sizeof(int32_t) * (size_t)a.n, s, a, k_out, v_out);
+  const int per = kSmallThreads / 64;  // tokens of a CTA; without any the checks are left
+  return launch_pdl(span_small_copy_kernel<E, D, Q8, kRead>, dim3(a.T > 0 ? (a.T + per - 1) / per : 1), dim3(kSmallThreads),
+                    sizeof(int32_t) * (((size_t)a.n_blocks + 31) / 32), s, a, k_out, v_out);
+}
+template <bool kRead>
+cudaError_t launch_copy(const SpanArgs& a, void* k_out, void* v_out, bool checked, int num_sms, cudaStream_t s) {
   const bool q8 = a.pool_elem == 1;
-  auto kern = a.elem == 2 ? (a.d == 64 ? (q8 ? span_write_kernel<2, 64, true> : span_write_kernel<2, 64, false>)
-                                       : (q8 ? span_write_kernel<2, 128, true> : span_write_kernel<2, 128, false>))
-                          : (a.d == 64 ? (q8 ? span_write_kernel<4, 64, true> : span_write_kernel<4, 64, false>)
-                                       : (q8 ? span_write_kernel<4, 128, true> : span_write_kernel<4, 128, false>));
-  return launch_pdl(kern, dim3(grid_of(a, num_sms)), dim3(kThreads), sizeof(int32_t) * (size_t)a.n, s, a);
+  auto f = a.elem == 2 ? (a.d == 64 ? (q8 ? launch<2, 64, true, kRead> : launch<2, 64, false, kRead>)
+                                    : (q8 ? launch<2, 128, true, kRead> : launch<2, 128, false, kRead>))
+                       : (a.d == 64 ? (q8 ? launch<4, 64, true, kRead> : launch<4, 64, false, kRead>)
+                                    : (q8 ? launch<4, 128, true, kRead> : launch<4, 128, false, kRead>));
+  return f(a, k_out, v_out, checked, num_sms, s);
 }
 
-cudaError_t launch_span_read(const SpanArgs& a, void* k_out, void* v_out, int num_sms, cudaStream_t s) {
-  if (a.T <= 0) return cudaSuccess;
-  const bool q8 = a.pool_elem == 1;
-  auto kern = a.elem == 2 ? (a.d == 64 ? (q8 ? span_read_kernel<2, 64, true> : span_read_kernel<2, 64, false>)
-                                       : (q8 ? span_read_kernel<2, 128, true> : span_read_kernel<2, 128, false>))
-                          : (a.d == 64 ? (q8 ? span_read_kernel<4, 64, true> : span_read_kernel<4, 64, false>)
-                                       : (q8 ? span_read_kernel<4, 128, true> : span_read_kernel<4, 128, false>));
-  return launch_pdl(kern, dim3(grid_of(a, num_sms)), dim3(kThreads), sizeof(int32_t) * (size_t)a.n, s, a, k_out, v_out);
+}  // namespace
+
+// What the small kernel's shared memory holds without asking for more: 512 tokens and questions (every CTA
+// checks them all) and 2^18 blocks.
+bool span_small_copy(const SpanArgs& a) { return a.T <= kSmall && a.n <= kSmall && a.n_blocks <= 1 << 18; }
+
+cudaError_t launch_span_write(const SpanArgs& a, bool checked, int num_sms, cudaStream_t s) {
+  return a.T <= 0 && checked ? cudaSuccess : launch_copy<false>(a, nullptr, nullptr, checked, num_sms, s);
+}
+
+cudaError_t launch_span_read(const SpanArgs& a, void* k_out, void* v_out, bool checked, int num_sms, cudaStream_t s) {
+  return a.T <= 0 && checked ? cudaSuccess : launch_copy<true>(a, k_out, v_out, checked, num_sms, s);
 }
 
 }  // namespace kev

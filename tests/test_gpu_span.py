@@ -242,6 +242,81 @@ def test_write_and_read_back(dtype, d, pool, h_kv):
         assert torch.equal(got, wantrow)
 
 
+COPIES = [([1] * 32, [i * 9 for i in range(32)], 8), ([1], [128], 5), ([512], [77], 1), ([1, 0, 300, 129, 0, 60], [3, 5, 127, 0, 0, 250], 3),
+          ([1] * 512, [i % 140 for i in range(512)], 1), ([0, 0], [4, 0], 2)]
+
+
+@pytest.mark.parametrize("dtype,d,pool", [("bf16", 128, "e4m3"), ("fp32", 64, "e4m3"), ("bf16", 64, "bf16"), ("fp32", 128, "fp32")])
+@pytest.mark.parametrize("lens,prefix,h_kv", COPIES)
+def test_copies_of_small_calls_equal_those_of_large_ones(lens, prefix, h_kv, dtype, d, pool):
+    """Up to 512 tokens take one kernel; the same batch with rows of no question behind it takes two."""
+    order = np.random.default_rng(5).permutation(len(lens)).tolist()
+    b = Span(90, lens, prefix, h_kv, h_kv, d, dtype, pool, order=order, spare=3)
+    more = 600
+    k, v = (torch.cat([x, torch.zeros((more, h_kv, d), dtype=TD[dtype], device="cuda")]) for x in (b.k, b.v))
+    n, ws = len(lens), torch.full((kev.kev_paged_workspace_size(len(lens), b.T + more, b.shape),), 0xff, dtype=torch.uint8, device="cuda")
+    start = [(p.view(torch.uint8).clone(), None if s is None else s.clone()) for p, s in b.pools]
+    b.write()
+    b.ok()
+    small = [(p.view(torch.uint8).clone(), None if s is None else s.clone()) for p, s in b.pools]
+    for (p, s), (p0, s0) in zip(b.pools, start):
+        p.view(torch.uint8).copy_(p0)
+        if s is not None:
+            s.copy_(s0)
+    end = (b.shape, ws, ws.numel(), b.status)
+    kev.kev_paged_write(k, v, b.T + more, b.iv, n, b.pre, b.cache, *end)
+    b.ok()
+    for (p, s), (p0, s0), (p1, _) in zip(b.pools, small, start):
+        assert torch.equal(p.view(torch.uint8), p0) and (s is None or torch.equal(s, s0))
+        assert b.T == 0 or not torch.equal(p0, p1)
+    got = []
+    for t in (b.T, b.T + more):
+        ko, vo = torch.full_like(k, -7.0), torch.full_like(v, -9.0)
+        kev.kev_paged_read(ko, vo, t, b.iv, n, b.pre, b.cache, *end)
+        b.ok()
+        got.append((ko, vo))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+@pytest.mark.parametrize("what", ["overlap", "nested", "outside", "reversed", "prefix", "overflow", "range", "negative", "twice", "two"])
+@pytest.mark.parametrize("more", [0, 600])
+def test_copies_check_before_they_write(what, more):
+    b = Span(104, [5, 9, 1], [130, 40, 0], 4, 2, 128, "bf16", "e4m3")
+    if what == "overlap":
+        b.intervals[1, 0] -= 1
+    elif what == "nested":
+        b.intervals[2] = (2, 3)
+    elif what == "outside":
+        b.intervals[2, 1] = b.T + more + 1
+    elif what == "reversed":
+        b.intervals[0] = b.intervals[0][::-1]
+    elif what == "prefix":
+        b.prefix[1] = -1
+    elif what == "overflow":
+        b.prefix[1] = b.width * PAGE - 8
+    elif what == "range":
+        b.table[0, 1] = b.n_blocks
+    elif what == "negative":
+        b.table[1, 0] = -1
+    elif what == "twice":
+        b.table[1, 0] = b.table[0, 1]
+    else:  # a block used twice and an overlap: the overlap is reported
+        b.table[1, 0] = b.table[0, 1]
+        b.intervals[2] = (2, 3)
+    b.to_device()
+    code = O.validate_span(b.intervals, b.T + more, b.prefix, b.table, b.n_blocks, attend=False)
+    want = CODES[O.INTERVALS if what == "two" else code]
+    k, v = (torch.cat([x, torch.ones((more, 2, 128), dtype=x.dtype, device="cuda")]) for x in (b.k, b.v))
+    ws = torch.full((kev.kev_paged_workspace_size(3, b.T + more, b.shape),), 0xff, dtype=torch.uint8, device="cuda")
+    before = [(p.view(torch.uint8).clone(), s.clone()) for p, s in b.pools] + [(k.clone(), v.clone())]
+    for f in (kev.kev_paged_write, kev.kev_paged_read):
+        b.status.fill_(-1)
+        assert f(k, v, b.T + more, b.iv, 3, b.pre, b.cache, b.shape, ws, ws.numel(), b.status) == 0
+        assert kev.kev_read_status(b.status) == want
+    for (p, s), (p0, s0) in zip([(p.view(torch.uint8), s) for p, s in b.pools] + [(k, v)], before):
+        assert torch.equal(p, p0) and torch.equal(s, s0)
+
+
 def test_rows_with_nan_or_infinity_read_back_as_nan():
     b = Span(90, [4], [10], 2, 2, 128, "bf16", "e4m3")
     b.k[1, 0, 5], b.k[2, 1, 77] = float("nan"), float("inf")

@@ -108,12 +108,20 @@ def test_values_whose_sizes_differ_by_millions(pool):
 
 def test_launch_counts():
     b = Span(204, [1, 1], [5, 9], 8, 2, 64)
-    assert kev.kev_launch_count(16) == 2 and kev.kev_launch_count(17) == 2 and kev.kev_launch_count(19) == 3
+    assert kev.kev_launch_count(19) == 3
+    b.write()
+    kev.kev_paged_read(b.k, b.v, b.T, b.iv, 2, b.pre, b.cache, *b.end())
+    assert kev.kev_launch_count(16) == 1 and kev.kev_launch_count(17) == 1
     b.chunk(max_chunk=1)
     assert kev.kev_launch_count(18) == 2
     b = Span(205, [90, 1], [5, 9], 8, 2, 64)
     b.chunk()
     assert kev.kev_launch_count(18) == 4
+    c = Span(206, [513], [5], 8, 2, 64)
+    c.write()
+    kev.kev_paged_read(c.k, c.v, c.T, c.iv, 1, c.pre, c.cache, *c.end())
+    assert kev.kev_launch_count(16) == 2 and kev.kev_launch_count(17) == 2
+    c.ok()
     b.chunk(write=False)
     assert kev.kev_launch_count(18) == 3
     b.ok()
