@@ -434,7 +434,8 @@ kev_status kev_paged_read(void* k, void* v, int32_t total_tokens, const kev_inte
  * with K_i, V_i as the cache holds them (c_e * s for KEV_E4M3, the chunk's own rows among them) and
  * g = h / G.  Rows of tokens in no interval are written as zeros.  k and v NULL: the rows are in
  * the cache already.  max_chunk: no question brings more tokens (0: not known); a caller that
- * knows, above all of a decode step (1), gets the kernel for few rows.
+ * knows, above all of a decode step (1), gets the kernel for few rows.  out overlaps none of q, k, v
+ * and the cache (out inside q, k or v's rows: KEV_ERR_INVALID_ARG).
  * Arithmetic: bf16 q: products on the tensor cores, fp32 accumulation, softmax weights rounded for
  * the product with V, to bf16 or (few rows over KEV_E4M3) to fp16; fp32 q: fp32 throughout.  What masked positions hold, NaN and
  * infinities among it, does not reach the result. */

@@ -112,6 +112,13 @@ kev_status span_mask(SpanArgs* a, int32_t window, int32_t sinks) {
   return KEV_OK;
 }
 
+// Do the T rows at out and those of `heads` heads at `in` share bytes?  (Units read q, k and v while others write out.)
+bool overlap(const SpanArgs& a, const void* in, int heads) {
+  const uint64_t row = (uint64_t)a.d * a.elem * a.T, o = (uint64_t)(uintptr_t)a.out, i = (uint64_t)(uintptr_t)in;
+  return in && o < i + row * heads && i < o + row * a.h_q;
+}
+bool out_overlaps(const SpanArgs& a) { return overlap(a, a.q, a.h_q) || overlap(a, a.k, a.h_kv) || overlap(a, a.v, a.h_kv); }
+
 // Launches the attention; *launches: how many kernels.
 kev_status span_attend(const SpanArgs& call, bool write, int32_t* launches, cudaStream_t s) {
   const int sms = sms_of_current_device();
@@ -230,6 +237,7 @@ kev_status kev_chunk_attn_paged(const void* q, const void* k, const void* v, int
   a.k = k;
   a.v = v;
   a.out = out;
+  if (out_overlaps(a)) return KEV_ERR_INVALID_ARG;
   if (max_chunk > 0 && max_chunk < a.max_chunk) a.max_chunk = max_chunk;
   int32_t launches;
   st = span_attend(a, k != nullptr, &launches, (cudaStream_t)stream);
@@ -252,6 +260,7 @@ kev_status kev_prefill_attn_window(const void* q, const void* k, const void* v, 
   a.k = k;
   a.v = v;
   a.out = out;
+  if (out_overlaps(a)) return KEV_ERR_INVALID_ARG;
   int32_t launches;
   return span_attend(a, false, &launches, (cudaStream_t)stream);
 }

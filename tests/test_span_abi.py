@@ -53,6 +53,17 @@ def test_span_calls_refuse_on_the_host(lib, kw, code):
                                            *end, check=False) == want
 
 
+@pytest.mark.parametrize("q,k,v,out", [  # 8 tokens: 16,384 bytes of q and out, 4,096 of k and v
+    (0x100000, 0x200000, 0x300000, 0x100000), (0x100000, 0x200000, 0x300000, 0x103ff0),
+    (0x103ff0, 0x200000, 0x300000, 0x100000), (0x100000, 0x200ff0, 0x300000, 0x201fe0), (0x100000, 0x200000, 0x303ff0, 0x300000)])
+def test_out_over_an_input_is_refused(lib, q, k, v, out):
+    c = _span_args(lib)
+    end = (c["shape"], c["ws"], c["bytes"], None, 0)
+    assert lib.kev_chunk_attn_paged(q, k, v, 8, c["iv"], 2, c["pre"], 0, c["cache"], 0, 0, out, *end,
+                                    check=False) == lib.binding.KEV_ERR_INVALID_ARG
+    assert lib.kev_prefill_attn_window(q, k, v, 8, c["iv"], 2, 0, 0, out, *end, check=False) == lib.binding.KEV_ERR_INVALID_ARG
+
+
 @pytest.mark.parametrize("shape,code", [((8, 3, 128, "bf16"), "UNSUPPORTED"), ((34, 2, 128, "bf16"), "UNSUPPORTED"),
                                         ((8, 2, 96, "fp32"), "UNSUPPORTED"), ((8, 2, 256, "fp32"), "UNSUPPORTED"),
                                         ((8, 2, 128, "e4m3"), "UNSUPPORTED"), ((0, 2, 128, "bf16"), "INVALID_ARG"),
