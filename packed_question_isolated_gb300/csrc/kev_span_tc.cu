@@ -425,11 +425,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               if (!is_v) {
                 // This thread's key: K's factor with the softmax's (1 for a row of zeros, whose scores are 0;
-                // a row with a NaN scale has NaN codes), and V's, where a NaN at a tile with masked keys
-                // becomes 0: the epilogue puts it back for the rows that see it
+                // a row with a NaN scale has NaN codes), never 0, which would make NaN of the -inf of a row that
+                // does not see the key (as a normal number at the least: scores of such keys are 0 to within
+                // 2^-126 q . codes); and V's, where a NaN at a tile with masked keys becomes 0: the epilogue puts
+                // it back for the rows that see it
                 float* sc = reinterpret_cast<float*>(smem + L::kScale) + tiles_done % kScaleSlots * (2 * kBN) + x;
                 const float k = sc[0], v = sc[kBN];
-                sc[0] = k > 0.f ? k * p.scale_log2 : 1.f;
+                sc[0] = k > 0.f ? fmaxf(k * p.scale_log2, 1.17549435e-38f) : 1.f;
                 if (edge && !(v <= 3.4028235e38f)) {
                   sc[kBN] = 0.f;
                   *reinterpret_cast<volatile int*>(&bars->bad[n & 7]) = 1;

@@ -1,0 +1,103 @@
+"""The span operators on values at the ends of their types' ranges, and with a scale of the caller's, against the float64
+oracle.
+
+Tolerances, for out = sum_u w_u v_u with weights w_u of sum 1, size = sum_u w_u |v_u|, n positions and
+S = scale sum_e |q_e k_e| of the largest key:
+* the result is rounded to bf16 once: half a step, 2^-8 of at most size (2^-134 below the normal range);
+* the weights are rounded once for the product with V: 2^-8 of each to bf16, so 2^-8 size; to fp16 (decode over e4m3)
+  2^-11 size, and for those below fp16's normal range 2^-25 per position of the unit that they are held in: the largest
+  w_u s_u so far, s_u = max_e |v_ue| / 448, or 2^-126 if that is more; codes are at most 448;
+* fp32: a score is off by (d + 2) 2^-24 S, so a weight by a relative (d + 8) 2^-24 S + 2^-21, both in the sum of the
+  weights and in the sum over v, and the sums by (n + 4) 2^-24: (2 (d + 8) S + 2 n + 32) 2^-24 size;
+* exponentials below 2^-126 are zero: 2^-126 sum_u |v_u|.
+"""
+import numpy as np
+import pytest
+import torch
+
+import packed_question_isolated_gb300 as kev
+from oracle import kev_oracle as O
+
+from test_gpu_span import PAGE, Span
+
+pytestmark = pytest.mark.gpu
+
+
+def judge(b, caches, mask=(0, 0), scale=None, weights=2.0 ** -8, rows=None):
+    """b.out against the oracle over `caches`; `weights`: half a step of the softmax weights' type; `rows`: the tokens looked at."""
+    q = b.q.float().cpu().numpy().astype(np.float64)
+    got = b.out.float().cpu().numpy().astype(np.float64)
+    sc = 1 / np.sqrt(b.d) if scale is None else scale
+    worst = 0.0
+    for i, (s, e) in enumerate(b.intervals):
+        k, v = caches[i]
+        for t in range(s, e):
+            if rows is not None and t not in rows:
+                continue
+            p = b.prefix[i] + t - s
+            seen = O.span_visible(p, p + 1, *mask)
+            for h in range(b.h_q):
+                g = h // (b.h_q // b.h_kv)
+                ku, vu = k[:p + 1, g][seen], v[:p + 1, g][seen]
+                z = sc * (ku @ q[t, h])
+                w = np.exp(z - z.max())
+                w /= w.sum()
+                n, ref, size = len(z), w @ vu, w @ np.abs(vu)
+                big = sc * (np.abs(ku) @ np.abs(q[t, h])).max()
+                tol = (2 * (b.d + 8) * big + 2 * n + 32) * 2.0 ** -24 * size + 2.0 ** -126 * np.abs(vu).sum(0)
+                if b.dtype == "bf16":
+                    tol += (2.0 ** -8 + weights) * size + 2.0 ** -134
+                    if weights < 2.0 ** -8:
+                        tol += n * 2.0 ** -25 * max((w * np.abs(vu).max(-1)).max(), 448 * 2.0 ** -126)
+                err = np.abs(got[t, h] - ref)
+                assert (err <= tol).all(), (t, h, float(err.max()), float(tol[err.argmax()]), got[t, h][:4], ref[:4])
+                worst = max(worst, float((err / tol).max()))
+    return worst
+
+
+def with_scale(b, scale):
+    if scale is not None:
+        b.shape = kev.make_shape(b.h_q, b.h_kv, b.d, b.dtype, scale)
+    return b
+
+
+def seen_by_some(b, mask):
+    """bool[n_blocks, PAGE]: cached positions that some new token sees."""
+    keep = np.zeros((b.n_blocks, PAGE), bool)
+    for i, (m, p) in enumerate(zip(b.lens, b.prefix)):
+        for x in range(p, p + m):
+            for u in np.flatnonzero(O.span_visible(x, x + 1, *mask)):
+                keep[b.table[i, u // PAGE], u % PAGE] = True
+    return torch.from_numpy(keep).cuda()
+
+
+# lens, prefix, mask, max_chunk: decode, few rows, chunks, a mixed round
+BATCHES = [([1, 1, 1], [300, 129, 5], (100, 2), 1), ([2, 1], [300, 129], (0, 0), 2), ([40, 1, 150], [300, 129, 5], (100, 2), 0),
+           ([1] * 12 + [70], [30 * i for i in range(13)], (0, 0), 0)]
+
+
+def masked_scales(side, bits, batch, dtype, d, scale):
+    lens, prefix, mask, mc = BATCHES[batch]
+    b = with_scale(Span(400 + batch, lens, prefix, 8, 2, d, dtype, "e4m3"), scale)
+    b.write()
+    caches = b.caches()
+    masked = (~seen_by_some(b, mask))[:, None, :].expand(-1, b.h_kv, -1)
+    p, s = b.pools[side]
+    s.view(torch.int32)[masked] = int(np.array([bits], np.uint32).view(np.int32)[0])
+    g = torch.Generator(device="cuda").manual_seed(bits & 0xffff)
+    p.view(torch.uint8)[masked] = torch.randint(0, 256, (int(masked.sum()), d), generator=g, device="cuda", dtype=torch.uint8)
+    b.chunk(*mask, max_chunk=mc, write=False)
+    b.ok()
+    judge(b, caches, mask, scale)
+
+
+# the smallest subnormals (as small integers look in memory that held some), a product with the scale that underflows,
+# -0, infinities, NaN, the largest and the smallest finite number
+BITS = [0x1, 0x2, 0x3, 0x400, 0x80000000, 0x80000001, 0xff800000, 0x7f800000, 0xffc00000, 0x7fffffff, 0x7f7fffff, 0xff7fffff]
+
+
+@pytest.mark.parametrize("bits", BITS, ids=hex)
+@pytest.mark.parametrize("batch", range(len(BATCHES)))
+@pytest.mark.parametrize("dtype,d,scale", [("bf16", 128, None), ("bf16", 64, 2.0 ** -12), ("fp32", 64, None)])
+def test_key_scales_of_masked_positions_may_hold_anything(bits, batch, dtype, d, scale):
+    masked_scales(0, bits, batch, dtype, d, scale)
