@@ -427,12 +427,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // This thread's key: K's factor with the softmax's (1 for a row of zeros, whose scores are 0;
                 // a row with a NaN scale has NaN codes), never 0, which would make NaN of the -inf of a row that
                 // does not see the key (as a normal number at the least: scores of such keys are 0 to within
-                // 2^-126 q . codes); and V's, where a NaN at a tile with masked keys becomes 0: the epilogue puts
-                // it back for the rows that see it
+                // 2^-126 q . codes); and V's, where a NaN or an infinity at a tile with masked keys becomes 0: the
+                // epilogue makes NaN of the rows that see it
                 float* sc = reinterpret_cast<float*>(smem + L::kScale) + tiles_done % kScaleSlots * (2 * kBN) + x;
                 const float k = sc[0], v = sc[kBN];
                 sc[0] = k > 0.f ? fmaxf(k * p.scale_log2, 1.17549435e-38f) : 1.f;
-                if (edge && !(v <= 3.4028235e38f)) {
+                if (edge && !(fabsf(v) <= 3.4028235e38f)) {
                   sc[kBN] = 0.f;
                   *reinterpret_cast<volatile int*>(&bars->bad[n & 7]) = 1;
                 }
@@ -648,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (Q8) {
                 const int64_t cell =
                     ((int64_t)a.table[(int64_t)w.item.question * a.max_blocks + u / kPage] * a.h_kv + w.head) * kPage + u % kPage;
-                if (!(a.scale_v[cell] <= 3.4028235e38f)) l_run = __int_as_float(0x7fffffff);
+                if (!(fabsf(a.scale_v[cell]) <= 3.4028235e38f)) l_run = __int_as_float(0x7fffffff);
                 continue;
               }
               const uint4* v = reinterpret_cast<const uint4*>(

@@ -101,3 +101,10 @@ BITS = [0x1, 0x2, 0x3, 0x400, 0x80000000, 0x80000001, 0xff800000, 0x7f800000, 0x
 @pytest.mark.parametrize("dtype,d,scale", [("bf16", 128, None), ("bf16", 64, 2.0 ** -12), ("fp32", 64, None)])
 def test_key_scales_of_masked_positions_may_hold_anything(bits, batch, dtype, d, scale):
     masked_scales(0, bits, batch, dtype, d, scale)
+
+
+@pytest.mark.parametrize("bits", BITS, ids=hex)
+@pytest.mark.parametrize("batch", range(len(BATCHES)))
+@pytest.mark.parametrize("dtype,d,scale", [("bf16", 128, None), ("bf16", 64, 2.0 ** -12), ("fp32", 64, None)])
+def test_value_scales_of_masked_positions_may_hold_anything(bits, batch, dtype, d, scale):
+    masked_scales(1, bits, batch, dtype, d, scale)
