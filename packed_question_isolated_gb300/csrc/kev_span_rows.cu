@@ -659,8 +659,11 @@ __global__ void __launch_bounds__(kThreads, few_rows_ctas(D, NT))
                   const float w0 = z[nt][x] == -INFINITY ? 0.f : ex2_approx(z[nt][x] - ref) * vf0;
                   const float w1 = z[nt][2 + x] == -INFINITY ? 0.f : ex2_approx(z[nt][2 + x] - ref) * vf1;
                   const float top = top_of(w0, w1), old = per[nt][x] > 0.f ? alpha / per[nt][x] : 0.f;
-                  mul = top > old * 16384.f ? old / top : 1.f;
-                  const float unit = top > old * 16384.f ? top : old;
+                  float unit = top > old * 16384.f ? top : old;
+                  // 2^-126 at the least, or 1 / unit is infinite (values below 1e-36, or beside a key far above
+                  // them whose own are zero); the smallest scale, 2^-149, is in fp16's range then too
+                  if (unit > 0.f) unit = fmaxf(unit, 1.17549435e-38f);
+                  mul = unit == old ? 1.f : old / unit;
                   per[nt][x] = unit > 0.f ? 1.f / unit : 0.f;
                 }
 #pragma unroll

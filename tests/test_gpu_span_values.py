@@ -108,3 +108,51 @@ def test_key_scales_of_masked_positions_may_hold_anything(bits, batch, dtype, d,
 @pytest.mark.parametrize("dtype,d,scale", [("bf16", 128, None), ("bf16", 64, 2.0 ** -12), ("fp32", 64, None)])
 def test_value_scales_of_masked_positions_may_hold_anything(bits, batch, dtype, d, scale):
     masked_scales(1, bits, batch, dtype, d, scale)
+
+
+def set_value_rows(b, at, factor):
+    """Multiplies the cached V rows of positions `at` of every question by `factor`, as quantised rows are: their codes stay."""
+    pv, sv = b.pools[1]
+    for i, (m, p) in enumerate(zip(b.lens, b.prefix)):
+        for u in at(p + m):
+            blk, r = int(b.table[i, u // PAGE]), u % PAGE
+            if sv is None:
+                pv[blk, :, r] *= factor
+            else:
+                sv[blk, :, r] *= factor
+
+
+WHERE = [lambda n: range(n), lambda n: range(min(n, PAGE)), lambda n: range(n - n // 3, n), lambda n: range(0, n, 5)]
+
+
+@pytest.mark.parametrize("factor", [0.0, 1e-43, 1e-40, 1e-37, 1e-35, 1e-33, 1e25])
+@pytest.mark.parametrize("where", range(len(WHERE)), ids=["all", "first page", "last", "every fifth"])
+@pytest.mark.parametrize("pool,h_q,h_kv,d", [("e4m3", 8, 2, 128), ("e4m3", 16, 1, 64), ("e4m3", 4, 4, 64), ("bf16", 8, 2, 128)])
+def test_decode_over_values_of_any_size(pool, h_q, h_kv, d, where, factor):
+    b = Span(410, [1, 1, 1], [600, 200, 17], h_q, h_kv, d, "bf16", pool)
+    b.write()
+    set_value_rows(b, WHERE[where], factor)
+    b.chunk(max_chunk=1, write=False)
+    b.ok()
+    judge(b, b.caches(), weights=2.0 ** -11 if pool == "e4m3" else 2.0 ** -8)
+
+
+@pytest.mark.parametrize("above", [20, 90, 110, 114, 116, 118, 120, 122, 124, 126, 130, 150, 200])
+@pytest.mark.parametrize("key", [0, 3, 300])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_key_far_above_the_others_whose_values_are_zero(d, key, above):
+    """A null sink: one key's score stands 2^above over the others' and its V row is zero, so the result is the others' share."""
+    b = Span(411, [1], [400], 4, 2, d, "bf16", "e4m3")
+    b.write()
+    (pk, sk), (pv, sv) = b.pools
+    b.q.fill_(1.0)
+    blk, r = int(b.table[0, key // PAGE]), key % PAGE
+    sk.zero_()
+    pk.view(torch.uint8).zero_()
+    pk.view(torch.uint8)[blk, :, r] = 0x7e  # 448
+    sk[blk, :, r] = above * np.log(2.0) / (448 * np.sqrt(d))
+    pv.view(torch.uint8)[blk, :, r] = 0
+    sv[blk, :, r] = 0.0
+    b.chunk(max_chunk=1, write=False)
+    b.ok()
+    judge(b, b.caches(), weights=2.0 ** -11)
