@@ -436,9 +436,12 @@ kev_status kev_paged_read(void* k, void* v, int32_t total_tokens, const kev_inte
  * the cache already.  max_chunk: no question brings more tokens (0: not known); a caller that
  * knows, above all of a decode step (1), gets the kernel for few rows.  out overlaps none of q, k, v
  * and the cache (out inside q, k or v's rows: KEV_ERR_INVALID_ARG).
- * Arithmetic: bf16 q: products on the tensor cores, fp32 accumulation, softmax weights rounded for
- * the product with V, to bf16 or (few rows over KEV_E4M3) to fp16; fp32 q: fp32 throughout.  What masked positions hold, NaN and
- * infinities among it, does not reach the result. */
+ * Arithmetic: bf16 q: products on the tensor cores, fp32 accumulation, softmax weights (over
+ * KEV_E4M3 times the scale of V's row) rounded for the product with V, to bf16 or (few rows over
+ * KEV_E4M3) to fp16, at any size of V's rows down to the smallest; above, |v| < 2^40 is sure to stay
+ * finite, since a weight may stand at up to 2^64 before its sum divides it.  fp32 q: fp32 throughout.
+ * What masked positions hold, NaN and infinities in rows or scales among it, does not reach the
+ * result. */
 kev_status kev_chunk_attn_paged(const void* q, const void* k, const void* v, int32_t total_tokens,
                                 const kev_interval* intervals, int32_t n_questions, const int32_t* prefix_lens,
                                 int32_t max_chunk, const kev_paged_cache* cache, int32_t window, int32_t sinks, void* out,

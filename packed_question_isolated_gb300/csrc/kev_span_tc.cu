@@ -55,6 +55,10 @@ constexpr uint32_t kTmemCols = 512;
 constexpr float kOverflowSum = 1.8446744e19f;  // 2^64
 constexpr long long kDrainBudget = 4000000000ll;
 constexpr int kScaleSlots = 4;
+// Over e4m3 the weight times V's scale is what becomes bf16, and a bf16 value's scale may be 2^-135 (of a subnormal
+// one 2^-142): the weights start 2^24 higher, so the product stays a normal bf16 number down to weights of 2^-15 at
+// that scale.  O and l share the factor.
+constexpr float kLift = 24.f;
 
 template <int D, bool Q8>
 struct Smem {
@@ -486,6 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
       const uint32_t tm_s = tmem + t * kBN + lane_off, tm_o = tmem + 256 + t * D + lane_off;
       const float sl2 = Q8 ? 1.f : p.scale_log2;  // e4m3: in the keys' factors
+      constexpr float lift = Q8 ? kLift : 0.f;
       const unsigned long long sl2x2 = f2pack(sl2, sl2);
       const int tok = r / a.group;  // token of the tile
       uint32_t s_cnt = 0, o_cnt = 0, n = 0, tiles_done = 0;
@@ -590,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // The first tile in which a row sees a key sets its reference; a later one moves it only
           // when the weights approach the end of the fp32 range.
           if (__any_sync(0xffffffffu, row_ok && m_run == -INFINITY)) {
-            const float mt = row_max();
+            const float mt = row_max() - lift;
             if (m_run == -INFINITY) m_run = mt;
           }
           float lt = exp_tile(m_run == -INFINITY ? 0.f : m_run);
@@ -598,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (__any_sync(0xffffffffu, big)) {
             float alpha = 1.f;
             if (big) {
-              const float mt = fmaxf(row_max(), m_run);
+              const float mt = fmaxf(row_max() - lift, m_run);
               alpha = ex2_approx(m_run - mt);
               m_run = mt;
               l_run *= alpha;

@@ -156,3 +156,35 @@ def test_a_key_far_above_the_others_whose_values_are_zero(d, key, above):
     b.chunk(max_chunk=1, write=False)
     b.ok()
     judge(b, b.caches(), weights=2.0 ** -11)
+
+
+@pytest.mark.parametrize("factor", [0.0, 1e-43, 1e-40, 1e-37, 1e-35, 1e-33, 1e25])
+@pytest.mark.parametrize("where", range(len(WHERE)), ids=["all", "first page", "last", "every fifth"])
+@pytest.mark.parametrize("pool,d", [("e4m3", 128), ("e4m3", 64), ("bf16", 128)])
+def test_chunks_over_values_of_any_size(pool, d, where, factor):
+    b = Span(412, [20, 40], [300, 17], 8, 2, d, "bf16", pool)
+    b.write()
+    set_value_rows(b, WHERE[where], factor)
+    b.chunk(write=False)
+    b.ok()
+    judge(b, b.caches())
+
+
+@pytest.mark.parametrize("above", [20, 60, 90, 110, 118, 122, 126, 150])
+@pytest.mark.parametrize("key", [0, 300])
+@pytest.mark.parametrize("d", [64, 128])
+def test_chunks_with_a_key_far_above_the_others_whose_values_are_zero(d, key, above):
+    b = Span(413, [20], [400], 4, 2, d, "bf16", "e4m3")
+    b.write()
+    (pk, sk), (pv, sv) = b.pools
+    b.q.fill_(1.0)
+    blk, r = int(b.table[0, key // PAGE]), key % PAGE
+    sk.zero_()
+    pk.view(torch.uint8).zero_()
+    pk.view(torch.uint8)[blk, :, r] = 0x7e  # 448
+    sk[blk, :, r] = above * np.log(2.0) / (448 * np.sqrt(d))
+    pv.view(torch.uint8)[blk, :, r] = 0
+    sv[blk, :, r] = 0.0
+    b.chunk(write=False)
+    b.ok()
+    judge(b, b.caches())
