@@ -538,7 +538,7 @@ const char* kev_status_string(kev_status status);
  * small calls, else 2: plan, copy), 18 = chunk_attn_paged (plan and attention for few rows per
  * question, 2; else plan, cache write if k is given, attention -- two kernels in a mixed round over an
  * e4m3 cache -- and merge), 19 = prefill_attn_window (3: plan, attention, merge).  16 to 18: the most
- * recent call's, 2 before any.  -1 for an unknown id. */
+ * recent call's, 2 before any.  18 and 19 launch the plan alone, 1, without tokens.  -1 for an unknown id. */
 int32_t kev_launch_count(int32_t entry_point);
 
 #ifdef __cplusplus

@@ -124,6 +124,10 @@ kev_status span_attend(const SpanArgs& call, bool write, int32_t* launches, cuda
   const int sms = sms_of_current_device();
   if (sms <= 0) return KEV_ERR_CUDA;
   cudaError_t e;
+  if (call.T <= 0) {  // no tokens (every question dropped): the checks alone; a tile of max_chunk = 0 rows holds no token
+    *launches = 1;
+    return from_cuda(launch_span_plan(call, 0, nullptr, nullptr, s));
+  }
   *launches = 3 + write;
   if (call.elem == 4) {
     SpanArgs a = span_line(call, 0, 64, 1, 2 * sms);

@@ -870,7 +870,6 @@ cudaError_t launch_nt(const SpanArgs& a, bool write, cudaStream_t s) {
 int span_rows_ctas(int d, int rows) { return few_rows_ctas(d, rows / 8); }
 
 cudaError_t launch_span_rows(const SpanArgs& a, bool write, cudaStream_t s) {
-  if (a.T <= 0) return cudaSuccess;
   if (a.pool_elem == 1) return a.d == 64 ? launch_nt<64, 1>(a, write, s) : launch_nt<128, 1>(a, write, s);
   return a.d == 64 ? launch_nt<64, 2>(a, write, s) : launch_nt<128, 2>(a, write, s);
 }

@@ -188,3 +188,22 @@ def test_chunks_with_a_key_far_above_the_others_whose_values_are_zero(d, key, ab
     b.chunk(write=False)
     b.ok()
     judge(b, b.caches())
+
+
+@pytest.mark.parametrize("pool", ["bf16", "e4m3"])
+@pytest.mark.parametrize("h_q,h_kv", [(16, 1), (12, 1), (9, 1), (8, 2), (4, 4)])
+def test_calls_without_tokens(h_q, h_kv, pool):
+    """Every question dropped: the checks run, nothing is written, with and without max_chunk."""
+    b = Span(420, [0, 0, 0], [700, 3, 0], h_q, h_kv, 128, "bf16", pool, width=6)
+    before = [(p.view(torch.uint8).clone(), None if s is None else s.clone()) for p, s in b.pools]
+    for mask in ((0, 0), (9, 2)):
+        for mc in (0, 1):
+            b.status.fill_(-1)
+            b.chunk(*mask, max_chunk=mc)
+            b.ok()
+            assert kev.kev_launch_count(18) == 1
+        b.status.fill_(-1)
+        b.packed(*mask)
+        b.ok()
+    for (p, s), (p0, s0) in zip(b.pools, before):
+        assert torch.equal(p.view(torch.uint8), p0) and (s is None or torch.equal(s, s0))
