@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(const __grid_con
       base0[n] = all.items[0];
       base1[n] = all.items[1];
     }
-    if (words) {  // pages: one or more warps per question, a lane per page; a block's bit may be set once
+    if (words && n > 0) {  // pages: one or more warps per question, a lane per page; a block's bit may be set once
       const int slices = n < kThreads / 32 ? kThreads / 32 / n : 1;
 #pragma unroll 1
       for (int x = warp; x < n * slices; x += kThreads / 32) {

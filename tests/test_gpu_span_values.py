@@ -207,3 +207,25 @@ def test_calls_without_tokens(h_q, h_kv, pool):
         b.ok()
     for (p, s), (p0, s0) in zip(b.pools, before):
         assert torch.equal(p.view(torch.uint8), p0) and (s is None or torch.equal(s, s0))
+
+
+@pytest.mark.parametrize("pool", ["bf16", "e4m3"])
+@pytest.mark.parametrize("T", [0, 5, 600])
+def test_calls_without_questions(T, pool):
+    """Tokens of no question: rows of out are zero, nothing else is touched."""
+    b = Span(421, [T], [200], 4, 2, 128, "bf16", pool)
+    before = [(p.view(torch.uint8).clone(), None if s is None else s.clone()) for p, s in b.pools]
+    ko, vo = b.k.clone(), b.v.clone()
+    for f in (kev.kev_paged_write, kev.kev_paged_read):
+        b.status.fill_(-1)
+        f(ko, vo, T, None, 0, None, b.cache, *b.end())
+        b.ok()
+    assert torch.equal(ko, b.k) and torch.equal(vo, b.v)
+    for mask, mc in (((0, 0), 0), ((9, 2), 0), ((0, 0), 1)):
+        b.status.fill_(-1)
+        b.out.fill_(3.0)
+        kev.kev_chunk_attn_paged(b.q, b.k, b.v, T, None, 0, None, mc, b.cache, *mask, b.out, *b.end())
+        b.ok()
+        assert (b.out == 0).all()
+    for (p, s), (p0, s0) in zip(b.pools, before):
+        assert torch.equal(p.view(torch.uint8), p0) and (s is None or torch.equal(s, s0))
