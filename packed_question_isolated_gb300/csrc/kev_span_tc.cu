@@ -88,7 +88,7 @@ struct Bars {
   uint32_t tmem;
   int abort;
   int never;
-  int bad[8];  // unit u % 8 has NaN or infinities in V (e4m3: in its scales) at tiles with masked keys
+  int bad;  // the last unit, + 1, known to have NaN or infinities in V (e4m3: in its scales) at tiles with masked keys
 };
 static_assert(sizeof(Bars) <= 1024, "barriers");
 
@@ -173,7 +173,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars->st_empty[s], 4);
       mbar_init(&bars->sc_full[s], 4);
     }
-    for (int u = 0; u < 8; ++u) bars->bad[u] = 0;
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bars->s_full[t], 1);
       mbar_init(&bars->p_full[t], 4);
@@ -184,6 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bars->stall, 1);
     bars->abort = 0;
     bars->never = 0;
+    bars->bad = 0;
     fence_mbar_init();
   }
   if (warp == kLoadWarp && lane == 0) {
@@ -377,9 +377,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (SpanWalk w(a, blockIdx.x); ok && w.live(); w.next(), ++n) {
         const int p0 = w.item.p0, p1 = p0 + w.item.tokens - 1;
         const SpanTiles tiles(p0, p1, a.window, a.sinks);
-        // A later unit's flag: no warp here is that far ahead (a slot's next tile waits for all four
-        // warps), and the epilogue of unit n - 4 has read it (its PV came before the V slots of n - 1)
-        if (x == 0) *reinterpret_cast<volatile int*>(&bars->bad[(n + 4) & 7]) = 0;
         for (int j = w.j0; ok && j < w.j1; ++j, ++tiles_done) {
           const bool edge = edge_tile(a, tiles.at(j) * kBN, p0, p1);
           for (int is_v = 0; is_v < 2; ++is_v, ++seq) {
@@ -415,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   }
                 }
                 if (__any_sync(0xffffffffu, any != 0)) {
-                  if (lane == 0) *reinterpret_cast<volatile int*>(&bars->bad[n & 7]) = 1;
+                  if (lane == 0) atomicMax(&bars->bad, (int)n + 1);
                   fence_proxy_async_smem();
                 }
               }
@@ -438,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sc[0] = k > 0.f ? fmaxf(k * p.scale_log2, 1.17549435e-38f) : 1.f;
                 if (edge && !(fabsf(v) <= 3.4028235e38f)) {
                   sc[kBN] = 0.f;
-                  *reinterpret_cast<volatile int*>(&bars->bad[n & 7]) = 1;
+                  atomicMax(&bars->bad, (int)n + 1);
                 }
                 mbar_arrive_warp(&bars->sc_full[tiles_done % kScaleSlots]);
               }
@@ -639,7 +636,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < D / 32; ++c) tmem_ld32(tm_o + c * 32, o[c]);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) tmem_ld_wait(o[c]);
-        const bool bad = *reinterpret_cast<volatile int*>(&bars->bad[n & 7]);
+        // Set before this unit's tiles were ready.  It only grows, so a late epilogue cannot miss it, whatever the
+        // later units' tiles did to it meanwhile: at worst it looks through a unit that has nothing to put back.
+        const bool bad = *reinterpret_cast<volatile int*>(&bars->bad) > (int)n;
         tc_fence_before();
         mbar_arrive_warp(&bars->o_free[t]);
         if (bad && row_ok) {

@@ -229,3 +229,48 @@ def test_calls_without_questions(T, pool):
         assert (b.out == 0).all()
     for (p, s), (p0, s0) in zip(b.pools, before):
         assert torch.equal(p.view(torch.uint8), p0) and (s is None or torch.equal(s, s0))
+
+
+@pytest.mark.parametrize("pool", ["packed", "bf16", "e4m3"])
+@pytest.mark.parametrize("long,short", [(60, 9), (40, 30), (64, 64)])
+def test_infinities_are_put_back_in_every_unit(pool, long, short):
+    """Many units per CTA, of two row tiles and of one in turns, each with an infinity (e4m3: a NaN row) in the middle of its V:
+    the rows that see it get it, the others are as without it."""
+    h_q, h_kv, d, n = 16, 4, 64, 600
+    r = np.random.default_rng(430 + long)
+    lens = np.where(r.random(n) < 0.5, long, short) - r.integers(0, 8, n)
+    b = Span(430, lens.tolist(), [0] * n, h_q, h_kv, d, "bf16", "bf16" if pool == "packed" else pool)
+    at = torch.from_numpy(b.intervals[:, 0] + (lens * 0.6).astype(int)).cuda()
+    if pool == "packed":
+        b.v[at, :, 5::17] = float("inf")
+        b.packed(0, 0)
+    else:
+        b.write()
+        blk = torch.from_numpy(b.table[:, 0]).cuda().long()
+        row = at - b.iv[:, 0]
+        pv, sv = b.pools[1]
+        if pool == "bf16":
+            pv[blk, :, row, 5::17] = float("inf")
+        else:
+            pv.view(torch.uint8)[blk, :, row] = 0x7f
+            sv[blk, :, row] = float("nan")
+        b.chunk(write=False)
+    b.ok()
+    stored = [torch.from_numpy(x).cuda() for x in b.stored()] if pool != "packed" else None
+    for i, (s, e) in enumerate(b.intervals.tolist()):
+        if pool == "packed":
+            k, v = b.k[s:e].double(), b.v[s:e].double()
+        else:
+            k, v = (x[int(b.table[i, 0])].transpose(0, 1)[:e - s] for x in stored)
+        q = b.q[s:e].double().view(e - s, h_kv, h_q // h_kv, d)
+        z = torch.einsum("thgd,uhd->thgu", q, k) / 8
+        seen = torch.ones(e - s, e - s, dtype=torch.bool, device="cuda").tril()[:, None, None]
+        w = torch.softmax(z.masked_fill(~seen, -np.inf), -1)
+        ok = v.isfinite()
+        clean = torch.where(ok, v, 0)
+        ref, size = (torch.einsum("thgu,uhd->thgd", w, x).reshape(e - s, h_q, d) for x in (clean, clean.abs()))
+        hit = torch.einsum("thgu,uhd->thgd", seen.expand_as(z).double(), (~ok).double()).reshape(e - s, h_q, d) > 0
+        got = b.out[s:e].double()
+        assert torch.equal(~got.isfinite(), hit), i
+        # two roundings to bf16 and the fp32 part: scores of at most a few tens
+        assert ((got - ref).abs() <= (2.0 ** -7 + 2.0 ** -12) * size + 1e-30)[~hit].all(), i
