@@ -385,12 +385,13 @@ int32_t kev_assign_blocks(const int32_t* need, int32_t n, uint8_t* free_map, int
  * Shapes: bf16 or fp32 q, k, v and out, d_h 64 or 128 (else KEV_ERR_UNSUPPORTED).  Cache: blocks
  * of KEV_PAGE positions and a block table as for the paged slot pool above, of the type of q or
  * of KEV_E4M3, with at most 2^20 blocks and fewer than 2^31 rows (n_blocks * H_kv * KEV_PAGE).
- * Device-detected errors, found before anything is written: KEV_ERR_INTERVALS (also a question
- * longer than max_chunk), KEV_ERR_PREFIX (negative), KEV_ERR_SLOT_OVERFLOW (P_i + L_i >
- * max_blocks * KEV_PAGE), KEV_ERR_SLOT (a block out of range, or used twice).  Only pages that
- * some new token sees or that are written are looked at: entries of pages that have wholly left
- * the window may be anything.  The workspace (kev_paged_workspace_size bytes, 256-byte aligned)
- * needs no initial value; calls in flight at the same time must not share one.
+ * Device-detected errors, found before anything is written, of several the first in this order:
+ * KEV_ERR_INTERVALS (also a question longer than max_chunk), KEV_ERR_PREFIX (negative),
+ * KEV_ERR_SLOT_OVERFLOW (P_i + L_i > max_blocks * KEV_PAGE), KEV_ERR_SLOT (a block out of range, or
+ * used twice).  Only pages that some new token sees or that are written are looked at: entries of
+ * pages that have wholly left the window may be anything.  The workspace
+ * (kev_paged_workspace_size bytes, 256-byte aligned) needs no initial value; calls in flight at the
+ * same time must not share one.
  * ------------------------------------------------------------------------------------- */
 
 /* A paged cache.  With dtype KEV_E4M3, position p's row of kv head g is d_h codes c_e and the

@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kSmallThreads) span_small_copy_kernel(SpanArgs
     }
   }
   __syncthreads();
-  const bool clean = s_err == 0;
+  const bool clean = s_err == 0, inside = s_err != 8;  // inside: every interval at least
   __syncthreads();
   if (clean) {
     for (int i = t; i < a.n; i += kSmallThreads) {  // pages; a block's bit may be set once
@@ -302,6 +302,8 @@ __global__ void __launch_bounds__(kSmallThreads) span_small_copy_kernel(SpanArgs
         if (b < 0 || b >= a.n_blocks || atomicOr(&used[b >> 5], bit) & bit) error(3);
       }
     }
+  }
+  if (inside) {
     for (int i = warp; i < a.n; i += kSmallThreads / 32)
       for (int x = s_iv[i].x + lane; x < s_iv[i].y; x += 32)
         if (atomicExch(&s_owner[x], i) >= 0) error(0);

@@ -137,13 +137,14 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(const __grid_con
   Scan all;
   const Scan before = block_scan<kThreads>(mine, Scan{}, s_scan, &all);
 
-  const bool clean = s_err == 0;  // the checks of single questions passed
+  const bool clean = s_err == 0;   // the checks of single questions passed
+  const bool inside = s_err != 8;  // at least those of their intervals
   __syncthreads();
 
   // Disjoint, if every interval begins at or after the end of all before it; otherwise sorted by
   // beginning and looked at again.
   bool ok = true;
-  if (clean) {
+  if (inside) {
     int end = before.end, tokens = before.tokens, items0 = before.items[0], items1 = before.items[1];
 #pragma unroll 1
     for (int e = 0; e < per; ++e) {
@@ -167,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(const __grid_con
       base0[n] = all.items[0];
       base1[n] = all.items[1];
     }
-    if (words && n > 0) {  // pages: one or more warps per question, a lane per page; a block's bit may be set once
+    if (words && n > 0 && clean) {  // pages: one or more warps per question, a lane per page; a block's bit may be set once
       const int slices = n < kThreads / 32 ? kThreads / 32 / n : 1;
 #pragma unroll 1
       for (int x = warp; x < n * slices; x += kThreads / 32) {
@@ -195,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(const __grid_con
   bool sorted = __syncthreads_and(ok);
   auto interval = [&](int i) { return iv[i]; };
   auto ordered = [&](int i) { return kev_interval{(int)(area[i] >> 32), (int)(area[i] & 0xffffffffu)}; };
-  if (clean && !sorted) {
+  if (inside && !sorted) {
     int n2 = 1;
     while (n2 < n) n2 <<= 1;
     for (int i = t; i < n2; i += kThreads)  // empty intervals last
@@ -251,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(const __grid_con
       hdr->n_gaps = total.gaps + (total.end < a.T);
     }
   };
-  if (clean) {
+  if (inside) {
     if (!sorted) find_gaps(ordered, true);
     else if (p.lines && all.tokens < a.T) find_gaps(interval, false);
     else if (t == 0) hdr->n_gaps = 0;

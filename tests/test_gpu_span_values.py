@@ -274,3 +274,36 @@ def test_infinities_are_put_back_in_every_unit(pool, long, short):
         assert torch.equal(~got.isfinite(), hit), i
         # two roundings to bf16 and the fp32 part: scores of at most a few tens
         assert ((got - ref).abs() <= (2.0 ** -7 + 2.0 ** -12) * size + 1e-30)[~hit].all(), i
+
+
+@pytest.mark.parametrize("what", ["prefix", "overflow", "range", "twice"])
+@pytest.mark.parametrize("more", [0, 600])
+def test_overlapping_intervals_come_before_other_errors(what, more):
+    """Of several errors the first in the order intervals, prefix, overflow, slot is reported, whatever question has it."""
+    b = Span(431, [5, 9, 4], [130, 40, 0], 4, 2, 128, "bf16", "e4m3")
+    b.intervals[2] = (2, 3)  # inside question 0
+    if what == "prefix":
+        b.prefix[1] = -1
+    elif what == "overflow":
+        b.prefix[1] = b.width * PAGE - 8
+    elif what == "range":
+        b.table[0, 1] = b.n_blocks
+    else:
+        b.table[1, 0] = b.table[0, 1]
+    b.to_device()
+    assert O.validate_span(b.intervals, b.T + more, b.prefix, b.table, b.n_blocks) == O.INTERVALS
+    want = kev.binding.KEV_ERR_INTERVALS
+    T = b.T + more
+    q, k, v, out = (torch.cat([x, torch.ones((more, *x.shape[1:]), dtype=x.dtype, device="cuda")]) for x in (b.q, b.k, b.v, b.out))
+    ws = torch.full((kev.kev_paged_workspace_size(3, T, b.shape),), 0xff, dtype=torch.uint8, device="cuda")
+    end = (b.shape, ws, ws.numel(), b.status)
+    before = [(p.view(torch.uint8).clone(), s.clone()) for p, s in b.pools]
+    for f in (kev.kev_paged_write, kev.kev_paged_read):
+        b.status.fill_(-1)
+        f(k, v, T, b.iv, 3, b.pre, b.cache, *end)
+        assert kev.kev_read_status(b.status) == want
+    b.status.fill_(-1)
+    kev.kev_chunk_attn_paged(q, k, v, T, b.iv, 3, b.pre, 0, b.cache, 0, 0, out, *end)
+    assert kev.kev_read_status(b.status) == want
+    for (p, s), (p0, s0) in zip(b.pools, before):
+        assert torch.equal(p.view(torch.uint8), p0) and torch.equal(s, s0)
