@@ -397,9 +397,11 @@ int32_t kev_assign_blocks(const int32_t* need, int32_t n, uint8_t* free_map, int
 /* A paged cache.  With dtype KEV_E4M3, position p's row of kv head g is d_h codes c_e and the
  * scale s at the same place, s = max_e |x_e| / 448 and c_e = x_e / s rounded to the nearest e4m3
  * value (ties to even): each element comes back as c_e * s, off by at most max(2^-4 |x_e|,
- * 2^-10 s) and the last place of s.  A row of zeros has s = 0.  A row that holds a NaN or an
- * infinity has s = NaN and comes back as NaN throughout (rows of a cache filled by other means
- * keep to this: the NaN codes 0x7f and 0xff only under a NaN scale). */
+ * 2^-10 s) and 224 units in the last place of s (448 times its rounding; more than the fp32 rounding
+ * of x_e only where s is subnormal, rows under 2^-117).  A row of zeros, or of values so small that s
+ * rounds to zero, has s = 0 and comes back as zeros.  A row that holds a NaN or an infinity has s =
+ * NaN and comes back as NaN throughout (rows of a cache filled by other means keep to this: the NaN
+ * codes 0x7f and 0xff only under a NaN scale). */
 typedef struct {
   void* k;                    /* [n_blocks, H_kv, KEV_PAGE, d_h] of dtype, 16-byte aligned */
   void* v;

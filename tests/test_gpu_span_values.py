@@ -307,3 +307,32 @@ def test_overlapping_intervals_come_before_other_errors(what, more):
     assert kev.kev_read_status(b.status) == want
     for (p, s), (p0, s0) in zip(b.pools, before):
         assert torch.equal(p.view(torch.uint8), p0) and torch.equal(s, s0)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("fp32", 128), ("fp32", 64)])
+@pytest.mark.parametrize("how", ["small", "large", "decode"])
+def test_rows_with_subnormal_scales_are_written_as_defined(dtype, d, how):
+    """Rows of 2^-149 to 2^-100 and of the largest numbers: codes and scales bit for bit, by both copies and by a decode step."""
+    n, h_kv = (300, 3) if how == "large" else (120, 3)
+    b = Span(440, [1] * n if how == "decode" else [n], list(range(n)) if how == "decode" else [70], 6, h_kv, d, dtype, "e4m3")
+    g = torch.Generator(device="cuda").manual_seed(440)
+    for x in (b.k, b.v):
+        e = torch.randint(-149, -99, (n, h_kv, 1), generator=g, device="cuda")
+        e[::7] = 126
+        x.copy_(torch.ldexp(x.double(), e).clamp(-3.3e38, 3.3e38).to(x.dtype))
+    if how == "decode":
+        b.chunk(max_chunk=1)
+    else:
+        k, v = (torch.cat([x, torch.zeros((500 if how == "large" else 0, h_kv, d), dtype=x.dtype, device="cuda")]) for x in (b.k, b.v))
+        ws = torch.empty(kev.kev_paged_workspace_size(1, len(k), b.shape), dtype=torch.uint8, device="cuda")
+        kev.kev_paged_write(k, v, len(k), b.iv, 1, b.pre, b.cache, b.shape, ws, ws.numel(), b.status)
+    b.ok()
+    t = np.arange(n)
+    q, pos = (t, np.array(b.prefix)) if how == "decode" else (np.zeros(n, int), 70 + t)
+    row = b.intervals[q, 0] + (0 if how == "decode" else t)
+    blk = b.table[q, pos // PAGE]
+    for x, (p, s) in zip((b.k, b.v), b.pools):
+        code, scale = O.quantise_rows(x.float().cpu().numpy()[row])
+        want = torch.from_numpy(code).float().to(torch.float8_e4m3fn).view(torch.uint8)
+        assert torch.equal(s.cpu()[blk, :, pos % PAGE], torch.from_numpy(scale))
+        assert torch.equal(p.view(torch.uint8).cpu()[blk, :, pos % PAGE], want)
