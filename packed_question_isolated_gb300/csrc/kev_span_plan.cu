@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(const __grid_con
       base0[n] = all.items[0];
       base1[n] = all.items[1];
     }
-    if (words && n > 0 && clean) {  // pages: one or more warps per question, a lane per page; a block's bit may be set once
+    if (words && clean) {  // pages: one or more warps per question, a lane per page; a block's bit may be set once
       const int slices = n < kThreads / 32 ? kThreads / 32 / n : 1;
 #pragma unroll 1
       for (int x = warp; x < n * slices; x += kThreads / 32) {
@@ -371,6 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(const __grid_con
 cudaError_t launch_span_plan(const SpanArgs& a, int lines, const SpanArgs* line0, const SpanArgs* line1, cudaStream_t s) {
   PlanArgs p = {};
   p.a = a;
+  if (a.n == 0) p.a.pool_elem = 0;  // no questions, no pages: the kernel divides by n where there are (a test there: 0.4 us a call)
   p.lines = lines;
   // intervals, prefixes and first items of the questions, and beside them the largest of: the sort
   // keys, the bit map of the blocks, the tile counts of the items
