@@ -88,7 +88,9 @@ struct Bars {
   uint32_t tmem;
   int abort;
   int never;
-  int bad;  // the last unit, + 1, known to have NaN or infinities in V (e4m3: in its scales) at tiles with masked keys
+  // [u % 64]: unit u (or one that many times 64 before it) has NaN or infinities in V (e4m3: in its scales) at
+  // tiles with masked keys.  Never cleared: nothing holds the next units' tiles back until an epilogue has read it
+  int bad[64];
 };
 static_assert(sizeof(Bars) <= 1024, "barriers");
 
@@ -183,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bars->stall, 1);
     bars->abort = 0;
     bars->never = 0;
-    bars->bad = 0;
+    for (int u = 0; u < 64; ++u) bars->bad[u] = 0;
     fence_mbar_init();
   }
   if (warp == kLoadWarp && lane == 0) {
@@ -412,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   }
                 }
                 if (__any_sync(0xffffffffu, any != 0)) {
-                  if (lane == 0) atomicMax(&bars->bad, (int)n + 1);
+                  if (lane == 0) *reinterpret_cast<volatile int*>(&bars->bad[n & 63]) = 1;
                   fence_proxy_async_smem();
                 }
               }
@@ -435,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sc[0] = k > 0.f ? fmaxf(k * p.scale_log2, 1.17549435e-38f) : 1.f;
                 if (edge && !(fabsf(v) <= 3.4028235e38f)) {
                   sc[kBN] = 0.f;
-                  atomicMax(&bars->bad, (int)n + 1);
+                  *reinterpret_cast<volatile int*>(&bars->bad[n & 63]) = 1;
                 }
                 mbar_arrive_warp(&bars->sc_full[tiles_done % kScaleSlots]);
               }
@@ -631,14 +633,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++o_cnt;
         tc_fence_after();
+        const bool bad = *reinterpret_cast<volatile int*>(&bars->bad[n & 63]);  // at worst nothing is found to put back
         uint32_t o[D / 32][32];
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) tmem_ld32(tm_o + c * 32, o[c]);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) tmem_ld_wait(o[c]);
-        // Set before this unit's tiles were ready.  It only grows, so a late epilogue cannot miss it, whatever the
-        // later units' tiles did to it meanwhile: at worst it looks through a unit that has nothing to put back.
-        const bool bad = *reinterpret_cast<volatile int*>(&bars->bad) > (int)n;
         tc_fence_before();
         mbar_arrive_warp(&bars->o_free[t]);
         if (bad && row_ok) {
