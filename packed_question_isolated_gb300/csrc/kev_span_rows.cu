@@ -488,7 +488,8 @@ __global__ void __launch_bounds__(kThreads, few_rows_ctas(D, NT))
       ++n;
       // fp16 has no exponents to spare: a row of q is scaled by a power of two that puts its largest element
       // in [2^14, 2^15) -- exact down to 2^-29 of it, and off by at most 2^-40 of it below -- and the
-      // scores by its inverse
+      // scores by its inverse; or by 2^126, the largest that has an inverse, which is exact for every element of
+      // the rows below 2^-112 that it is left to
       float q_inv[NT][2];
       if (E == 1) {
 #pragma unroll
@@ -501,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, few_rows_ctas(D, NT))
               top = max(top, max(q[nt][i][x] & 0x7fffu, q[nt][i][x] >> 16 & 0x7fffu));
           top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          const int up = min(127 + 14 - (int)(top >> 7), 100);  // 2^up; 14 - (exponent - 127)
+          const int up = min(127 + 14 - (int)(top >> 7), 126);  // 2^up; 14 - (exponent - 127)
           const float mul = __int_as_float((127 + up) << 23);
 #pragma unroll
           for (int i = 0; i < kChunks * kSteps; ++i)

@@ -336,3 +336,19 @@ def test_rows_with_subnormal_scales_are_written_as_defined(dtype, d, how):
         want = torch.from_numpy(code).float().to(torch.float8_e4m3fn).view(torch.uint8)
         assert torch.equal(s.cpu()[blk, :, pos % PAGE], torch.from_numpy(scale))
         assert torch.equal(p.view(torch.uint8).cpu()[blk, :, pos % PAGE], want)
+
+
+@pytest.mark.parametrize("shift", [-124, -118, -110, -100, -60, 60, 100])
+@pytest.mark.parametrize("dtype,pool,d", [("bf16", "e4m3", 128), ("bf16", "e4m3", 64), ("bf16", "bf16", 128), ("fp32", "e4m3", 64)])
+@pytest.mark.parametrize("lens,max_chunk", [([1, 1], 1), ([2, 1], 2), ([20, 40], 0)])
+def test_small_q_and_large_k_and_the_other_way_round(lens, max_chunk, dtype, pool, d, shift):
+    """Rows of q times 2^shift, cached K times 2^-shift: the scores are as without either."""
+    b = Span(450, lens, [300, 17], 8, 2, d, dtype, pool)
+    b.write()
+    b.q.copy_(torch.ldexp(b.q.double(), torch.tensor(shift, device="cuda")).to(b.q.dtype))
+    pk, sk = b.pools[0]
+    x = pk if sk is None else sk
+    x.copy_(torch.ldexp(x.double(), torch.tensor(-shift, device="cuda")).to(x.dtype))
+    b.chunk(max_chunk=max_chunk, write=False)
+    b.ok()
+    judge(b, b.caches(), weights=2.0 ** -11 if (dtype, pool) == ("bf16", "e4m3") and max_chunk else 2.0 ** -8)
