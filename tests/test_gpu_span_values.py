@@ -352,3 +352,39 @@ def test_small_q_and_large_k_and_the_other_way_round(lens, max_chunk, dtype, poo
     b.chunk(max_chunk=max_chunk, write=False)
     b.ok()
     judge(b, b.caches(), weights=2.0 ** -11 if (dtype, pool) == ("bf16", "e4m3") and max_chunk else 2.0 ** -8)
+
+
+@pytest.mark.parametrize("side", ["k", "v", "q"])
+@pytest.mark.parametrize("dtype,pool", [("bf16", "bf16"), ("bf16", "e4m3"), ("fp32", "fp32"), ("fp32", "e4m3")])
+@pytest.mark.parametrize("lens,prefix,max_chunk", [([1, 1, 1], [300, 129, 5], 1), ([2, 1, 2], [300, 129, 126], 2),
+                                                   ([40, 1, 150], [300, 129, 5], 0), ([1] * 20 + [70], [9 * i for i in range(21)], 0)])
+def test_rows_that_see_a_nan_are_nan_and_no_others(lens, prefix, max_chunk, dtype, pool, side):
+    """NaN in a new row of q, k or v (through the cache it goes into) and, for k and v, in a cached one."""
+    b = Span(460, lens, prefix, 8, 2, 128, dtype, pool)
+    b.write()
+    bad = int(b.intervals[-1, 0]) + lens[-1] // 2  # a token of the last question
+    at = prefix[-1] + lens[-1] // 2
+    if side == "q":
+        b.q[bad, 3] = float("nan")
+    else:
+        x = b.k if side == "k" else b.v
+        x[bad, 1] = float("nan")
+        p, s = b.pools["kv".index(side)]  # and position 3 of question 0, head 0
+        if s is None:
+            p[b.table[0, 0], 0, 3] = float("nan")
+        else:
+            p.view(torch.uint8)[b.table[0, 0], 0, 3] = 0x7f
+            s[b.table[0, 0], 0, 3] = float("nan")
+    b.chunk(max_chunk=max_chunk)
+    b.ok()
+    nan = torch.isnan(b.out.float()).cpu().numpy()
+    want = np.zeros(nan.shape, bool)
+    if side == "q":
+        want[bad, 3] = True
+    else:
+        s0, e0 = b.intervals[0]
+        want[[t for t in range(s0, e0) if prefix[0] + t - s0 >= 3], :4] = True
+        s1, e1 = b.intervals[-1]
+        want[[t for t in range(s1, e1) if prefix[-1] + t - s1 >= at], 4:] = True
+    assert (nan == want).all(), np.argwhere(nan != want)[:5]
+    assert np.isfinite(b.out.float().cpu().numpy()[~want]).all()
