@@ -11,7 +11,7 @@
 // Bound by memory: 2 T H_kv (d elem + d + 4) bytes each way for an e4m3 cache.  A warp takes one
 // token's K and V rows of all kv heads: one search for the token's question (in shared memory) and
 // one page look-up, then 16-byte loads with up to 8 in flight per lane (8 heads of 128 bf16: exactly
-// 8).  Measured: 97k tokens of 8 heads read back in 100 us (6.0 TB/s, 88 % of the measured copy rate);
+// 8).  Measured: 97k tokens of 8 heads read back in 102 us (5.9 TB/s, 87 % of the measured copy rate);
 // 27k tokens written in 42.6 us (4.0 TB/s: neither fewer instructions nor more bytes in flight moved it; the
 // writes land 128 bytes at a time, 16 KB apart).
 #include <cuda_fp8.h>
@@ -261,8 +261,9 @@ __global__ void __launch_bounds__(kThreads) span_copy_kernel(SpanArgs a, void* k
 // The checks of the plan (kev_span_plan.cu) and the copy in one kernel, for small calls: every CTA makes all
 // the checks for itself, in shared memory, and comes to the same verdict, so none has to wait for another.
 // Overlapping intervals show as a token that is marked twice; the mark is also the token's question.  A warp
-// copies one token's K or V.  Measured for one token of each of 32 questions 3.6 us, with two kernels 7.0; at the
-// ends of what it takes, a chunk of 512 tokens 4.9 against 7.3 and 512 questions of one token 9.0 against 15.6.
+// copies one token's K or V.  Measured on the GPU (the call takes the host 7.2 us) for one token of each of 32
+// questions 3.6 us, with two kernels 7.0; at the ends of what it takes, a chunk of 512 tokens 4.9 against 7.3 and
+// 512 questions of one token 9.0 against 15.6.
 template <int E, int D, bool Q8, bool kRead>
 __global__ void __launch_bounds__(kSmallThreads) span_small_copy_kernel(SpanArgs a, void* k_out, void* v_out) {
   extern __shared__ unsigned small_smem[];

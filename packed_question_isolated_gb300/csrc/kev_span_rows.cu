@@ -25,7 +25,8 @@
 // Measured on a GB300: decode of 16 bf16 caches of 2 to 32 Ki positions 116 us (5.7 TB/s, 84 % of the
 // measured copy rate); 32 e4m3 caches of 64 to 2400 positions 29 us and 64 windowed ones (1024 positions, 4
 // sinks) 37 us, of which the plan is 5 to 7, the first page 4 and the last unit's joins 4: with 10 to 17
-// pages per SM these are most of it.  Measured and left: 8 warps with tcgen05-shaped 128-row tiles (the
+// pages per SM these are most of it.  16 long e4m3 caches take 84 us (4.0 TB/s, 59 %): there the conversions, one
+// per two codes, are the likely bound.  Measured and left: 8 warps with tcgen05-shaped 128-row tiles (the
 // tensor-core kernel: 78 us for the 32 caches); codes widened to bf16 by integer operations (94 us against
 // 82 for 16 long caches); the joins by the warps that compute (31.9 against 31.2); the new rows written by a
 // warp of their own before their pages are loaded (33 against 31).
