@@ -4,9 +4,10 @@
 // c_e = rn_e4m3(x_e / s) and one fp32 scale s = max_e |x_e| / 448 (448: the largest e4m3 value), so
 // a row's largest element is stored exactly up to fp32 rounding and every other one within half
 // an e4m3 step of its size (relative 2^-4, or 2^-10 s below the normal range; 448 times the rounding
-// of s beside that, which counts where s is subnormal).  A row of zeros has s = 0 and codes 0; a row that holds a NaN or an infinity has a NaN for its scale and reads
-// back as NaN throughout.  Reading gives c_e * s, rounded once to the output type.  Both
-// quotients are the correctly rounded ones: the codes do not depend on the kernel's shape.
+// of s beside that, which counts where s is subnormal).  A row of zeros has s = 0 and codes 0; a row
+// that holds a NaN or an infinity has a NaN for its scale and reads back as NaN throughout.  Reading
+// gives c_e * s, rounded once to the output type.  Both quotients are the correctly rounded ones: the
+// codes do not depend on the kernel's shape.
 //
 // Bound by memory: 2 T H_kv (d elem + d + 4) bytes each way for an e4m3 cache.  A warp takes one
 // token's K and V rows of all kv heads: one search for the token's question (in shared memory) and

@@ -371,7 +371,8 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(const __grid_con
 cudaError_t launch_span_plan(const SpanArgs& a, int lines, const SpanArgs* line0, const SpanArgs* line1, cudaStream_t s) {
   PlanArgs p = {};
   p.a = a;
-  if (a.n == 0) p.a.pool_elem = 0;  // no questions, no pages: the kernel divides by n where there are (a test there: 0.4 us a call)
+  // No questions, no pages: the kernel divides by n where there are pages (a test in the kernel costs 0.4 us a call)
+  if (a.n == 0) p.a.pool_elem = 0;
   p.lines = lines;
   // intervals, prefixes and first items of the questions, and beside them the largest of: the sort
   // keys, the bit map of the blocks, the tile counts of the items

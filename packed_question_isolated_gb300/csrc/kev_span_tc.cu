@@ -18,18 +18,20 @@
 //   warp 10          loads the q tiles: a 3-D box of tokens x group heads x 64 dims
 //   warps 12-15      make the loaded tiles ready.  bf16: on tiles with masked keys, NaN and infinities
 //                    in V become zeros (0 x NaN would reach rows that do not see the key; the
-//                    epilogue puts them back for the rows that do, by a flag per unit: reading it costs 0.3 % of
-//                    the prompts below, and where in the epilogue moves them by up to 2 %).  e4m3: the codes become bf16,
-//                    which holds every e4m3 value exactly, in the MMA's swizzled layout; the scales
-//                    multiply S (K) and P (V) in fp32 instead, so quantisation is the only loss.
+//                    epilogue puts them back for the rows that do, by a flag per unit; where it
+//                    reads the flag moves the whole kernel by up to 2 %).  e4m3: the codes become
+//                    bf16, which holds every e4m3 value exactly, in the MMA's swizzled layout; the
+//                    scales multiply S (K) and P (V) in fp32 instead, so quantisation is the only
+//                    loss.
 // What bounds it.  With many rows the shared-memory reads of the MMA operands, which share the 128 bytes a
 // clock with the loads: S and PV of a 128 x 128 x 128 tile take about 750 clocks instead of 512, and the two
 // row tiles' softmax (about 1450 clocks each) and MMAs then fill each other's gaps to about 3300 clocks a key
 // tile.  Over e4m3 the codes' way through shared memory adds 96 KB a key tile and bounds it at about 4100.
 // With few rows the latency of one key tile's chain, S - softmax - PV.  Measured on a GB300 at the clocks it
 // keeps under load: 27k tokens under a window of 2048 715 to 750 us, from one GPU to the next (766 GFLOP useful,
-// 1.02 to 1.07 PFLOP/s, 53 to 56 % of the measured burst peak); 8 chunks of 128 to 1024 tokens over bf16 caches 131 us, over e4m3 ones of up to 16k
-// positions 336 us (0.64 PFLOP/s); 8 prompts under a window of 512 100 us, 64 short ones at d = 64 60 us.
+// 1.02 to 1.07 PFLOP/s, 53 to 56 % of the measured burst peak); 8 chunks of 128 to 1024 tokens over bf16 caches
+// 132 us, over e4m3 ones of up to 16k positions 337 us (0.64 PFLOP/s); 8 prompts under a window of 512 99 us, 64
+// short ones at d = 64 59 us.
 // Why these tiles: all G heads of a group on one row tile load each K/V tile once and waste nothing on short
 // chunks; two row tiles per CTA are what 512 columns of tensor memory hold (S and O in fp32, P over S).
 // Measured and left: scores in pieces of 32 keys, for fewer registers (855 us against 729); a ring of 5
