@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from test_gpu_span import Span
-from test_gpu_span_values import judge, with_scale
+from test_gpu_span_values import against_oracle, with_scale
 
 pytestmark = pytest.mark.gpu
 
@@ -20,7 +20,7 @@ def test_chunks_with_a_scale(dtype, pool, mask, scale):
     b = with_scale(Span(500, [3, 0, 70, 1], [5, 9, 250, 600], 8, 2, 128, dtype, pool, gaps=1), scale)
     b.chunk(*mask)
     b.ok()
-    judge(b, b.caches(), mask, scale)
+    against_oracle(b, b.caches(), mask, scale)
 
 
 @pytest.mark.parametrize("scale", [None] + SCALES)
@@ -31,7 +31,7 @@ def test_decode_with_a_scale(dtype, pool, h_q, h_kv, d, mask, scale):
     b = with_scale(Span(501 + d, [1, 1, 0, 1, 1, 1], [0, 128, 50, 511, 2500, 640], h_q, h_kv, d, dtype, pool), scale)
     b.chunk(*mask, max_chunk=1)
     b.ok()
-    judge(b, b.caches(), mask, scale, weights=2.0 ** -11 if (dtype, pool) == ("bf16", "e4m3") else 2.0 ** -8)
+    against_oracle(b, b.caches(), mask, scale, weights=2.0 ** -11 if (dtype, pool) == ("bf16", "e4m3") else 2.0 ** -8)
 
 
 @pytest.mark.parametrize("scale", SCALES)
@@ -43,7 +43,7 @@ def test_mixed_rounds_with_a_scale(pool, scale):
     b = with_scale(Span(502, lens, prefix, 8, 2, 128, "bf16", pool, order=r.permutation(len(lens)).tolist()), scale)
     b.chunk()
     b.ok()
-    judge(b, b.caches(), scale=scale)
+    against_oracle(b, b.caches(), scale=scale)
 
 
 @pytest.mark.parametrize("scale", SCALES)
@@ -55,7 +55,7 @@ def test_packed_windows_with_a_scale(dtype, h_q, h_kv, d, scale):
     b.packed(60, 3)
     b.ok()
     k, v = (x.float().cpu().numpy().astype(np.float64) for x in (b.k, b.v))
-    judge(b, [(k[s:e], v[s:e]) for s, e in b.intervals], (60, 3), scale)
+    against_oracle(b, [(k[s:e], v[s:e]) for s, e in b.intervals], (60, 3), scale)
 
 
 @pytest.mark.parametrize("h_q,h_kv,d,mask", [(8, 2, 128, (0, 0)), (16, 1, 64, (300, 2)), (4, 4, 64, (0, 0))])
@@ -69,4 +69,4 @@ def test_decode_over_e4m3_with_weights_that_span_a_wide_range(h_q, h_kv, d, mask
     sv *= torch.exp2(torch.randint(-30, 31, sv.shape, generator=g, device="cuda").float())
     b.chunk(*mask, max_chunk=1, write=False)
     b.ok()
-    judge(b, b.caches(), mask, weights=2.0 ** -11)
+    against_oracle(b, b.caches(), mask, weights=2.0 ** -11)

@@ -23,7 +23,7 @@ from test_gpu_span import PAGE, Span
 pytestmark = pytest.mark.gpu
 
 
-def judge(b, caches, mask=(0, 0), scale=None, weights=2.0 ** -8, rows=None):
+def against_oracle(b, caches, mask=(0, 0), scale=None, weights=2.0 ** -8, rows=None):
     """b.out against the oracle over `caches`; `weights`: half a step of the softmax weights' type; `rows`: the tokens looked at."""
     q = b.q.float().cpu().numpy().astype(np.float64)
     got = b.out.float().cpu().numpy().astype(np.float64)
@@ -88,7 +88,7 @@ def masked_scales(side, bits, batch, dtype, d, scale):
     p.view(torch.uint8)[masked] = torch.randint(0, 256, (int(masked.sum()), d), generator=g, device="cuda", dtype=torch.uint8)
     b.chunk(*mask, max_chunk=mc, write=False)
     b.ok()
-    judge(b, caches, mask, scale)
+    against_oracle(b, caches, mask, scale)
 
 
 # the smallest subnormals (as small integers look in memory that held some), a product with the scale that underflows,
@@ -134,7 +134,7 @@ def test_decode_over_values_of_any_size(pool, h_q, h_kv, d, where, factor):
     set_value_rows(b, WHERE[where], factor)
     b.chunk(max_chunk=1, write=False)
     b.ok()
-    judge(b, b.caches(), weights=2.0 ** -11 if pool == "e4m3" else 2.0 ** -8)
+    against_oracle(b, b.caches(), weights=2.0 ** -11 if pool == "e4m3" else 2.0 ** -8)
 
 
 @pytest.mark.parametrize("above", [20, 90, 110, 114, 116, 118, 120, 122, 124, 126, 130, 150, 200])
@@ -155,7 +155,7 @@ def test_a_key_far_above_the_others_whose_values_are_zero(d, key, above):
     sv[blk, :, r] = 0.0
     b.chunk(max_chunk=1, write=False)
     b.ok()
-    judge(b, b.caches(), weights=2.0 ** -11)
+    against_oracle(b, b.caches(), weights=2.0 ** -11)
 
 
 @pytest.mark.parametrize("factor", [0.0, 1e-43, 1e-40, 1e-37, 1e-35, 1e-33, 1e25])
@@ -167,7 +167,7 @@ def test_chunks_over_values_of_any_size(pool, d, where, factor):
     set_value_rows(b, WHERE[where], factor)
     b.chunk(write=False)
     b.ok()
-    judge(b, b.caches())
+    against_oracle(b, b.caches())
 
 
 @pytest.mark.parametrize("above", [20, 60, 90, 110, 118, 122, 126, 150])
@@ -187,7 +187,7 @@ def test_chunks_with_a_key_far_above_the_others_whose_values_are_zero(d, key, ab
     sv[blk, :, r] = 0.0
     b.chunk(write=False)
     b.ok()
-    judge(b, b.caches())
+    against_oracle(b, b.caches())
 
 
 @pytest.mark.parametrize("pool", ["bf16", "e4m3"])
@@ -351,7 +351,7 @@ def test_small_q_and_large_k_and_the_other_way_round(lens, max_chunk, dtype, poo
     x.copy_(torch.ldexp(x.double(), torch.tensor(-shift, device="cuda")).to(x.dtype))
     b.chunk(max_chunk=max_chunk, write=False)
     b.ok()
-    judge(b, b.caches(), weights=2.0 ** -11 if (dtype, pool) == ("bf16", "e4m3") and max_chunk else 2.0 ** -8)
+    against_oracle(b, b.caches(), weights=2.0 ** -11 if (dtype, pool) == ("bf16", "e4m3") and max_chunk else 2.0 ** -8)
 
 
 @pytest.mark.parametrize("side", ["k", "v", "q"])
