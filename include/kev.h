@@ -66,8 +66,10 @@ typedef enum {
   KEV_ERR_CUDA = 7,          /* a CUDA runtime call failed (launch error, no device, ...) */
   KEV_ERR_POSITION = 8,      /* (device) a position at or past the RoPE table's max_pos */
   KEV_ERR_PREFIX = 9,        /* (device) a cached prefix length negative or not a multiple of 128 */
-  KEV_ERR_SAMPLING = 10,     /* (device) a live temperature negative / not finite, or a uniform outside [0,1) */
-  KEV_ERR_ADAPTER = 11       /* (device) a LoRA adapter id outside [-1, n_adapters) */
+  KEV_ERR_SAMPLING = 10,     /* (device) a live temperature negative / not finite, a uniform outside [0,1), or a token outside
+                                the vocabulary */
+  KEV_ERR_ADAPTER = 11,      /* (device) a LoRA adapter id outside [-1, n_adapters) */
+  KEV_ERR_KEPT = 12          /* (device) kept positions not ascending inside the cached ones, or more of them than fit */
 } kev_status;
 
 typedef enum {
@@ -266,6 +268,25 @@ kev_status kev_sample(const void* logits, int32_t n_questions, int32_t vocab, in
                       const float* uniforms, const uint8_t* active, int32_t* tokens, int32_t* dev_status,
                       kev_stream_t stream);
 
+/* Log probabilities of given tokens, entropy and likeliest tokens of n_rows rows of logits (device [n_rows, vocab] of
+ * `dtype`; any vocab): what a serving program reports beside the token that kev_sample draws, or how likely a model finds
+ * a given text.  With p = softmax(logits_r / T_r):
+ *   logprobs[r] = log p[tokens[r]],   entropy[r] = -sum_k p[k] log p[k],
+ *   top_tokens[r, 0 .. top_n), top_logprobs[r, ..]: the tokens of the largest logits, larger ones first and of equal ones
+ *   the lowest index first, and their log p.
+ * temperature: device float[n_rows], or NULL for 1.  T_r = 0 is the distribution that kev_sample draws from there: all on
+ * the first of the largest logits (log probability 0, -infinity elsewhere; entropy 0).  active: device uint8[n_rows], or
+ * NULL for all; rows of 0 are neither read nor written.  tokens and logprobs: device int32 and float[n_rows], or both
+ * NULL; entropy: device float[n_rows] or NULL; top_n: 0 (top_tokens and top_logprobs not looked at) to
+ * min(vocab, KEV_MAX_TOP), device int32 and float[n_rows, top_n].  Logits of -infinity have probability 0 (a grammar's
+ * mask).  A row that holds a NaN or +infinity, or nothing above -infinity, has no distribution: its floats are NaN and its
+ * top tokens -1.  A live temperature that is negative or not finite, or a live token outside [0, vocab), sets
+ * KEV_ERR_SAMPLING and nothing is written.  fp32 arithmetic.  One kernel. */
+#define KEV_MAX_TOP 32
+kev_status kev_logprobs(const void* logits, int32_t n_rows, int32_t vocab, int32_t dtype, const float* temperature,
+                        const uint8_t* active, const int32_t* tokens, float* logprobs, float* entropy, int32_t top_n,
+                        int32_t* top_tokens, float* top_logprobs, int32_t* dev_status, kev_stream_t stream);
+
 /* ---------------------------------------------------------------------------------------
  * Token-grouped LoRA
  *
@@ -458,6 +479,88 @@ kev_status kev_prefill_attn_window(const void* q, const void* k, const void* v, 
                                    void* out, const kev_attn_shape* shape, void* workspace, size_t workspace_bytes,
                                    int32_t* dev_status, kev_stream_t stream);
 
+/* Query and key norms, the rotation and the cache write in one pass, for the questions and new tokens of the calls above.
+ * For every head row x of q and k, in fp32 and rounded once:
+ *   y = x / sqrt(mean_e x_e^2 + eps) * w   (q_weight, k_weight: [d_h] of the shape's dtype; NULL: y = x),
+ * then y turns as described under the rotary encoding below, at position positions[i] + j for the token begin_i + j
+ * (positions: device int32[n_questions]; NULL: prefix_lens, and 0 without these).  positions counts the tokens that
+ * question i has seen, prefix_lens the rows that its cache holds: after kev_compact_paged they differ.
+ * q, k, v: rows of H_q d_h, H_kv d_h and H_kv d_h elements, the rows of neighbouring tokens q_stride, k_stride and
+ * v_stride elements apart (0: none between them; multiples of 16 bytes), as the rows of one projection are.
+ * q_out [T, H_q, d_h] and k_out [T, H_kv, d_h] (NULL with a cache: not wanted) are contiguous; q_out may be q and k_out
+ * may be k where these are contiguous too, no other overlap.  cache: y of k and the rows of v go to positions P_i + j, as
+ * kev_paged_write puts them but for e4m3 keys, which are quantised from the fp32 row (one rounding instead of two); NULL:
+ * no cache is written and v is not read.  Rows of tokens in no interval are neither read nor written.  A position outside
+ * [0, max_pos) sets KEV_ERR_POSITION (after the errors above).  A row of q or k whose sum of squares overflows comes back
+ * as zeros.  With a weight, eps > 0.  One kernel for up to 512 tokens and questions (and 2^18 blocks), else two. */
+kev_status kev_norm_rope_paged(const void* q, const void* k, const void* v, int32_t q_stride, int32_t k_stride,
+                               int32_t v_stride, void* q_out, void* k_out, int32_t total_tokens,
+                               const kev_interval* intervals, int32_t n_questions, const int32_t* prefix_lens,
+                               const int32_t* positions, const void* q_weight, const void* k_weight, float eps,
+                               const void* rope_table, int32_t max_pos, const kev_paged_cache* cache,
+                               const kev_attn_shape* shape, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                               kev_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Eviction: a paged cache cut to its most attended positions
+ *
+ * A question's cache need not hold every position.  kev_attn_mass_paged adds up how much attention each cached position
+ * receives (per kv head, over its group's q-heads and the new tokens); kev_select_paged chooses, per question and kv head,
+ * the positions that stay: the first few, the last few and the most attended between them; kev_compact_paged moves their
+ * rows to the front, in their order.  Afterwards the question holds kept_lens[i] positions: that is its prefix_lens[i] in
+ * the calls above, its blocks past them are free, and its rotations go on from the tokens seen (kev_norm_rope_paged).
+ * Each kv head keeps positions of its own, all of them equally many.  Windows count cached rows, so windowed layers are
+ * not cut this way.  The keys keep the rotation that they were cached with.
+ *
+ * mass: device float [n_blocks, H_kv, KEV_PAGE], 16-byte aligned, beside the cache: position p of question i and kv head g
+ * at block_table[i * max_blocks + p / KEV_PAGE], g, p % KEV_PAGE.
+ * ------------------------------------------------------------------------------------- */
+
+/* Bytes of device workspace of kev_attn_mass_paged for at most `n_questions` questions with `total_tokens` packed new
+ * tokens (256-byte aligned, no initial value; not shared by calls in flight together).  0 on bad arguments. */
+size_t kev_attn_mass_workspace_size(int32_t n_questions, int32_t total_tokens, const kev_attn_shape* shape);
+
+/* For every question i and its cached positions u < P_i + L_i, the new tokens' rows among them (they are in the cache
+ * already: kev_chunk_attn_paged or kev_norm_rope_paged put them there):
+ *   mass[u, g] = (u < P_i ? decay * mass[u, g] : 0) + sum over j < L_i and q-heads h of g of w_{j,h}[u]
+ * with w_{j,h} = softmax_u(scale q[begin_i + j, h] . K_i[u, g]) over u <= P_i + j, K_i as the cache holds it.  decay is
+ * finite and not negative: 1 adds up, 0 counts afresh (the old values are not read), between them old attention fades.
+ * Only K is read; V may be anything.  Questions without new tokens are left as they are.  Errors and max_chunk as for
+ * kev_chunk_attn_paged.  Scores and sums in fp32 (bf16 q: products on the tensor cores).  The result does not depend on
+ * the order in which the GPU works. */
+kev_status kev_attn_mass_paged(const void* q, int32_t total_tokens, const kev_interval* intervals, int32_t n_questions,
+                               const int32_t* prefix_lens, int32_t max_chunk, const kev_paged_cache* cache, float decay,
+                               float* mass, const kev_attn_shape* shape, void* workspace, size_t workspace_bytes,
+                               int32_t* dev_status, kev_stream_t stream);
+
+/* Bytes of device workspace of the two calls below (256-byte aligned, no initial value; not shared by calls in flight
+ * together).  0 on bad arguments. */
+size_t kev_evict_workspace_size(int32_t n_questions, int32_t keep, const kev_attn_shape* shape);
+
+/* For every live question (active: device uint8[n_questions], or NULL for all) with lens[i] cached positions, and every
+ * kv head g: kept[i, g, 0 .. kept_lens[i]) in ascending order, kept_lens[i] = min(lens[i], keep) -- all positions where
+ * they fit, else the first `first`, the last `last` and of the others those of the largest mass, of equal mass the lowest
+ * positions (a NaN counts as larger than any number).  Of a question that is not live kept_lens[i] = lens[i], and its kept
+ * is left as it is.  kept: device int32 [n_questions, H_kv, keep]; kept_lens: device int32[n_questions], not lens itself.
+ * keep > 0, first and last not negative, first + last <= keep (else KEV_ERR_INVALID_ARG).  Device errors:
+ * KEV_ERR_SLOT_OVERFLOW (a live lens[i] negative or past max_blocks * KEV_PAGE), KEV_ERR_SLOT (a block of its pages out of
+ * range).  Of the shape only h_kv counts. */
+kev_status kev_select_paged(const float* mass, const int32_t* lens, const uint8_t* active, int32_t n_questions,
+                            const int32_t* block_table, int32_t max_blocks, int32_t n_blocks, int32_t keep, int32_t first,
+                            int32_t last, int32_t* kept, int32_t* kept_lens, const kev_attn_shape* shape, void* workspace,
+                            size_t workspace_bytes, int32_t* dev_status, kev_stream_t stream);
+
+/* Rows kept[i, g, j] of the K, V (and scales) of kv head g of question i, and of mass where it is given, to position j,
+ * for j < kept_lens[i], for every question with kept_lens[i] < lens[i] (the others are left as they are, their kept and
+ * pages not looked at).  In place: rows from kept_lens[i] on hold nothing of use afterwards.  kept as kev_select_paged
+ * writes it, or by any other rule: per question and head strictly ascending within [0, lens[i]), else KEV_ERR_KEPT (also a
+ * kept_lens[i] negative, above keep or above lens[i]).  Other device errors: KEV_ERR_SLOT_OVERFLOW (lens[i] negative or
+ * past max_blocks * KEV_PAGE), KEV_ERR_SLOT (a block of pages in use out of range, or used twice).  All are found before
+ * anything is written. */
+kev_status kev_compact_paged(const int32_t* kept, int32_t keep, const int32_t* lens, const int32_t* kept_lens,
+                             int32_t n_questions, const kev_paged_cache* cache, float* mass, const kev_attn_shape* shape,
+                             void* workspace, size_t workspace_bytes, int32_t* dev_status, kev_stream_t stream);
+
 /* ---------------------------------------------------------------------------------------
  * Rotary position encoding with positions counted per question
  *
@@ -541,7 +644,9 @@ const char* kev_status_string(kev_status status);
  * small calls, else 2: plan, copy), 18 = chunk_attn_paged (plan and attention for few rows per
  * question, 2; else plan, cache write if k is given, attention -- two kernels in a mixed round over an
  * e4m3 cache -- and merge), 19 = prefill_attn_window (3: plan, attention, merge).  16 to 18: the most
- * recent call's, 2 before any.  18 and 19 launch the plan alone, 1, without tokens.  -1 for an unknown id. */
+ * recent call's, 2 before any.  18 and 19 launch the plan alone, 1, without tokens.  20 = norm_rope_paged (as 16),
+ * 21 = attn_mass_paged (the most recent call's, 4 before any; the plan alone, 1, without tokens), 22 = select_paged (2:
+ * checks, selection), 23 = compact_paged (2: checks, move), 24 = logprobs (1).  -1 for an unknown id. */
 int32_t kev_launch_count(int32_t entry_point);
 
 #ifdef __cplusplus

@@ -34,17 +34,20 @@ KEV_ERR_POSITION = 8
 KEV_ERR_PREFIX = 9
 KEV_ERR_SAMPLING = 10
 KEV_ERR_ADAPTER = 11
+KEV_ERR_KEPT = 12
 KEV_BF16 = 0
 KEV_FP32 = 1
 KEV_E4M3 = 2
 KEV_PAGE = 128
 KEV_MAX_PAGED_ENTRIES = 16384
 KEV_MAX_QUESTIONS = 4096
+KEV_MAX_TOP = 32
 
 STATUS_NAMES = {
     0: "KEV_OK", 1: "KEV_ERR_INVALID_ARG", 2: "KEV_ERR_UNSUPPORTED", 3: "KEV_ERR_INTERVALS",
     4: "KEV_ERR_SLOT", 5: "KEV_ERR_SLOT_OVERFLOW", 6: "KEV_ERR_TIMEOUT", 7: "KEV_ERR_CUDA",
     8: "KEV_ERR_POSITION", 9: "KEV_ERR_PREFIX", 10: "KEV_ERR_SAMPLING", 11: "KEV_ERR_ADAPTER",
+    12: "KEV_ERR_KEPT",
 }
 
 # every symbol include/kev.h declares
@@ -57,7 +60,8 @@ EXPORTED = [
     "kev_decode_attn_rope", "kev_prefill_attn_paged", "kev_kv_write_paged", "kev_decode_attn_paged",
     "kev_assign_blocks", "kev_prefill_chunk", "kev_sample", "kev_lora_apply",
     "kev_paged_workspace_size", "kev_paged_write", "kev_paged_read", "kev_chunk_attn_paged",
-    "kev_prefill_attn_window",
+    "kev_prefill_attn_window", "kev_norm_rope_paged", "kev_attn_mass_workspace_size", "kev_attn_mass_paged",
+    "kev_evict_workspace_size", "kev_select_paged", "kev_compact_paged", "kev_logprobs",
 ]
 
 
@@ -140,6 +144,15 @@ _c = {
                                  _Z, _P, _P),
     "kev_prefill_attn_window": _sig("kev_prefill_attn_window", _I, _P, _P, _P, _I, _P, _I, _I, _I, _P, _S, _P, _Z, _P,
                                     _P),
+    "kev_norm_rope_paged": _sig("kev_norm_rope_paged", _I, _P, _P, _P, _I, _I, _I, _P, _P, _I, _P, _I, _P, _P, _P, _P,
+                                ctypes.c_float, _P, _I, _C, _S, _P, _Z, _P, _P),
+    "kev_attn_mass_workspace_size": _sig("kev_attn_mass_workspace_size", _Z, _I, _I, _S),
+    "kev_attn_mass_paged": _sig("kev_attn_mass_paged", _I, _P, _I, _P, _I, _P, _I, _C, ctypes.c_float, _P, _S, _P, _Z,
+                                _P, _P),
+    "kev_evict_workspace_size": _sig("kev_evict_workspace_size", _Z, _I, _I, _S),
+    "kev_select_paged": _sig("kev_select_paged", _I, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _P, _P, _S, _P, _Z, _P, _P),
+    "kev_compact_paged": _sig("kev_compact_paged", _I, _P, _I, _P, _P, _I, _C, _P, _S, _P, _Z, _P, _P),
+    "kev_logprobs": _sig("kev_logprobs", _I, _P, _I, _I, _I, _P, _P, _P, _P, _P, _I, _P, _P, _P, _P),
 }
 
 
@@ -509,3 +522,65 @@ def kev_prefill_attn_window(q, k, v, total_tokens, intervals, n_questions, windo
                                        int(n_questions), int(window), int(sinks), _ptr(out), ctypes.byref(s),
                                        _ptr(workspace), int(workspace_bytes), _ptr(dev_status), _stream(stream))
     return _check(st, "kev_prefill_attn_window", check)
+
+
+def kev_norm_rope_paged(q, k, v, q_stride, k_stride, v_stride, q_out, k_out, total_tokens, intervals, n_questions,
+                        prefix_lens, positions, q_weight, k_weight, eps, rope_table, max_pos, cache, shape, workspace,
+                        workspace_bytes, dev_status=None, stream=None, check=True) -> int:
+    """Query and key norms, the rotation and the cache write in one pass (``cache`` None: no write;
+    strides in elements, 0: contiguous)."""
+    s = _shape(shape)
+    st = _c["kev_norm_rope_paged"](_ptr(q), _ptr(k), _ptr(v), int(q_stride), int(k_stride), int(v_stride), _ptr(q_out),
+                                   _ptr(k_out), int(total_tokens), _ptr(intervals), int(n_questions), _ptr(prefix_lens),
+                                   _ptr(positions), _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(rope_table),
+                                   int(max_pos), None if cache is None else ctypes.byref(cache), ctypes.byref(s),
+                                   _ptr(workspace), int(workspace_bytes), _ptr(dev_status), _stream(stream))
+    return _check(st, "kev_norm_rope_paged", check)
+
+
+def kev_attn_mass_workspace_size(n_questions: int, total_tokens: int, shape) -> int:
+    s = _shape(shape)
+    return int(_c["kev_attn_mass_workspace_size"](int(n_questions), int(total_tokens), ctypes.byref(s)))
+
+
+def kev_attn_mass_paged(q, total_tokens, intervals, n_questions, prefix_lens, max_chunk, cache, decay, mass, shape,
+                        workspace, workspace_bytes, dev_status=None, stream=None, check=True) -> int:
+    s = _shape(shape)
+    st = _c["kev_attn_mass_paged"](_ptr(q), int(total_tokens), _ptr(intervals), int(n_questions), _ptr(prefix_lens),
+                                   int(max_chunk), ctypes.byref(cache), float(decay), _ptr(mass), ctypes.byref(s),
+                                   _ptr(workspace), int(workspace_bytes), _ptr(dev_status), _stream(stream))
+    return _check(st, "kev_attn_mass_paged", check)
+
+
+def kev_evict_workspace_size(n_questions: int, keep: int, shape) -> int:
+    s = _shape(shape)
+    return int(_c["kev_evict_workspace_size"](int(n_questions), int(keep), ctypes.byref(s)))
+
+
+def kev_select_paged(mass, lens, active, n_questions, block_table, max_blocks, n_blocks, keep, first, last, kept,
+                     kept_lens, shape, workspace, workspace_bytes, dev_status=None, stream=None, check=True) -> int:
+    s = _shape(shape)
+    st = _c["kev_select_paged"](_ptr(mass), _ptr(lens), _ptr(active), int(n_questions), _ptr(block_table),
+                                int(max_blocks), int(n_blocks), int(keep), int(first), int(last), _ptr(kept),
+                                _ptr(kept_lens), ctypes.byref(s), _ptr(workspace), int(workspace_bytes),
+                                _ptr(dev_status), _stream(stream))
+    return _check(st, "kev_select_paged", check)
+
+
+def kev_compact_paged(kept, keep, lens, kept_lens, n_questions, cache, mass, shape, workspace, workspace_bytes,
+                      dev_status=None, stream=None, check=True) -> int:
+    s = _shape(shape)
+    st = _c["kev_compact_paged"](_ptr(kept), int(keep), _ptr(lens), _ptr(kept_lens), int(n_questions),
+                                 ctypes.byref(cache), _ptr(mass), ctypes.byref(s), _ptr(workspace),
+                                 int(workspace_bytes), _ptr(dev_status), _stream(stream))
+    return _check(st, "kev_compact_paged", check)
+
+
+def kev_logprobs(logits, n_rows, vocab, dtype, temperature, active, tokens, logprobs, entropy, top_n=0, top_tokens=None,
+                 top_logprobs=None, dev_status=None, stream=None, check=True) -> int:
+    if isinstance(dtype, str):
+        dtype = {"bf16": KEV_BF16, "fp32": KEV_FP32}[dtype]
+    st = _c["kev_logprobs"](_ptr(logits), int(n_rows), int(vocab), int(dtype), _ptr(temperature), _ptr(active),
+                            _ptr(tokens), _ptr(logprobs), _ptr(entropy), int(top_n), _ptr(top_tokens),
+                            _ptr(top_logprobs), _ptr(dev_status), _stream(stream))
+    return _check(st, "kev_logprobs", check)

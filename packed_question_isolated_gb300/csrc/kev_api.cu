@@ -452,6 +452,39 @@ kev_status kev_sample(const void* logits, int32_t n_questions, int32_t vocab, in
   return from_cuda(launch_sample(a, (cudaStream_t)stream));
 }
 
+kev_status kev_logprobs(const void* logits, int32_t n_rows, int32_t vocab, int32_t dtype, const float* temperature,
+                        const uint8_t* active, const int32_t* tokens, float* logprobs, float* entropy, int32_t top_n,
+                        int32_t* top_tokens, float* top_logprobs, int32_t* dev_status, kev_stream_t stream) {
+  if (n_rows < 0 || vocab <= 0 || top_n < 0 || top_n > vocab) return KEV_ERR_INVALID_ARG;
+  if (dtype != KEV_BF16 && dtype != KEV_FP32) return KEV_ERR_UNSUPPORTED;
+  // chunks and tiles past a row's end are counted in 32 bits
+  if (top_n > KEV_MAX_TOP || vocab > (1 << 30)) return KEV_ERR_UNSUPPORTED;
+  if ((uintptr_t)dev_status & 3u) return KEV_ERR_INVALID_ARG;
+  if (n_rows == 0) return KEV_OK;
+  if (!logits || !aligned16(logits) || ((uintptr_t)temperature & 3u)) return KEV_ERR_INVALID_ARG;
+  if (!tokens != !logprobs || ((uintptr_t)tokens & 3u) || ((uintptr_t)logprobs & 3u) || ((uintptr_t)entropy & 3u))
+    return KEV_ERR_INVALID_ARG;
+  if (top_n > 0 && (!top_tokens || !top_logprobs || ((uintptr_t)top_tokens & 3u) || ((uintptr_t)top_logprobs & 3u)))
+    return KEV_ERR_INVALID_ARG;
+  const int sms = num_sms_of_current_device();
+  if (sms <= 0) return KEV_ERR_CUDA;
+  LogprobsArgs a;
+  a.logits = logits;
+  a.n = n_rows;
+  a.vocab = vocab;
+  a.elem = dtype == KEV_BF16 ? 2 : 4;
+  a.temperature = temperature;
+  a.active = active;
+  a.tokens = tokens;
+  a.logprobs = logprobs;
+  a.entropy = entropy;
+  a.top_n = top_n;
+  a.top_tokens = top_tokens;
+  a.top_logprobs = top_logprobs;
+  a.dev_status = dev_status;
+  return from_cuda(launch_logprobs(a, sms, (cudaStream_t)stream));
+}
+
 kev_status kev_prefill_chunk(const void* q, const void* k, const void* v, int32_t total_tokens,
                              const kev_interval* intervals, int32_t n_questions, const int32_t* prefix_lens,
                              const int32_t* slot_ids, void* pool_k, void* pool_v, int32_t n_slots, int32_t slot_cap,
@@ -877,7 +910,7 @@ kev_status kev_read_status(const int32_t* dev_status, kev_stream_t stream) {
   if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return KEV_ERR_CUDA;
   int32_t h = 0;
   if (cudaMemcpy(&h, dev_status, sizeof(h), cudaMemcpyDeviceToHost) != cudaSuccess) return KEV_ERR_CUDA;
-  if (h < KEV_OK || h > KEV_ERR_ADAPTER) return KEV_ERR_CUDA;
+  if (h < KEV_OK || h > KEV_ERR_KEPT) return KEV_ERR_CUDA;
   return (kev_status)h;
 }
 
@@ -893,8 +926,10 @@ const char* kev_status_string(kev_status s) {
     case KEV_ERR_CUDA: return "CUDA runtime error";
     case KEV_ERR_POSITION: return "a position at or past the RoPE table's max_pos";
     case KEV_ERR_PREFIX: return "a cached prefix length negative or not a multiple of 128";
-    case KEV_ERR_SAMPLING: return "a live temperature negative or not finite, or a uniform outside [0, 1)";
+    case KEV_ERR_SAMPLING:
+      return "a live temperature negative or not finite, a uniform outside [0, 1), or a token outside the vocabulary";
     case KEV_ERR_ADAPTER: return "a LoRA adapter id outside [-1, n_adapters)";
+    case KEV_ERR_KEPT: return "kept positions not ascending inside the cached ones, or too many of them";
   }
   return "unknown status";
 }
@@ -921,6 +956,11 @@ int32_t kev_launch_count(int32_t entry_point) {
     case 17: return paged_read_launches();
     case 18: return chunk_launches();
     case 19: return 3;
+    case 20: return norm_rope_launches();
+    case 21: return mass_launches();
+    case 22: return 2;
+    case 23: return 2;
+    case 24: return 1;
   }
   return -1;
 }

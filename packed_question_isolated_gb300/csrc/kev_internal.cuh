@@ -33,6 +33,7 @@ enum : int32_t {
   ST_PREFIX = KEV_ERR_PREFIX,
   ST_SAMPLING = KEV_ERR_SAMPLING,
   ST_ADAPTER = KEV_ERR_ADAPTER,
+  ST_KEPT = KEV_ERR_KEPT,
 };
 
 // ---------------------------------------------------------------------------------------
@@ -300,6 +301,62 @@ struct SampleArgs {
 cudaError_t launch_sample(const SampleArgs& a, cudaStream_t s);
 
 // ---------------------------------------------------------------------------------------
+// log probabilities, entropy and likeliest tokens (kev_logprobs.cu)
+// ---------------------------------------------------------------------------------------
+struct LogprobsArgs {
+  const void* logits;  // [n, vocab]
+  int32_t n, vocab;
+  int32_t elem;              // 2: bf16, 4: fp32
+  const float* temperature;  // null: 1
+  const uint8_t* active;     // null: all
+  const int32_t* tokens;     // null (with logprobs): not wanted
+  float* logprobs;
+  float* entropy;  // null: not wanted
+  int32_t top_n;
+  int32_t* top_tokens;
+  float* top_logprobs;
+  int32_t* dev_status;
+};
+cudaError_t launch_logprobs(const LogprobsArgs& a, int num_sms, cudaStream_t s);
+
+// ---------------------------------------------------------------------------------------
+// eviction from a paged cache (kev_evict.cu)
+// ---------------------------------------------------------------------------------------
+constexpr int kEvictChunk = 64;       // rows of a move (half a page)
+constexpr int kEvictCheckCtas = 304;  // of the check kernel, at most
+// words of the workspace: the next chunk's ticket, a wait gave up, one that nothing sets (test hook), verdicts, flags
+enum : int32_t { kEvictTicket = 0, kEvictAbort = 1, kEvictNever = 2, kEvictVerdicts = 16 };
+struct EvictArgs {
+  const float* mass;            // selection: [n_blocks, h_kv, kPage]
+  const int32_t* lens;          // [n] cached positions
+  const uint8_t* active;        // selection; null: all
+  int32_t n, h_kv;
+  const int32_t* table;         // [n, max_blocks]
+  int32_t max_blocks, n_blocks;
+  int32_t keep, first, last;
+  int32_t* kept;                // selection: [n, h_kv, keep], [n]
+  int32_t* kept_lens;
+  const int32_t* kept_in;       // compaction: the same
+  const int32_t* kept_lens_in;
+  void* k;
+  void* v;
+  float* scale_k;               // null: not e4m3
+  float* scale_v;
+  float* mass_io;               // null: not moved
+  int32_t cells;                // compaction: bytes of a cached row (0: a selection)
+  int32_t chunks;               // of kEvictChunk rows a list has at most
+  int64_t flags, n_flags;       // word of the first flag [n * h_kv, chunks]: the chunk's rows have been read
+  int32_t check_ctas;
+  int32_t smem_keys;
+  long long wait_budget;
+  int32_t test_stall;
+  char* ws;
+  int32_t* dev_status;
+};
+cudaError_t launch_select(const EvictArgs& a, int num_sms, cudaStream_t s);
+cudaError_t launch_compact(const EvictArgs& a, int num_sms, cudaStream_t s);
+
+// ---------------------------------------------------------------------------------------
 // token-grouped LoRA (kev_lora.cu)
 // ---------------------------------------------------------------------------------------
 struct LoraArgs {
@@ -360,6 +417,9 @@ cudaError_t launch_decode_tc(const DecodeArgs& a, int num_sms, cudaStream_t s); 
 int32_t chunk_launches();
 int32_t paged_write_launches();
 int32_t paged_read_launches();
+// kev_evict_api.cu: of the most recent kev_norm_rope_paged, kev_attn_mass_paged
+int32_t norm_rope_launches();
+int32_t mass_launches();
 // lens[i] += 1 for active i; with `code` (a device word), only if *code is ST_OK
 cudaError_t launch_advance(int32_t* lens, const uint8_t* active, int32_t n, cudaStream_t s,
                            const int32_t* code = nullptr);

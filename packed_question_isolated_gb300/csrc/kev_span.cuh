@@ -118,6 +118,8 @@ struct SpanArgs {
   int32_t max_blocks, n_blocks;
   int32_t window, sinks;  // window 0: every earlier position
   int32_t max_chunk;      // no question has more tokens
+  const int32_t* positions;  // rotation: each question's first position (null: its prefix)
+  int32_t max_pos;           // and how many the angle table has (0: no rotation)
   // The work line of this launch: the questions of min_tokens .. max_tokens tokens
   SpanLine line;
   int32_t min_tokens, max_tokens;
@@ -131,6 +133,19 @@ struct SpanArgs {
   SpanLayout layout;
   int32_t* dev_status;
 };
+
+// Norms, rotation and cache write in one pass (kev_norm_rope.cu): a.q, a.k, a.v with rows of any stride
+struct NormRopeArgs {
+  SpanArgs s;
+  int64_t q_stride, k_stride, v_stride;  // elements between tokens
+  void* q_out;
+  void* k_out;  // null: not wanted
+  const void* q_weight;  // null: not normalised
+  const void* k_weight;
+  float eps;
+  const float2* table;
+};
+cudaError_t launch_norm_rope(const NormRopeArgs& p, bool checked, int num_sms, cudaStream_t s);
 
 // tensor maps (kev_span_tc.cu): `rank` dimensions, innermost first and contiguous, of `elem`-byte elements
 bool span_tensor_map(CUtensorMap* m, const void* base, int elem, int rank, const cuuint64_t* dims, const cuuint32_t* box,
@@ -241,6 +256,76 @@ __device__ __forceinline__ void span_quotients(float (&f)[N], float scale) {
 #pragma unroll
     for (int e = 0; e < N; ++e) f[e] = scale == 0.f ? 0.f : __fdiv_rn(f[e], scale);
   }
+}
+
+// Errors of device data by rank -- intervals, prefix, overflow, slot, position: the first that applies is
+// reported -- as 8 - rank in a word that starts at 0, and the status of that word.
+__device__ __forceinline__ int span_code(int err) {
+  const int rank = 8 - err;
+  return err == 0 ? ST_OK : rank == 0 ? ST_INTERVALS : rank == 1 ? ST_PREFIX : rank == 2 ? ST_OVERFLOW : rank == 3 ? ST_SLOT : ST_POSITION;
+}
+// Are the positions of question i's L new tokens, cached from `prefix` on, rows of the angle table?
+__device__ __forceinline__ bool span_positions(const SpanArgs& a, int i, int prefix, int L) {
+  if (a.max_pos == 0) return true;
+  const int first = a.positions ? a.positions[i] : prefix;
+  return first >= 0 && (int64_t)first + L <= a.max_pos;
+}
+
+// Small calls: every CTA makes the plan's checks (kev_span_plan.cu) for itself and comes to the same verdict,
+// so none has to wait for another.  Overlapping intervals show as a token that is marked twice; the mark is
+// also the token's question.
+constexpr int kSpanSmall = 512;  // tokens and questions of a small call at most, and threads of its kernels
+struct SpanSmall {
+  int2 iv[kSpanSmall];
+  int prefix[kSpanSmall], owner[kSpanSmall], err;
+};
+// Before the launch's inputs are ready: shared memory cleared (`used`: a bit per block of the pool).
+__device__ __forceinline__ void span_small_clear(const SpanArgs& a, SpanSmall& sm, unsigned* used) {
+  const int words = a.pool_elem ? (a.n_blocks + 31) / 32 : 0, t = threadIdx.x;
+  if (t == 0) sm.err = 0;
+  for (int i = t; i < words; i += kSpanSmall) used[i] = 0u;
+  for (int i = t; i < a.T; i += kSpanSmall) sm.owner[i] = -1;
+}
+// The checks, by kSpanSmall threads that have passed a barrier since the clearing; true: the call is valid.
+__device__ __forceinline__ bool span_small_check(const SpanArgs& a, SpanSmall& sm, unsigned* used) {
+  const int t = threadIdx.x, warp = t / 32, lane = t & 31;
+  auto error = [&](int rank) { atomicMax(&sm.err, 8 - rank); };
+  for (int i = t; i < a.n; i += kSpanSmall) {
+    const kev_interval v = a.intervals[i];
+    const int first = a.prefix ? a.prefix[i] : 0;
+    sm.iv[i] = make_int2(v.begin, v.end);
+    sm.prefix[i] = first;
+    if (v.begin < 0 || v.end < v.begin || v.end > a.T) {
+      error(0);
+    } else if (v.end > v.begin) {
+      if (first < 0) error(1);
+      else if (a.pool_elem && (int64_t)first + (v.end - v.begin) > (int64_t)a.max_blocks * kPage) error(2);
+      if (!span_positions(a, i, first, v.end - v.begin)) error(4);
+    }
+  }
+  __syncthreads();
+  // clean: the checks of single questions passed (positions are no one's address yet); inside: every interval at least
+  const bool clean = sm.err <= 4, inside = sm.err != 8;
+  __syncthreads();
+  if (clean && a.pool_elem) {
+    for (int i = t; i < a.n; i += kSpanSmall) {  // pages; a block's bit may be set once
+      const int L = sm.iv[i].y - sm.iv[i].x;
+      if (L <= 0) continue;
+      for (int e = sm.prefix[i] / kPage; e <= (sm.prefix[i] + L - 1) / kPage; ++e) {
+        const int b = a.table[(int64_t)i * a.max_blocks + e];
+        const unsigned bit = 1u << (b & 31);
+        if (b < 0 || b >= a.n_blocks || atomicOr(&used[b >> 5], bit) & bit) error(3);
+      }
+    }
+  }
+  if (inside) {
+    for (int i = warp; i < a.n; i += kSpanSmall / 32)
+      for (int x = sm.iv[i].x + lane; x < sm.iv[i].y; x += 32)
+        if (atomicExch(&sm.owner[x], i) >= 0) error(0);
+  }
+  __syncthreads();
+  if (blockIdx.x == 0 && t == 0 && a.dev_status) *a.dev_status = span_code(sm.err);
+  return sm.err == 0;
 }
 
 // Is position u visible to the token at position p?

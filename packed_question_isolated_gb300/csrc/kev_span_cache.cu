@@ -23,7 +23,6 @@ namespace kev {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kSmallThreads = 512, kSmall = 512;  // of the one kernel for small calls: threads, tokens and questions
 
 // The prefix sums of the questions' lengths into shared memory, by the whole CTA.
 __device__ __forceinline__ const int32_t* share_cu(const SpanArgs& a) {
@@ -259,67 +258,23 @@ __global__ void __launch_bounds__(kThreads) span_copy_kernel(SpanArgs a, void* k
   }
 }
 
-// The checks of the plan (kev_span_plan.cu) and the copy in one kernel, for small calls: every CTA makes all
-// the checks for itself, in shared memory, and comes to the same verdict, so none has to wait for another.
-// Overlapping intervals show as a token that is marked twice; the mark is also the token's question.  A warp
+// The checks of the plan (kev_span_plan.cu) and the copy in one kernel, for small calls.  A warp
 // copies one token's K or V.  Measured on the GPU (the call takes the host 7.2 us) for one token of each of 32
 // questions 3.6 us, with two kernels 7.0; at the ends of what it takes, a chunk of 512 tokens 4.9 against 7.3 and
 // 512 questions of one token 9.0 against 15.6.
 template <int E, int D, bool Q8, bool kRead>
-__global__ void __launch_bounds__(kSmallThreads) span_small_copy_kernel(SpanArgs a, void* k_out, void* v_out) {
-  extern __shared__ unsigned small_smem[];
-  unsigned* used = small_smem;  // a bit per block
-  const int words = (a.n_blocks + 31) / 32, t = threadIdx.x, warp = t / 32, lane = t & 31;
-  __shared__ int2 s_iv[kSmall];
-  __shared__ int s_prefix[kSmall], s_owner[kSmall], s_err;
-  if (t == 0) s_err = 0;
-  for (int i = t; i < words; i += kSmallThreads) used[i] = 0u;
-  for (int i = t; i < a.T; i += kSmallThreads) s_owner[i] = -1;
+__global__ void __launch_bounds__(kSpanSmall) span_small_copy_kernel(SpanArgs a, void* k_out, void* v_out) {
+  extern __shared__ unsigned used[];  // a bit per block
+  __shared__ SpanSmall sm;
+  span_small_clear(a, sm, used);
   pdl_wait();
   pdl_trigger();
   __syncthreads();
-  auto error = [&](int rank) { atomicMax(&s_err, 8 - rank); };  // ranks as in the plan
-  for (int i = t; i < a.n; i += kSmallThreads) {
-    const kev_interval v = a.intervals[i];
-    const int first = a.prefix[i];
-    s_iv[i] = make_int2(v.begin, v.end);
-    s_prefix[i] = first;
-    if (v.begin < 0 || v.end < v.begin || v.end > a.T) {
-      error(0);
-    } else if (v.end > v.begin) {
-      if (first < 0) error(1);
-      else if ((int64_t)first + (v.end - v.begin) > (int64_t)a.max_blocks * kPage) error(2);
-    }
-  }
-  __syncthreads();
-  const bool clean = s_err == 0, inside = s_err != 8;  // inside: every interval at least
-  __syncthreads();
-  if (clean) {
-    for (int i = t; i < a.n; i += kSmallThreads) {  // pages; a block's bit may be set once
-      const int L = s_iv[i].y - s_iv[i].x;
-      if (L <= 0) continue;
-      for (int e = s_prefix[i] / kPage; e <= (s_prefix[i] + L - 1) / kPage; ++e) {
-        const int b = a.table[(int64_t)i * a.max_blocks + e];
-        const unsigned bit = 1u << (b & 31);
-        if (b < 0 || b >= a.n_blocks || atomicOr(&used[b >> 5], bit) & bit) error(3);
-      }
-    }
-  }
-  if (inside) {
-    for (int i = warp; i < a.n; i += kSmallThreads / 32)
-      for (int x = s_iv[i].x + lane; x < s_iv[i].y; x += 32)
-        if (atomicExch(&s_owner[x], i) >= 0) error(0);
-  }
-  __syncthreads();
-  if (blockIdx.x == 0 && t == 0 && a.dev_status) {
-    const int rank = 8 - s_err;
-    *a.dev_status = s_err == 0 ? ST_OK : rank == 0 ? ST_INTERVALS : rank == 1 ? ST_PREFIX : rank == 2 ? ST_OVERFLOW : ST_SLOT;
-  }
-  if (s_err) return;
-  const int y = blockIdx.x * (kSmallThreads / 32) + warp, x = y >> 1;
-  const int i = x < a.T ? s_owner[x] : -1;
+  if (!span_small_check(a, sm, used)) return;
+  const int y = blockIdx.x * (kSpanSmall / 32) + threadIdx.x / 32, x = y >> 1;
+  const int i = x < a.T ? sm.owner[x] : -1;
   if (i < 0) return;
-  const int p = s_prefix[i] + x - s_iv[i].x;
+  const int p = sm.prefix[i] + x - sm.iv[i].x;
   const Place at = {x, a.table[(int64_t)i * a.max_blocks + p / kPage], p % kPage};
   if (kRead) read_token<E, D, Q8, true>(a, k_out, v_out, at, true, y & 1);
   else write_token<E, D, Q8, true>(a, at, true, y & 1);
@@ -334,8 +289,8 @@ template <int E, int D, bool Q8, bool kRead>
 cudaError_t launch(const SpanArgs& a, void* k_out, void* v_out, bool checked, int num_sms, cudaStream_t s) {
   if (checked) return launch_pdl(span_copy_kernel<E, D, Q8, kRead>, dim3(grid_of(a, num_sms)), dim3(kThreads),
                                  sizeof(int32_t) * (size_t)a.n, s, a, k_out, v_out);
-  const int per = kSmallThreads / 64;  // tokens of a CTA; without any the checks are left
-  return launch_pdl(span_small_copy_kernel<E, D, Q8, kRead>, dim3(a.T > 0 ? (a.T + per - 1) / per : 1), dim3(kSmallThreads),
+  const int per = kSpanSmall / 64;  // tokens of a CTA; without any the checks are left
+  return launch_pdl(span_small_copy_kernel<E, D, Q8, kRead>, dim3(a.T > 0 ? (a.T + per - 1) / per : 1), dim3(kSpanSmall),
                     sizeof(int32_t) * (((size_t)a.n_blocks + 31) / 32), s, a, k_out, v_out);
 }
 template <bool kRead>
@@ -352,7 +307,7 @@ cudaError_t launch_copy(const SpanArgs& a, void* k_out, void* v_out, bool checke
 
 // What the small kernel's shared memory holds without asking for more: 512 tokens and questions (every CTA
 // checks them all) and 2^18 blocks.
-bool span_small_copy(const SpanArgs& a) { return a.T <= kSmall && a.n <= kSmall && a.n_blocks <= 1 << 18; }
+bool span_small_copy(const SpanArgs& a) { return a.T <= kSpanSmall && a.n <= kSpanSmall && a.n_blocks <= 1 << 18; }
 
 cudaError_t launch_span_write(const SpanArgs& a, bool checked, int num_sms, cudaStream_t s) {
   return a.T <= 0 && checked ? cudaSuccess : launch_copy<false>(a, nullptr, nullptr, checked, num_sms, s);

@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(const __grid_con
   SpanHeader* hdr = reinterpret_cast<SpanHeader*>(a.ws);
   int32_t* cu = reinterpret_cast<int32_t*>(a.ws + a.layout.cu);
   int2* gaps = reinterpret_cast<int2*>(a.ws + a.layout.gaps);
-  // error ranks: intervals, prefix, overflow, slot -- the first that applies is reported
+  // ranks as for span_code
   auto error = [&](int rank) { atomicMax(&s_err, 8 - rank); };
   auto items_of = [&](int l, int L) {
     return l < p.lines && L >= p.line[l].min_tokens && L <= p.line[l].max_tokens ? (L + p.line[l].item_tokens - 1) / p.line[l].item_tokens : 0;
@@ -128,6 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(const __grid_con
       const int L = v.end - v.begin;
       if (first < 0) error(1);
       else if (a.pool_elem && (int64_t)first + L > (int64_t)a.max_blocks * kPage) error(2);
+      if (!span_positions(a, i, first, L)) error(4);
       mine.end = max(mine.end, v.end);
       mine.tokens += L;
       mine.items[0] += items_of(0, L);
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(const __grid_con
   Scan all;
   const Scan before = block_scan<kThreads>(mine, Scan{}, s_scan, &all);
 
-  const bool clean = s_err == 0;   // the checks of single questions passed
+  const bool clean = s_err <= 4;   // the checks of single questions passed (but for positions: the pages come first)
   const bool inside = s_err != 8;  // at least those of their intervals
   __syncthreads();
 
@@ -260,8 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(const __grid_con
   }
   if (s_err) {
     if (t == 0) {
-      const int rank = 8 - s_err;
-      const int code = rank == 0 ? ST_INTERVALS : rank == 1 ? ST_PREFIX : rank == 2 ? ST_OVERFLOW : ST_SLOT;
+      const int code = span_code(s_err);
       hdr->status = code;
       if (a.dev_status) *a.dev_status = code;
     }
