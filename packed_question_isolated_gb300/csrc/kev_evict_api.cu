@@ -11,26 +11,35 @@ namespace {
 // kernel launches of the most recent successful call of each
 std::atomic<int32_t> g_norm_rope_launches{2}, g_mass_launches{4};
 
-// Attention mass: the span workspace, the rows' log sums and a ticket behind it.
-size_t mass_layout(const SpanLayout& l, int32_t T, int32_t h_q, size_t* lse, size_t* ticket) {
-  *lse = l.total;
-  *ticket = align_up(*lse + sizeof(float) * (size_t)T * h_q, 256);
-  return *ticket + 256;
+// Attention mass: the span workspace, and behind it the rows' log sums, a ticket and the second pass's parts.
+size_t mass_layout(const SpanLayout& l, int32_t T, int32_t h_q, MassArgs* m) {
+  m->lse = l.total;
+  m->ticket = align_up(m->lse + sizeof(float) * (size_t)T * h_q, 256);
+  m->cuts = m->ticket + 256;
+  return m->cuts + align_up(mass_cuts_bytes(), 256);
 }
 
 kev_status mass_attend(const MassArgs& call, int32_t* launches, cudaStream_t s) {
   const int sms = sms_of_current_device();
   if (sms <= 0) return KEV_ERR_CUDA;
-  if (call.s.T <= 0) {  // no tokens: the checks alone
+  if (call.s.T <= 0 || call.s.n <= 0) {  // no tokens, or none in a question: the checks alone
     *launches = 1;
     return from_cuda(launch_span_plan(call.s, 0, nullptr, nullptr, s));
   }
   MassArgs m = call;
-  m.s = span_line(call.s, 0, 64, 1, 2 * sms);
+  const bool bf16 = call.s.elem == 2;
+  m.s = bf16 ? span_line(call.s, 0, 128, 2, sms) : span_line(call.s, 0, 64, 1, 2 * sms);
+  m.s.unit_cost = bf16 ? 1 : 0;
   m.s.join_from = 2;
+  if (bf16 && (int64_t)call.s.max_chunk * call.s.group <= 16) {  // few rows per question, and the caller said so
+    *launches = 2;
+    cudaError_t e = launch_span_plan(call.s, 1, &m.s, nullptr, s);
+    if (e == cudaSuccess) e = launch_mass_rows(m, sms, s);
+    return from_cuda(e);
+  }
   *launches = 4;
   cudaError_t e = launch_span_plan(call.s, 1, &m.s, nullptr, s);
-  if (e == cudaSuccess) e = launch_mass_simt(m, sms, s);
+  if (e == cudaSuccess) e = bf16 ? launch_mass_tc(m, sms, s) : launch_mass_simt(m, sms, s);
   return from_cuda(e);
 }
 
@@ -145,9 +154,8 @@ kev_status kev_norm_rope_paged(const void* q, const void* k, const void* v, int3
 
 size_t kev_attn_mass_workspace_size(int32_t n_questions, int32_t total_tokens, const kev_attn_shape* shape) {
   if (check_span_shape(shape) != KEV_OK || n_questions < 0 || n_questions > kMaxQuestions || total_tokens < 0) return 0;
-  size_t lse, ticket;
-  return mass_layout(span_layout(n_questions, total_tokens, shape->h_q / shape->h_kv, shape->d_h), total_tokens, shape->h_q, &lse,
-                     &ticket);
+  MassArgs m;
+  return mass_layout(span_layout(n_questions, total_tokens, shape->h_q / shape->h_kv, shape->d_h), total_tokens, shape->h_q, &m);
 }
 
 kev_status kev_attn_mass_paged(const void* q, int32_t total_tokens, const kev_interval* intervals, int32_t n_questions,
@@ -159,7 +167,7 @@ kev_status kev_attn_mass_paged(const void* q, int32_t total_tokens, const kev_in
   kev_status st = span_common(&a, total_tokens, intervals, n_questions, shape, workspace, workspace_bytes, dev_status);
   if (st == KEV_OK) st = span_cache(&a, shape, prefix_lens, cache);
   if (st != KEV_OK) return st;
-  if (workspace_bytes < mass_layout(a.layout, total_tokens, a.h_q, &m.lse, &m.ticket)) return KEV_ERR_INVALID_ARG;
+  if (workspace_bytes < mass_layout(a.layout, total_tokens, a.h_q, &m)) return KEV_ERR_INVALID_ARG;
   if (max_chunk < 0 || !(decay >= 0.f) || isinf(decay) || !mass || !aligned(mass, 16)) return KEV_ERR_INVALID_ARG;
   if (total_tokens > 0 && (!q || !aligned(q, 16))) return KEV_ERR_INVALID_ARG;
   a.q = q;

@@ -18,10 +18,14 @@ struct MassArgs {
   float* mass;
   float decay;
   size_t lse;     // workspace: float[T][h_q] log2 sums
-  size_t ticket;  // workspace: next unit of the second pass
+  size_t ticket;  // workspace: next unit of the second pass (CUDA cores)
+  size_t cuts;    // workspace: parts of the second pass (tensor cores)
 };
 
 cudaError_t launch_mass_simt(const MassArgs& m, int num_sms, cudaStream_t s);
+cudaError_t launch_mass_rows(const MassArgs& m, int num_sms, cudaStream_t s);  // bf16 q, at most 16 rows a question
+cudaError_t launch_mass_tc(const MassArgs& m, int num_sms, cudaStream_t s);    // bf16 q
+size_t mass_cuts_bytes();
 
 // Key tiles (units of the second pass, per kv head) before each question that brings tokens, and all of them: the
 // calling CTA's threads, into shared memory [n + 1].  Ends with a barrier.
