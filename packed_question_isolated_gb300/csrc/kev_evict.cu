@@ -108,9 +108,9 @@ __device__ __forceinline__ uint32_t order_of(float x) {
 
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant__ EvictArgs a) {
-  constexpr int kWarps = kThreads / 32, kBins = 2048;
+  constexpr int kWarps = kThreads / 32, kBins = 2048, kCopies = 4;
   extern __shared__ uint32_t s_keys[];  // [a.smem_keys] ordered masses, as far as they fit
-  __shared__ int s_bins[kBins];
+  __shared__ int s_bins[kCopies][kBins];  // lanes that differ mod kCopies count apart: masses share few exponents
   __shared__ int s_warp[kWarps][2];
   __shared__ int s_word[3];
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -143,17 +143,23 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
 #pragma unroll 1
     for (int shift = 21; shift >= 0; shift = shift == 21 ? 10 : shift == 10 ? 0 : -1) {
       const int bins = shift == 0 ? 1024 : 2048;
-      for (int b = t; b < bins; b += kThreads) s_bins[b] = 0;
+      for (int b = t; b < kCopies * kBins; b += kThreads) s_bins[0][b] = 0;
       __syncthreads();
       for (int u = lo + t; u < hi; u += kThreads) {
         const uint32_t k = key(u);
-        if ((k & mask) == v) atomicAdd(&s_bins[k >> shift & (bins - 1)], 1);
+        if ((k & mask) == v) atomicAdd(&s_bins[lane % kCopies][k >> shift & (bins - 1)], 1);
       }
       __syncthreads();
       // counts from the top: a thread has `per` neighbouring bins
       const int per = bins / kThreads;
       int mine = 0;
-      for (int b = 0; b < per; ++b) mine += s_bins[bins - 1 - (t * per + b)];
+      for (int b = 0; b < per; ++b) {
+        const int at = bins - 1 - (t * per + b);
+        int n_at = 0;
+#pragma unroll
+        for (int x = 0; x < kCopies; ++x) n_at += s_bins[x][at];
+        mine += s_bins[0][at] = n_at;
+      }
       int incl = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -166,7 +172,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
       for (int w = 0; w < warp; ++w) before += s_warp[w][0];
       if (before < left && before + mine >= left) {  // one thread
         int at = before, b = 0;
-        while (at + s_bins[bins - 1 - (t * per + b)] < left) at += s_bins[bins - 1 - (t * per + b++)];
+        while (at + s_bins[0][bins - 1 - (t * per + b)] < left) at += s_bins[0][bins - 1 - (t * per + b++)];
         s_word[1] = bins - 1 - (t * per + b);
         s_word[2] = at;
       }
@@ -349,12 +355,12 @@ cudaError_t launch_select(const EvictArgs& call, int num_sms, cudaStream_t s) {
   cudaError_t e = launch_check(a, num_sms, s);
   if (e != cudaSuccess) return e;
   const int64_t cap = (int64_t)a.max_blocks * kPage;
-  constexpr int kMost = 50 * 1024;  // keys: 200 KB
+  constexpr int kMost = 48 * 1024;  // keys: 192 KB
   a.smem_keys = (int32_t)(cap < kMost ? cap : kMost);
   const bool wide = cap > 4096;
   auto kern = wide ? select_kernel<1024> : select_kernel<256>;
   const size_t smem = 4 * (size_t)a.smem_keys;
-  if (smem > 32 * 1024) {
+  if (smem > 12 * 1024) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kMost);
     if (e != cudaSuccess) return e;
   }

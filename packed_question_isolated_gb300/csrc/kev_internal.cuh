@@ -316,6 +316,8 @@ struct LogprobsArgs {
   int32_t* top_tokens;
   float* top_logprobs;
   int32_t* dev_status;
+  long long wait_budget;
+  int32_t test_stall;  // timeout test hook
 };
 cudaError_t launch_logprobs(const LogprobsArgs& a, int num_sms, cudaStream_t s);
 

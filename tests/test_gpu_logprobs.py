@@ -6,6 +6,11 @@ after the other, each addition off by 2^-24, and the joins add some 2^-24 each: 
 relative (N + 256) 2^-24, and so is log S absolutely.  |log p| is off by that and 2^-21 |log p|.  The entropy is
 log S - W / S, both parts not negative, W with the same relative error: (N + 256) 2^-23 (1 + H).
 """
+import os
+import subprocess
+import sys
+import textwrap
+
 import numpy as np
 import pytest
 import torch
@@ -177,3 +182,25 @@ def test_captured_on_another_stream():
     want = torch.log_softmax(x.double(), -1)
     assert torch.allclose(lp.double(), want[torch.arange(n), tok.long()], atol=1e-4)
     assert (tl.double() - torch.topk(want, 5, -1)[0]).abs().max() < 1e-4
+
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CHILD = textwrap.dedent(r"""
+    import os, sys
+    sys.path[:0] = [ROOT, os.path.join(ROOT, "tests")]
+    import numpy as np
+    from test_gpu_logprobs import check, kev, run
+    for n, v in ((3, 151936), (700, 33000)):
+        x = np.random.default_rng(n).standard_normal((n, v))
+        os.environ.update(KEV_TEST_STALL="1", KEV_TEST_WAIT_LIMIT="2000000")  # ~1 ms
+        assert run(x, "bf16", [1] * n, None, 5)[1] == kev.binding.KEV_ERR_TIMEOUT
+        del os.environ["KEV_TEST_STALL"], os.environ["KEV_TEST_WAIT_LIMIT"]
+        check(x, "bf16", [1] * n, None, 5)
+    print("ALL OK")
+""").replace("ROOT", repr(ROOT))
+
+
+def test_a_wait_that_runs_out_is_reported():
+    env = {k: v for k, v in os.environ.items() if k not in ("KEV_TEST_STALL", "KEV_TEST_WAIT_LIMIT")}
+    r = subprocess.run([sys.executable, "-c", CHILD], capture_output=True, text=True, timeout=600, env=env)
+    assert r.returncode == 0 and "ALL OK" in r.stdout, f"child failed:\n{r.stdout}\n{r.stderr[-4000:]}"
