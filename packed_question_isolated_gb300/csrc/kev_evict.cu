@@ -23,7 +23,7 @@
 namespace kev {
 namespace {
 
-constexpr int kCheckThreads = 512;
+constexpr int kCheckThreads = 512, kCheckRun = 4 * kCheckThreads;  // entries of a kept list that a CTA looks at at a time
 constexpr int kCompactThreads = 256;
 
 __device__ __forceinline__ int32_t* words_of(const EvictArgs& a) { return reinterpret_cast<int32_t*>(a.ws); }
@@ -80,17 +80,25 @@ __global__ void __launch_bounds__(kCheckThreads) evict_check_kernel(const __grid
   }
   if (compact) {
     // kept lists: strictly ascending inside [0, lens[i])
-    const int64_t total = (int64_t)a.n * a.h_kv * a.keep, step = (int64_t)gridDim.x * kCheckThreads;
-    for (int64_t x = (int64_t)blockIdx.x * kCheckThreads + t; x < total; x += step) {
-      const int j = (int)(x % a.keep), i = (int)(x / a.keep / a.h_kv);
+    const int segments = (a.keep + kCheckRun - 1) / kCheckRun, units = a.n * a.h_kv * segments;
+    for (int x = blockIdx.x; x < units; x += gridDim.x) {
+      const int list = x / segments, j0 = x % segments * kCheckRun, i = list / a.h_kv;
       const int n = a.lens[i], m = a.kept_lens_in[i];
       if (n == m) continue;
-      if (m < 0 || m > a.keep || m > n) error(3);
-      else if (j < m) {
-        const int u = a.kept_in[x];
-        if (u < 0 || u >= n || (j > 0 && a.kept_in[x - 1] >= u)) error(3);
+      if (m < 0 || m > a.keep || m > n) {
+        error(3);
+        continue;
+      }
+      const int32_t* kept = a.kept_in + (int64_t)list * a.keep;
+#pragma unroll
+      for (int e = 0; e < kCheckRun / kCheckThreads; ++e) {
+        const int j = j0 + e * kCheckThreads + t;
+        if (j >= m) break;
+        const int u = kept[j];
+        if (u < 0 || u >= n || (j > 0 && kept[j - 1] >= u)) error(3);
       }
     }
+    const int64_t step = (int64_t)gridDim.x * kCheckThreads;
     int32_t* flags = words_of(a) + a.flags;
     for (int64_t x = (int64_t)blockIdx.x * kCheckThreads + t; x < a.n_flags; x += step) flags[x] = 0;
     if (blockIdx.x == 0 && t < kEvictVerdicts) words_of(a)[t] = 0;  // ticket, abort, never
@@ -108,7 +116,7 @@ __device__ __forceinline__ uint32_t order_of(float x) {
 
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant__ EvictArgs a) {
-  constexpr int kWarps = kThreads / 32, kBins = 2048, kCopies = 4;
+  constexpr int kWarps = kThreads / 32, kBins = 2048, kCopies = kThreads == 1024 ? 4 : 1;
   extern __shared__ uint32_t s_keys[];  // [a.smem_keys] ordered masses, as far as they fit
   __shared__ int s_bins[kCopies][kBins];  // lanes that differ mod kCopies count apart: masses share few exponents
   __shared__ int s_warp[kWarps][2];
@@ -132,7 +140,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
   const int32_t* row = a.table + (int64_t)i * a.max_blocks;
   const int lo = a.first, hi = n - a.last;       // the positions to choose from (lo <= hi: first + last <= keep < n)
   const int want = a.keep - a.first - a.last;    // and how many of them
-  auto load = [&](int u) { return order_of(a.mass[((int64_t)row[u / kPage] * a.h_kv + g) * kPage + u % kPage]); };
+  auto load = [&](int u) { return order_of(__ldg(a.mass + ((int64_t)__ldg(row + u / kPage) * a.h_kv + g) * kPage + u % kPage)); };
   for (int u = lo + t; u < hi && u < a.smem_keys; u += kThreads) s_keys[u] = load(u);
   auto key = [&](int u) { return u < a.smem_keys ? s_keys[u] : load(u); };
 
@@ -336,9 +344,8 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const __grid_c
 
 // The check kernel: as many CTAs as the kept lists fill.
 cudaError_t launch_check(EvictArgs& a, int num_sms, cudaStream_t s) {
-  const int64_t todo = a.cells ? (int64_t)a.n * a.h_kv * a.keep : 0;
-  int64_t ctas = (todo + 4 * kCheckThreads - 1) / (4 * kCheckThreads);
-  ctas = ctas < 1 ? 1 : ctas < num_sms ? ctas : num_sms;
+  int64_t ctas = a.cells ? (int64_t)a.n * a.h_kv * ((a.keep + kCheckRun - 1) / kCheckRun) : 1;
+  ctas = ctas < 1 ? 1 : ctas < 2 * num_sms ? ctas : 2 * num_sms;
   a.check_ctas = (int32_t)(ctas < kEvictCheckCtas ? ctas : kEvictCheckCtas);
   const size_t smem = a.cells ? ((size_t)a.n_blocks + 31) / 32 * 4 : 0;
   if (smem > 40 * 1024) {

@@ -22,6 +22,8 @@
 #include <cuda.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "kev_mass.cuh"
 #include "kev_sm100.cuh"
 
@@ -773,23 +775,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool whole = rows == a.tile_tokens * a.group && u0 + kM - 1 <= w.k.prefix + token0;
           unsigned long long s2[2] = {0, 0};
           const ulonglong2* ml2 = reinterpret_cast<const ulonglong2*>(ml);
+          auto weights = [&](auto masked) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < 4; ++c)
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const ulonglong2 nl = ml2[8 * c + e / 4];
-              float2 z0 = unpack2(fma2((unsigned long long)v[c][e] | (unsigned long long)v[c][e + 1] << 32, fx2, nl.x));
-              float2 z1 = unpack2(fma2((unsigned long long)v[c][e + 2] | (unsigned long long)v[c][e + 3] << 32, fx2, nl.y));
-              if (!whole) {
-                const int col = 32 * c + e;
-                z0.x = col < from || col >= rows ? -INFINITY : z0.x;
-                z0.y = col + 1 < from || col + 1 >= rows ? -INFINITY : z0.y;
-                z1.x = col + 2 < from || col + 2 >= rows ? -INFINITY : z1.x;
-                z1.y = col + 3 < from || col + 3 >= rows ? -INFINITY : z1.y;
+              for (int e = 0; e < 32; e += 4) {
+                const ulonglong2 nl = ml2[8 * c + e / 4];
+                float2 z0 = unpack2(fma2((unsigned long long)v[c][e] | (unsigned long long)v[c][e + 1] << 32, fx2, nl.x));
+                float2 z1 = unpack2(fma2((unsigned long long)v[c][e + 2] | (unsigned long long)v[c][e + 3] << 32, fx2, nl.y));
+                if (decltype(masked)::value) {
+                  const int col = 32 * c + e;
+                  z0.x = col < from || col >= rows ? -INFINITY : z0.x;
+                  z0.y = col + 1 < from || col + 1 >= rows ? -INFINITY : z0.y;
+                  z1.x = col + 2 < from || col + 2 >= rows ? -INFINITY : z1.x;
+                  z1.y = col + 3 < from || col + 3 >= rows ? -INFINITY : z1.y;
+                }
+                s2[0] = add2(s2[0], f2pack(ex2_approx(z0.x), ex2_approx(z0.y)));
+                s2[1] = add2(s2[1], f2pack(ex2_approx(z1.x), ex2_approx(z1.y)));
               }
-              s2[0] = add2(s2[0], f2pack(ex2_approx(z0.x), ex2_approx(z0.y)));
-              s2[1] = add2(s2[1], f2pack(ex2_approx(z1.x), ex2_approx(z1.y)));
-            }
+          };
+          if (whole) weights(std::false_type{});
+          else weights(std::true_type{});
           const float2 s0 = unpack2(add2(s2[0], s2[1]));
           sum += s0.x + s0.y;
         }
