@@ -392,11 +392,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int e = 0; e < 32; ++e)
                   if (32 * c + e >= seen) v[c][e] = 0xff800000u;
             }
-            float top = -INFINITY;
+            float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int e = 0; e < 32; e += 2)
 #pragma unroll
-              for (int e = 0; e < 32; e += 2) top = fmax3(top, __uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
+              for (int c = 0; c < 4; ++c) tops[c] = fmax3(tops[c], __uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
+            float top = fmax3(fmaxf(tops[0], tops[1]), tops[2], tops[3]);
             const float sl2 = Q8 ? 1.f : p.scale_log2;
             top *= sl2;
             if (top > m) {
@@ -762,27 +763,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           group_sync(grp);
           ok = ok && warp_wait(&bars->s_full[y % 4], (y / 4) & 1, abort_flag, budget);
           tc_fence_after();
-          uint32_t v[4][32];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(tm + y % 4 * kM + 32 * c, v[c]);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld_wait(v[c]);
-          tc_fence_before();
-          mbar_arrive_warp(&bars->s_free[y % 4]);
           const int token0 = w.k.token(w.j) + q * a.tile_tokens;
           const int rows = min(a.tile_tokens, w.k.L - token0) * a.group;       // columns that are rows of the question
           const int from = max(0, u - w.k.prefix - token0) * a.group;          // the first that sees this thread's key
           const bool whole = rows == a.tile_tokens * a.group && u0 + kM - 1 <= w.k.prefix + token0;
-          unsigned long long s2[2] = {0, 0};
           const ulonglong2* ml2 = reinterpret_cast<const ulonglong2*>(ml);
-          auto weights = [&](auto masked) {
+          unsigned long long s2[4] = {0, 0, 0, 0};
+          uint32_t v[2][32];
+          tmem_ld32(tm + y % 4 * kM, v[0]);
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 4; ++c) {  // 32 columns at a time, the next ones on their way
+            uint32_t(&s)[32] = v[c & 1];
+            tmem_ld_wait(s);
+            if (c < 3) {
+              tmem_ld32(tm + y % 4 * kM + 32 * (c + 1), v[(c + 1) & 1]);
+            } else {
+              tc_fence_before();
+              mbar_arrive_warp(&bars->s_free[y % 4]);
+            }
+            auto weights = [&](auto masked) {
 #pragma unroll
               for (int e = 0; e < 32; e += 4) {
                 const ulonglong2 nl = ml2[8 * c + e / 4];
-                float2 z0 = unpack2(fma2((unsigned long long)v[c][e] | (unsigned long long)v[c][e + 1] << 32, fx2, nl.x));
-                float2 z1 = unpack2(fma2((unsigned long long)v[c][e + 2] | (unsigned long long)v[c][e + 3] << 32, fx2, nl.y));
+                float2 z0 = unpack2(fma2((unsigned long long)s[e] | (unsigned long long)s[e + 1] << 32, fx2, nl.x));
+                float2 z1 = unpack2(fma2((unsigned long long)s[e + 2] | (unsigned long long)s[e + 3] << 32, fx2, nl.y));
                 if (decltype(masked)::value) {
                   const int col = 32 * c + e;
                   z0.x = col < from || col >= rows ? -INFINITY : z0.x;
@@ -790,13 +794,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                   z1.x = col + 2 < from || col + 2 >= rows ? -INFINITY : z1.x;
                   z1.y = col + 3 < from || col + 3 >= rows ? -INFINITY : z1.y;
                 }
-                s2[0] = add2(s2[0], f2pack(ex2_approx(z0.x), ex2_approx(z0.y)));
-                s2[1] = add2(s2[1], f2pack(ex2_approx(z1.x), ex2_approx(z1.y)));
+                s2[(e >> 1) & 3] = add2(s2[(e >> 1) & 3], f2pack(ex2_approx(z0.x), ex2_approx(z0.y)));
+                s2[((e >> 1) + 1) & 3] = add2(s2[((e >> 1) + 1) & 3], f2pack(ex2_approx(z1.x), ex2_approx(z1.y)));
               }
-          };
-          if (whole) weights(std::false_type{});
-          else weights(std::true_type{});
-          const float2 s0 = unpack2(add2(s2[0], s2[1]));
+            };
+            if (whole) weights(std::false_type{});
+            else weights(std::true_type{});
+          }
+          const float2 s0 = unpack2(add2(add2(s2[0], s2[1]), add2(s2[2], s2[3])));
           sum += s0.x + s0.y;
         }
         x += count;
