@@ -491,8 +491,8 @@ kev_status kev_prefill_attn_window(const void* q, const void* k, const void* v, 
  * may be k where these are contiguous too, no other overlap.  cache: y of k and the rows of v go to positions P_i + j, as
  * kev_paged_write puts them but for e4m3 keys, which are quantised from the fp32 row (one rounding instead of two); NULL:
  * no cache is written and v is not read.  Rows of tokens in no interval are neither read nor written.  A position outside
- * [0, max_pos) sets KEV_ERR_POSITION (after the errors above).  A row of q or k whose sum of squares overflows comes back
- * as zeros.  With a weight, eps > 0.  One kernel for up to 512 tokens and questions (and 2^18 blocks), else two. */
+ * [0, max_pos) sets KEV_ERR_POSITION (after the errors above).  A finite row of q or k whose sum of squares overflows
+ * comes back as zeros.  With a weight, eps > 0.  One kernel for up to 512 tokens and questions (and 2^18 blocks), else two. */
 kev_status kev_norm_rope_paged(const void* q, const void* k, const void* v, int32_t q_stride, int32_t k_stride,
                                int32_t v_stride, void* q_out, void* k_out, int32_t total_tokens,
                                const kev_interval* intervals, int32_t n_questions, const int32_t* prefix_lens,

@@ -18,6 +18,12 @@
 //                      begun), reads its rows into registers, says so, waits until every lower chunk of its list has
 //                      been read, and writes.  Nobody waits before it has read, so the waits end; they are bounded all
 //                      the same.  Every row is read once and written once.
+//
+// Measured: 16 caches of 2 to 32 Ki positions cut to 4096 (8 kv heads of 128) selected in 31 us, most of it the largest
+// list's: 32 Ki masses in 1024 threads, three counts of them; moved in 85 (bf16, 6.1 TB/s, 90 % of the measured copy rate
+// with the checks).  32 caches of 200 to 2400 positions cut to 1024 selected in 13 us and moved, e4m3, in 21.  Measured and
+// left in the selection: four copies of the counts with 256 threads (17 us against 13), eight masses on their way (38
+// against 31).
 #include "kev_internal.cuh"
 
 namespace kev {

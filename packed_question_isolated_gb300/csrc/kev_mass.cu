@@ -1,4 +1,6 @@
-// Attention mass on the CUDA cores: true fp32 products and sums.
+// Attention mass of fp32 q on the CUDA cores: true fp32 products and sums, cache fp32 or e4m3.  Bound by the multiply-adds
+// and the shared-memory loads beside them: chunks that take bf16 q on the tensor cores 0.21 ms took kernels of this shape
+// 7.5 (their rows widened from bf16 on the way).
 //
 // mass_rows_kernel   the rows' log sums: 64 (token, q-head) rows, 8 a warp, against 32 keys at a time; a lane owns a key
 //                    and keeps a running maximum and sum of its own for each row, joined at the end.
@@ -15,16 +17,10 @@ namespace {
 constexpr int kThreads = 256, kRows = 64, kSub = 32, kWarpRows = 8;
 constexpr int kKeyRows = 32;  // rows at a time of the second pass
 
-__device__ __forceinline__ float4 bf16x4(uint2 w) {
-  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
-                     __uint_as_float(w.y & 0xffff0000u));
-}
 // 4 elements of a cached key
 template <int D>
 __device__ __forceinline__ float4 load_key(const SpanArgs& a, int64_t cell, int e) {
   if (a.pool_elem == 4) return *reinterpret_cast<const float4*>(static_cast<const float*>(a.pool_k) + cell * D + e);
-  if (a.pool_elem == 2)
-    return bf16x4(*reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.pool_k) + cell * D + e));
   const uint32_t c = *reinterpret_cast<const uint32_t*>(static_cast<const unsigned char*>(a.pool_k) + cell * D + e);
   const float s = a.scale_k[cell];
   float f[4];
@@ -40,8 +36,7 @@ __device__ __forceinline__ float4 load_key(const SpanArgs& a, int64_t cell, int 
 }
 template <int D>
 __device__ __forceinline__ float4 load_query(const SpanArgs& a, int64_t row, int e) {
-  return a.elem == 4 ? *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + row * D + e)
-                     : bf16x4(*reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.q) + row * D + e));
+  return *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + row * D + e);
 }
 
 __device__ __forceinline__ void join_sums(float& m, float& l, float m2, float l2) {

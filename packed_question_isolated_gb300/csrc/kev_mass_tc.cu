@@ -19,6 +19,15 @@
 //                    score instead
 // A masked score is replaced, not multiplied, so what lies in keys that a row does not see never counts.  Every wait is
 // bounded, as in the other tensor-core kernels.
+//
+// What bounds it.  8 chunks of 128 to 1024 tokens behind up to 8192 positions (28/4 heads, bf16) take 210 us, 88 of them
+// the first kernel and 120 the second; 32 tokens of each of 8 e4m3 caches of 4 to 16 Ki positions 111 (49 and 59).  The
+// tensor pipe is busy 36 and 30 % of the time (19 and 16 over e4m3), the exponentials' pipe about as much, L2 and DRAM
+// under 15 %: a group's chain -- S from tensor memory, maximum, exponentials, hand-over -- takes some 2900 clocks for a
+// pair of tiles, and two groups are too few to hide it.  Every tile's chain is the same however few rows it holds, so the
+// 32 tokens of 4 q-heads that just fill one cost the second kernel a key tile's load and conversion each.
+// Measured and left: four groups of four warps at 96 registers, which spill (235 and 157 us); shorter chains for the
+// maximum (no difference).  A second key tile against each loaded q tile is not built.
 #include <cuda.h>
 #include <cuda_fp16.h>
 
@@ -260,8 +269,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!ok) raise_timeout(p, bars);
-        if (*abort_flag)  // every copy issued lands before the CTA leaves
-          for (uint32_t q = n < kSlots ? 0 : n - kSlots; q < n; ++q) mbar_wait(&full[q % kSlots], (q / kSlots) & 1, never, kDrainBudget);
+        // every copy issued lands before the CTA leaves, whoever gave up
+        for (uint32_t q = n < kSlots ? 0 : n - kSlots; q < n; ++q) mbar_wait(&full[q % kSlots], (q / kSlots) & 1, never, kDrainBudget);
       }
     } else if (warp == kQWarp) {
       if (lane == 0) {
@@ -280,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                           w.item.row0 + t * a.tile_tokens, &bars->q_full[0]);
         }
         if (!ok) raise_timeout(p, bars);
-        if (*abort_flag && n) mbar_wait(&bars->q_full[0], (n - 1) & 1, never, kDrainBudget);
+        if (n) mbar_wait(&bars->q_full[0], (n - 1) & 1, never, kDrainBudget);
       }
     } else if (warp == kMmaWarp) {
       uint32_t n = 0, x = 0, units = 0;
@@ -648,8 +657,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           load_keys<D, Q8, L>(a, &tm_k, smem, s, n, block, w.head, &full[s]);
         }
         if (!ok) raise_timeout(p, bars);
-        if (*abort_flag)  // every copy issued lands before the CTA leaves
-          for (uint32_t q = n < kSlots ? 0 : n - kSlots; q < n; ++q) mbar_wait(&full[q % kSlots], (q / kSlots) & 1, never, kDrainBudget);
+        // every copy issued lands before the CTA leaves, whoever gave up
+        for (uint32_t q = n < kSlots ? 0 : n - kSlots; q < n; ++q) mbar_wait(&full[q % kSlots], (q / kSlots) & 1, never, kDrainBudget);
       }
     } else if (warp == kQWarp) {
       if (lane == 0) {
@@ -670,8 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!ok) raise_timeout(p, bars);
-        if (*abort_flag)
-          for (uint32_t q = x < L::kNQ ? 0 : x - L::kNQ; q < x; ++q) mbar_wait(&bars->q_full[q % L::kNQ], (q / L::kNQ) & 1, never, kDrainBudget);
+        for (uint32_t q = x < L::kNQ ? 0 : x - L::kNQ; q < x; ++q) mbar_wait(&bars->q_full[q % L::kNQ], (q / L::kNQ) & 1, never, kDrainBudget);
       }
     } else if (warp == kMmaWarp) {
       uint32_t n = 0, x = 0;

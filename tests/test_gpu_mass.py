@@ -6,6 +6,11 @@ exponential of a score less the row's log sum, each off by that, and by a few la
 log2 units) and of the exponential: a relative (8 (d + 8) + 8) S 2^-24 + 2^-20.  A position adds n of them, whose
 additions are off by at most n 2^-24 (fewer, as they are added in parts), and decay times the old value, 2^-23 of it.
 """
+import os
+import subprocess
+import sys
+import textwrap
+
 import numpy as np
 import pytest
 import torch
@@ -232,3 +237,47 @@ def test_the_same_bits_every_time_and_captured(tokens, max_chunk):
         torch.cuda.synchronize()
         m.ok()
         assert (m.mass == want).all()
+
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CHILD = textwrap.dedent(r"""
+    import os, sys
+    sys.path[:0] = [ROOT, os.path.join(ROOT, "tests")]
+    from test_gpu_mass import Mass, kev
+    for pool in ("bf16", "e4m3"):
+        m = Mass(15, [90, 300, 1], [900, 100, 3000], 8, 2, 128, "bf16", pool)
+        os.environ.update(KEV_TEST_STALL="1", KEV_TEST_WAIT_LIMIT="2000000")  # ~1 ms
+        m.call()
+        assert kev.kev_read_status(m.status) == kev.binding.KEV_ERR_TIMEOUT
+        del os.environ["KEV_TEST_STALL"], os.environ["KEV_TEST_WAIT_LIMIT"]
+        m = Mass(15, [90, 300, 1], [900, 100, 3000], 8, 2, 128, "bf16", pool)
+        m.call()
+        m.ok()
+        m.check()
+    print("ALL OK")
+""").replace("ROOT", repr(ROOT))
+
+
+def test_a_wait_that_runs_out_is_reported():
+    env = {k: v for k, v in os.environ.items() if k not in ("KEV_TEST_STALL", "KEV_TEST_WAIT_LIMIT")}
+    r = subprocess.run([sys.executable, "-c", CHILD], capture_output=True, text=True, timeout=600, env=env)
+    assert r.returncode == 0 and "ALL OK" in r.stdout, f"child failed:\n{r.stdout}\n{r.stderr[-4000:]}"
+
+
+@pytest.mark.parametrize("tokens,max_chunk", [(1, 1), (70, 0)])
+def test_two_calls_at_once_on_two_streams(tokens, max_chunk):
+    """Each with a workspace of its own, over one cache, into a mass of its own."""
+    a = Mass(16, [tokens] * 3, [700, 0, 2000], 8, 2, 128, "bf16", "bf16")
+    b = Mass(16, [tokens] * 3, [700, 0, 2000], 8, 2, 128, "bf16", "bf16")
+    b.cache = a.cache
+    b.tab, b.table = a.tab, a.table
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for m, s in zip((a, b), streams):
+            m.call(0.0, max_chunk, stream=s)
+    torch.cuda.synchronize()
+    a.ok()
+    b.ok()
+    a.check(0.0)
+    assert (a.mass == b.mass).all()
