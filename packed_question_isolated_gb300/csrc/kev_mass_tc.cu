@@ -20,14 +20,15 @@
 // A masked score is replaced, not multiplied, so what lies in keys that a row does not see never counts.  Every wait is
 // bounded, as in the other tensor-core kernels.
 //
-// What bounds it.  8 chunks of 128 to 1024 tokens behind up to 8192 positions (28/4 heads, bf16) take 210 us, 88 of them
-// the first kernel and 120 the second; 32 tokens of each of 8 e4m3 caches of 4 to 16 Ki positions 111 (49 and 59).  The
+// What bounds it.  8 chunks of 128 to 1024 tokens behind up to 8192 positions (28/4 heads, bf16) take 208 us, 88 of them
+// the first kernel and 119 the second; 32 tokens of each of 8 e4m3 caches of 4 to 16 Ki positions 111 (49 and 59).  The
 // tensor pipe is busy 36 and 30 % of the time (19 and 16 over e4m3), the exponentials' pipe about as much, L2 and DRAM
-// under 15 %: a group's chain -- S from tensor memory, maximum, exponentials, hand-over -- takes some 2900 clocks for a
-// pair of tiles, and two groups are too few to hide it.  Every tile's chain is the same however few rows it holds, so the
-// 32 tokens of 4 q-heads that just fill one cost the second kernel a key tile's load and conversion each.
-// Measured and left: four groups of four warps at 96 registers, which spill (235 and 157 us); shorter chains for the
-// maximum (no difference).  A second key tile against each loaded q tile is not built.
+// under 15 %.  Neither the exponentials (without them 200 us), nor the MMAs (with one of a tile's eight 186) nor the copies
+// (of half the bytes: no change) carry it alone: what is left is the hand-over of a tile, MMA - barrier - tensor memory -
+// barrier, some 1500 clocks each, and in the second kernel a key tile's beginning and end.
+// Measured and left: four groups of four warps at 96 registers, which spill (235 and 157 us); three groups at 128 that
+// take 32 columns at a time (207 and 124); polling instead of suspended waits, shorter chains for the maximum (no
+// difference).  A second key tile against each loaded q tile is not built.
 #include <cuda.h>
 #include <cuda_fp16.h>
 
@@ -156,11 +157,12 @@ __device__ __forceinline__ void convert_tile(const unsigned char* from, unsigned
 template <int D, typename L>
 __device__ __forceinline__ void issue_scores(uint32_t tmem, const unsigned char* a, const unsigned char* b) {
   constexpr uint32_t idesc = idesc_bf16(kM, kM, false, false);
-  const uint32_t a_addr = smem_u32(a), b_addr = smem_u32(b);
+  // the descriptors' address field counts 16 bytes: one addition a step instead of building each anew (8 chunks 212 -> 208 us)
+  const uint64_t a_desc = sdesc_sw128(smem_u32(a), 16, 1024), b_desc = sdesc_sw128(smem_u32(b), 16, 1024);
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk) {
-    const uint32_t off = (kk >> 2) * L::kSubBytes + (kk & 3) * 32;
-    umma_bf16(tmem, sdesc_sw128(a_addr + off, 16, 1024), sdesc_sw128(b_addr + off, 16, 1024), idesc, kk > 0);
+    const uint32_t off = ((kk >> 2) * L::kSubBytes + (kk & 3) * 32) / 16;
+    umma_bf16(tmem, a_desc + off, b_desc + off, idesc, kk > 0);
   }
 }
 
