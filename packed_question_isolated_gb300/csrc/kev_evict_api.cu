@@ -33,7 +33,7 @@ kev_status mass_attend(const MassArgs& call, int32_t* launches, cudaStream_t s) 
   m.s.join_from = 2;
   if (bf16 && (int64_t)call.s.max_chunk * call.s.group <= 16) {  // few rows per question, and the caller said so
     *launches = 2;
-    cudaError_t e = launch_span_plan(call.s, 1, &m.s, nullptr, s);
+    cudaError_t e = launch_span_plan(call.s, 0, nullptr, nullptr, s, true);
     if (e == cudaSuccess) e = launch_mass_rows(m, sms, s);
     return from_cuda(e);
   }

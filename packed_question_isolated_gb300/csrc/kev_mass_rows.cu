@@ -14,10 +14,11 @@
 // e4m3: the codes become fp16, exactly, one conversion per two; q becomes fp16 with a power of two of its own per row that
 // brings its largest element to 2^14, so that what fp16 cannot hold is 2^-39 of it; the power and the key's scale multiply
 // the score, the power in two halves, which keeps the product in range where one factor is tiny and the other large.
-// Bound by memory over long caches: 16 bf16 caches of 2 to 32 Ki positions (32/8 heads) 95 us with the checks (4.8 TB/s, 70 %
-// of the measured copy rate; DRAM bytes 1.00 of what has to be read).  32 e4m3 caches of 64 to 2400 positions take 22, of
-// which the checks are 6 to 8 and the rest is the chain of a cluster: pages, maxima, two cluster barriers.  Why clusters:
+// Bound by memory over long caches: 16 bf16 caches of 2 to 32 Ki positions (32/8 heads) 91 us with the checks (5.0 TB/s, 73 %
+// of the measured copy rate; DRAM bytes 1.00 of what has to be read).  32 e4m3 caches of 64 to 2400 positions take 19, of
+// which the checks are 4 to 5 and the rest is the chain of a cluster: pages, maxima, two cluster barriers.  Why clusters:
 // scores written out for a second kernel cost a workspace as large as the caches, a second reading of K costs K again.
+// Measured and left: the longest caches first (97 us against 95).
 #include <cuda_fp16.h>
 
 #include "kev_mass.cuh"

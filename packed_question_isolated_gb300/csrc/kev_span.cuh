@@ -151,8 +151,10 @@ cudaError_t launch_norm_rope(const NormRopeArgs& p, bool checked, int num_sms, c
 bool span_tensor_map(CUtensorMap* m, const void* base, int elem, int rank, const cuuint64_t* dims, const cuuint32_t* box,
                      CUtensorMapSwizzle swizzle);
 // The checks of a call, and the work lines of its attention launches: none for a cache write or read,
-// or one or two (same call, other line) whose questions between them are all that have tokens
-cudaError_t launch_span_plan(const SpanArgs& a, int lines, const SpanArgs* line0, const SpanArgs* line1, cudaStream_t s);
+// or one or two (same call, other line) whose questions between them are all that have tokens.  seen: a call without
+// lines reads every page that its tokens see (else only those that they are written to are looked at)
+cudaError_t launch_span_plan(const SpanArgs& a, int lines, const SpanArgs* line0, const SpanArgs* line1, cudaStream_t s,
+                             bool seen = false);
 // checked: behind a plan; else a small call (span_small_copy), which checks for itself
 bool span_small_copy(const SpanArgs& a);
 cudaError_t launch_span_write(const SpanArgs& a, bool checked, int num_sms, cudaStream_t s);

@@ -27,6 +27,7 @@ struct PlanLine {
 struct PlanArgs {
   SpanArgs a;
   int32_t lines;
+  int32_t seen;  // look at every page that a new token sees, not only at those that are written
   PlanLine line[2];
 };
 
@@ -178,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(const __grid_con
         if (L <= 0) continue;
         const int p0 = pre[i], p1 = p0 + L - 1;
         int ns = 0, lo = p0 / kPage;
-        if (p.lines) {
+        if (p.seen) {
           const SpanTiles s(p0, p1, a.window, a.sinks);
           ns = s.ns;
           lo = s.lo;
@@ -368,12 +369,13 @@ __global__ void __launch_bounds__(kThreads, 1) span_plan_kernel(const __grid_con
 
 }  // namespace
 
-cudaError_t launch_span_plan(const SpanArgs& a, int lines, const SpanArgs* line0, const SpanArgs* line1, cudaStream_t s) {
+cudaError_t launch_span_plan(const SpanArgs& a, int lines, const SpanArgs* line0, const SpanArgs* line1, cudaStream_t s, bool seen) {
   PlanArgs p = {};
   p.a = a;
   // No questions, no pages: the kernel divides by n where there are pages (a test in the kernel costs 0.4 us a call)
   if (a.n == 0) p.a.pool_elem = 0;
   p.lines = lines;
+  p.seen = lines > 0 || seen;
   // intervals, prefixes and first items of the questions, and beside them the largest of: the sort
   // keys, the bit map of the blocks, the tile counts of the items
   size_t area = 8;
