@@ -776,6 +776,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int token0 = w.k.token(w.j) + q * a.tile_tokens;
           const int rows = min(a.tile_tokens, w.k.L - token0) * a.group;       // columns that are rows of the question
           const int from = max(0, u - w.k.prefix - token0) * a.group;          // the first that sees this thread's key
+          // whole: every row of the tile sees every key.  The columns behind the rows of a group that does not divide 128,
+          // fewer than 16 and so among the last 32, are q rows of zeros: beside an infinite key they are not 0 but NaN
           const bool whole = rows == a.tile_tokens * a.group && u0 + kM - 1 <= w.k.prefix + token0;
           const ulonglong2* ml2 = reinterpret_cast<const ulonglong2*>(ml);
           unsigned long long s2[4] = {0, 0, 0, 0};
@@ -808,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 s2[((e >> 1) + 1) & 3] = add2(s2[((e >> 1) + 1) & 3], f2pack(ex2_approx(z1.x), ex2_approx(z1.y)));
               }
             };
-            if (whole) weights(std::false_type{});
+            if (whole && (c < 3 || rows == kM)) weights(std::false_type{});
             else weights(std::true_type{});
           }
           const float2 s0 = unpack2(add2(add2(s2[0], s2[1]), add2(s2[2], s2[3])));
