@@ -281,7 +281,8 @@ kev_status kev_sample(const void* logits, int32_t n_questions, int32_t vocab, in
  * min(vocab, KEV_MAX_TOP), device int32 and float[n_rows, top_n].  Logits of -infinity have probability 0 (a grammar's
  * mask).  A row that holds a NaN or +infinity, or nothing above -infinity, has no distribution: its floats are NaN and its
  * top tokens -1.  A live temperature that is negative or not finite, or a live token outside [0, vocab), sets
- * KEV_ERR_SAMPLING and nothing is written.  fp32 arithmetic.  One kernel. */
+ * KEV_ERR_SAMPLING and nothing is written.  After KEV_ERR_TIMEOUT a row is either written or left as it was.  fp32
+ * arithmetic.  One kernel. */
 #define KEV_MAX_TOP 32
 kev_status kev_logprobs(const void* logits, int32_t n_rows, int32_t vocab, int32_t dtype, const float* temperature,
                         const uint8_t* active, const int32_t* tokens, float* logprobs, float* entropy, int32_t top_n,

@@ -122,6 +122,7 @@ struct Shared {
   unsigned long long merged[kMaxCluster * kTop];
   float warp_m[kWarps], warp_s[kWarps], warp_w[kWarps];
   float part[3];  // this CTA's stats, for the peers
+  uint32_t came;  // and whether its tiles came, all of them
   int scan[kWarps];
   int count, n_best;
   uint4 chunk[kChunks];  // chunks with a candidate, and which they are
@@ -511,7 +512,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const __grid_
     sm.abort = 0;
     sm100::fence_mbar_init();
     for (int s = 0; s < kStages; ++s) issue();
-    if (a.test_stall && blockIdx.x == 0 && !sm100::mbar_wait(&sm.stall, 0, &sm.abort, a.wait_budget)) give_up();
+    // (the last CTA of the first cluster: the row is written by another)
+    if (a.test_stall && (int)blockIdx.x == S - 1 && !sm100::mbar_wait(&sm.stall, 0, &sm.abort, a.wait_budget)) give_up();
   }
   __syncthreads();
 
@@ -563,7 +565,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const __grid_
         if (ok && !sm100::mbar_wait(&sm.empty[old % kStages], (old / kStages) & 1, &sm.abort, a.wait_budget)) give_up();
         if (ok) issue();
       }
-      // (after a wait that gave up the rows are walked on, for the barriers that the threads share, and nothing is written)
+      // (after a wait that gave up the rows are walked on, for the barriers that the threads share; a row of which any
+      // thread of the cluster missed a tile is not written)
       if (ok && !sm100::mbar_wait(&sm.full[seq % kStages], (seq / kStages) & 1, &sm.abort, a.wait_budget)) give_up();
       Tile<E> t;
       t.load(stages + seq % kStages * kTile, at, p.i1);
@@ -623,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const __grid_
       sm.warp_s[warp] = st.s;
       sm.warp_w[warp] = st.w;
     }
-    __syncthreads();
+    bool came = __syncthreads_and(ok);
     if (warp == 0) {
       Stats b = lane < kWarps ? Stats{sm.warp_m[lane], sm.warp_s[lane], sm.warp_w[lane]} : Stats{-INFINITY, 0.f, 0.f};
 #pragma unroll
@@ -634,6 +637,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const __grid_
         sm.part[0] = b.m;
         sm.part[1] = b.s;
         sm.part[2] = b.w;
+        sm.came = came;
       }
     }
     if (S > 1) {
@@ -641,6 +645,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const __grid_
       if (rank == 0) {
         if (warp == 0) {
           Stats b = {-INFINITY, 0.f, 0.f};
+          came = __all_sync(0xffffffffu, lane >= S || ld_peer_u32(&sm.came, lane) != 0u);
           if (lane < S)
             b = {__uint_as_float(ld_peer_u32(&sm.part[0], lane)), __uint_as_float(ld_peer_u32(&sm.part[1], lane)),
                  __uint_as_float(ld_peer_u32(&sm.part[2], lane))};
@@ -684,12 +689,14 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const __grid_
       const bool none = sm.bad;
       const float lse2 = sm.row_lse2;
       auto lp = [&](float x) { return ((x - sm.row_m) * c - lse2) * kLn2; };
-      if (tid == 0 && ok) {
+      // (came: the whole CTA's, or in the first warp the cluster's; the first warp writes)
+      static_assert(kTop <= 32, "top tokens are written by one warp");
+      if (tid == 0 && came) {
         const int first = greedy && !none ? (int)(0xffffffffu - (uint32_t)sm.best[0]) : 0;
         if (a.tokens) a.logprobs[r] = none ? NAN : greedy ? (a.tokens[r] == first ? 0.f : -INFINITY) : lp(token_logit);
         if (a.entropy) a.entropy[r] = none ? NAN : greedy ? 0.f : (lse2 - st.w / st.s) * kLn2;
       }
-      if (tid < a.top_n && ok) {
+      if (tid < a.top_n && came) {
         const unsigned long long key = none ? 0ull : sm.best[tid];
         a.top_tokens[(int64_t)r * a.top_n + tid] = none ? -1 : (int32_t)(0xffffffffu - (uint32_t)key);
         a.top_logprobs[(int64_t)r * a.top_n + tid] =
