@@ -274,15 +274,15 @@ kev_status kev_sample(const void* logits, int32_t n_questions, int32_t vocab, in
  *   logprobs[r] = log p[tokens[r]],   entropy[r] = -sum_k p[k] log p[k],
  *   top_tokens[r, 0 .. top_n), top_logprobs[r, ..]: the tokens of the largest logits, larger ones first and of equal ones
  *   the lowest index first, and their log p.
- * temperature: device float[n_rows], or NULL for 1.  T_r = 0 is the distribution that kev_sample draws from there: all on
- * the first of the largest logits (log probability 0, -infinity elsewhere; entropy 0).  active: device uint8[n_rows], or
- * NULL for all; rows of 0 are neither read nor written.  tokens and logprobs: device int32 and float[n_rows], or both
- * NULL; entropy: device float[n_rows] or NULL; top_n: 0 (top_tokens and top_logprobs not looked at) to
- * min(vocab, KEV_MAX_TOP), device int32 and float[n_rows, top_n].  Logits of -infinity have probability 0 (a grammar's
- * mask).  A row that holds a NaN or +infinity, or nothing above -infinity, has no distribution: its floats are NaN and its
- * top tokens -1.  A live temperature that is negative or not finite, or a live token outside [0, vocab), sets
- * KEV_ERR_SAMPLING and nothing is written.  After KEV_ERR_TIMEOUT a row is either written or left as it was.  fp32
- * arithmetic.  One kernel. */
+ * temperature: device float[n_rows], or NULL for 1.  T_r = 0 is the distribution that kev_sample draws from there:
+ * all on the first of the largest logits (log probability 0, -infinity elsewhere; entropy 0); above 0, what is below
+ * 4.3e-39 counts as 4.3e-39.  active: device uint8[n_rows], or NULL for all; rows of 0 are neither read nor written.
+ * tokens and logprobs: device int32 and float[n_rows], or both NULL; entropy: device float[n_rows] or NULL; top_n: 0
+ * (top_tokens and top_logprobs not looked at) to min(vocab, KEV_MAX_TOP), device int32 and float[n_rows, top_n].
+ * Logits of -infinity have probability 0 (a grammar's mask).  A row that holds a NaN or +infinity, or nothing above
+ * -infinity, has no distribution: its floats are NaN and its top tokens -1.  A live temperature that is negative or
+ * not finite, or a live token outside [0, vocab), sets KEV_ERR_SAMPLING and nothing is written.  After
+ * KEV_ERR_TIMEOUT a row is either written or left as it was.  fp32 arithmetic.  One kernel. */
 #define KEV_MAX_TOP 32
 kev_status kev_logprobs(const void* logits, int32_t n_rows, int32_t vocab, int32_t dtype, const float* temperature,
                         const uint8_t* active, const int32_t* tokens, float* logprobs, float* entropy, int32_t top_n,

@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const __grid_
     const float T = a.temperature ? a.temperature[r] : 1.f;
     const bool greedy = T == 0.f;
     const int need = greedy ? max(a.top_n, 1) : a.top_n;
-    const float c = greedy ? kLog2e : fminf(kLog2e / T, 1e30f);
+    const float c = greedy ? kLog2e : fminf(kLog2e / T, 3.4028235e38f);  // finite: 0 times it is 0
     const Part<E> p(a, r, rank, S);
     float token_logit = 0.f;
     if (a.tokens && tid == 0) {

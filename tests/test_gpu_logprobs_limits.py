@@ -1,12 +1,13 @@
-"""kev_logprobs where a wait gives up."""
+"""kev_logprobs where a wait gives up, and at the ends of what temperatures may be."""
 import os
 import subprocess
 import sys
 import textwrap
 
+import numpy as np
 import pytest
 
-from test_gpu_logprobs import ROOT
+from test_gpu_logprobs import ROOT, check
 
 pytestmark = pytest.mark.gpu
 
@@ -35,3 +36,11 @@ def test_rows_whose_tiles_did_not_come_are_left_as_they_were():
     env = {k: v for k, v in os.environ.items() if k not in ("KEV_TEST_STALL", "KEV_TEST_WAIT_LIMIT")}
     r = subprocess.run([sys.executable, "-c", CHILD], capture_output=True, text=True, timeout=600, env=env)
     assert r.returncode == 0 and "ALL OK" in r.stdout, f"child failed:\n{r.stdout}\n{r.stderr[-4000:]}"
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("size", [1e-28, 1e-31, 1e-34, 1e-37])
+def test_tiny_temperatures_of_tiny_differences(size, dtype):
+    """Logits of the temperature's size: the distribution is that of ordinary logits at temperature 1."""
+    x = 2.5 * np.random.default_rng(5).standard_normal((3, 2000)) * size
+    check(x, dtype, [int(x[0].argmax()), 7, 1999], [size, 2 * size, 0.5 * size], 4)
