@@ -528,7 +528,7 @@ size_t kev_attn_mass_workspace_size(int32_t n_questions, int32_t total_tokens, c
  * finite and not negative: 1 adds up, 0 counts afresh (the old values are not read), between them old attention fades.
  * Only K is read; V may be anything.  Questions without new tokens are left as they are.  Errors and max_chunk as for
  * kev_chunk_attn_paged.  Scores and sums in fp32 (bf16 q: products on the tensor cores).  The result does not depend on
- * the order in which the GPU works. */
+ * the order in which the GPU works.  After KEV_ERR_TIMEOUT the mass of questions with new tokens is lost. */
 kev_status kev_attn_mass_paged(const void* q, int32_t total_tokens, const kev_interval* intervals, int32_t n_questions,
                                const int32_t* prefix_lens, int32_t max_chunk, const kev_paged_cache* cache, float decay,
                                float* mass, const kev_attn_shape* shape, void* workspace, size_t workspace_bytes,
@@ -557,7 +557,8 @@ kev_status kev_select_paged(const float* mass, const int32_t* lens, const uint8_
  * writes it, or by any other rule: per question and head strictly ascending within [0, lens[i]), else KEV_ERR_KEPT (also a
  * kept_lens[i] negative, above keep or above lens[i]).  Other device errors: KEV_ERR_SLOT_OVERFLOW (lens[i] negative or
  * past max_blocks * KEV_PAGE), KEV_ERR_SLOT (a block of pages in use out of range, or used twice).  All are found before
- * anything is written. */
+ * anything is written.  After KEV_ERR_TIMEOUT some rows have been moved and others not: K, V, scales and mass of the
+ * questions that were to be cut are lost, and the call cannot be repeated on them. */
 kev_status kev_compact_paged(const int32_t* kept, int32_t keep, const int32_t* lens, const int32_t* kept_lens,
                              int32_t n_questions, const kev_paged_cache* cache, float* mass, const kev_attn_shape* shape,
                              void* workspace, size_t workspace_bytes, int32_t* dev_status, kev_stream_t stream);

@@ -326,8 +326,8 @@ cudaError_t launch_logprobs(const LogprobsArgs& a, int num_sms, cudaStream_t s);
 // ---------------------------------------------------------------------------------------
 constexpr int kEvictChunk = 64;       // rows of a move (half a page)
 constexpr int kEvictCheckCtas = 304;  // of the check kernel, at most
-// words of the workspace: the next chunk's ticket, a wait gave up, one that nothing sets (test hook), verdicts, flags
-enum : int32_t { kEvictTicket = 0, kEvictAbort = 1, kEvictNever = 2, kEvictVerdicts = 16 };
+// words of the workspace: the next chunk's ticket, a wait gave up, verdicts, flags
+enum : int32_t { kEvictTicket = 0, kEvictAbort = 1, kEvictVerdicts = 16 };
 struct EvictArgs {
   const float* mass;            // selection: [n_blocks, h_kv, kPage]
   const int32_t* lens;          // [n] cached positions
@@ -351,7 +351,7 @@ struct EvictArgs {
   int32_t check_ctas;
   int32_t smem_keys;
   long long wait_budget;
-  int32_t test_stall;
+  int32_t test_stall;  // timeout test hook
   char* ws;
   int32_t* dev_status;
 };
