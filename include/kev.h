@@ -543,9 +543,10 @@ size_t kev_evict_workspace_size(int32_t n_questions, int32_t keep, const kev_att
  * they fit, else the first `first`, the last `last` and of the others those of the largest mass, of equal mass the lowest
  * positions (a NaN counts as larger than any number).  Of a question that is not live kept_lens[i] = lens[i], and its kept
  * is left as it is.  kept: device int32 [n_questions, H_kv, keep]; kept_lens: device int32[n_questions], not lens itself.
- * keep > 0, first and last not negative, first + last <= keep (else KEV_ERR_INVALID_ARG).  Device errors:
- * KEV_ERR_SLOT_OVERFLOW (a live lens[i] negative or past max_blocks * KEV_PAGE), KEV_ERR_SLOT (a block of its pages out of
- * range).  Of the shape only h_kv counts. */
+ * keep > 0, first and last not negative, first + last <= keep (else KEV_ERR_INVALID_ARG); keep <= 2^30, and
+ * n_questions * H_kv * ceil(keep / 64) <= 2^30 (else KEV_ERR_UNSUPPORTED, here and in kev_compact_paged; the workspace's size
+ * is 0 then).  Device errors: KEV_ERR_SLOT_OVERFLOW (a live lens[i] negative or past max_blocks * KEV_PAGE), KEV_ERR_SLOT (a
+ * block of its pages out of range).  Of the shape only h_kv counts. */
 kev_status kev_select_paged(const float* mass, const int32_t* lens, const uint8_t* active, int32_t n_questions,
                             const int32_t* block_table, int32_t max_blocks, int32_t n_blocks, int32_t keep, int32_t first,
                             int32_t last, int32_t* kept, int32_t* kept_lens, const kev_attn_shape* shape, void* workspace,

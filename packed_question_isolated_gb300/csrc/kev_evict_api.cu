@@ -48,8 +48,9 @@ size_t evict_bytes(int32_t n, int32_t keep, int32_t h_kv) {
   const int64_t chunks = ((int64_t)keep + kEvictChunk - 1) / kEvictChunk;
   return align_up(4 * ((size_t)(kEvictVerdicts + kEvictCheckCtas) + (size_t)n * h_kv * chunks), 256);
 }
-bool evict_sizes_fit(int32_t n, int32_t keep, int32_t h_kv) {  // tickets are counted in 32 bits
-  return ((int64_t)keep + kEvictChunk - 1) / kEvictChunk * n * h_kv <= 1 << 30;
+// Positions end at 2^30 and cached rows at 2^31, so longer lists and more heads are of no use; tickets are counted in 32 bits
+bool evict_sizes_fit(int32_t n, int32_t keep, int32_t h_kv) {
+  return keep <= 1 << 30 && h_kv <= 1 << 24 && ((int64_t)keep + kEvictChunk - 1) / kEvictChunk * n * h_kv <= 1 << 30;
 }
 kev_status evict_common(EvictArgs* a, const int32_t* lens, int32_t n, const int32_t* table, int32_t max_blocks, int32_t n_blocks,
                         int32_t keep, const kev_attn_shape* shape, void* ws, size_t ws_bytes, int32_t* dev_status) {
