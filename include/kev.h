@@ -535,7 +535,7 @@ kev_status kev_attn_mass_paged(const void* q, int32_t total_tokens, const kev_in
                                int32_t* dev_status, kev_stream_t stream);
 
 /* Bytes of device workspace of the two calls below (256-byte aligned, no initial value; not shared by calls in flight
- * together).  0 on bad arguments. */
+ * together).  Of the shape only h_kv counts.  0 on bad arguments. */
 size_t kev_evict_workspace_size(int32_t n_questions, int32_t keep, const kev_attn_shape* shape);
 
 /* For every live question (active: device uint8[n_questions], or NULL for all) with lens[i] cached positions, and every

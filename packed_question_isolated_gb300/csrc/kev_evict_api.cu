@@ -54,8 +54,7 @@ bool evict_sizes_fit(int32_t n, int32_t keep, int32_t h_kv) {
 }
 kev_status evict_common(EvictArgs* a, const int32_t* lens, int32_t n, const int32_t* table, int32_t max_blocks, int32_t n_blocks,
                         int32_t keep, const kev_attn_shape* shape, void* ws, size_t ws_bytes, int32_t* dev_status) {
-  const kev_status st = check_span_shape(shape);
-  if (st != KEV_OK) return st;
+  if (!shape || shape->h_kv <= 0) return KEV_ERR_INVALID_ARG;  // the rest of it: the move, whose rows it describes
   if (n < 0 || keep <= 0 || max_blocks <= 0 || n_blocks <= 0) return KEV_ERR_INVALID_ARG;
   if (n > kMaxQuestions || n_blocks > kSpanMaxBlocks || (int64_t)max_blocks * kPage > (1 << 30) ||
       (int64_t)n_blocks * shape->h_kv * kPage > 0x7fffffffll || !evict_sizes_fit(n, keep, shape->h_kv))
@@ -182,7 +181,7 @@ kev_status kev_attn_mass_paged(const void* q, int32_t total_tokens, const kev_in
 }
 
 size_t kev_evict_workspace_size(int32_t n_questions, int32_t keep, const kev_attn_shape* shape) {
-  if (check_span_shape(shape) != KEV_OK || n_questions < 0 || n_questions > kMaxQuestions || keep <= 0 ||
+  if (!shape || shape->h_kv <= 0 || n_questions < 0 || n_questions > kMaxQuestions || keep <= 0 ||
       !evict_sizes_fit(n_questions, keep, shape->h_kv))
     return 0;
   return evict_bytes(n_questions, keep, shape->h_kv);
@@ -215,8 +214,10 @@ kev_status kev_compact_paged(const int32_t* kept, int32_t keep, const int32_t* l
                              void* workspace, size_t workspace_bytes, int32_t* dev_status, kev_stream_t stream) {
   EvictArgs a;
   if (!cache) return KEV_ERR_INVALID_ARG;
-  kev_status st = evict_common(&a, lens, n_questions, cache->block_table, cache->max_blocks, cache->n_blocks, keep, shape,
-                               workspace, workspace_bytes, dev_status);
+  kev_status st = check_span_shape(shape);
+  if (st == KEV_OK)
+    st = evict_common(&a, lens, n_questions, cache->block_table, cache->max_blocks, cache->n_blocks, keep, shape, workspace,
+                      workspace_bytes, dev_status);
   if (st != KEV_OK) return st;
   SpanArgs c = {};  // the cache's own checks
   c.h_kv = shape->h_kv;

@@ -1,4 +1,4 @@
-"""The move of kept rows when its waits run out."""
+"""The move of kept rows when its waits run out; the shape that a selection takes."""
 import os
 import subprocess
 import sys
@@ -6,7 +6,7 @@ import textwrap
 
 import pytest
 
-from test_gpu_evict import ROOT
+from test_gpu_evict import ROOT, Cut, kev
 
 pytestmark = pytest.mark.gpu
 
@@ -44,3 +44,13 @@ def test_the_wait_for_lower_chunks_gives_up():
     env = {k: v for k, v in os.environ.items() if k not in ("KEV_TEST_STALL", "KEV_TEST_WAIT_LIMIT")}
     r = subprocess.run([sys.executable, "-c", CHILD], capture_output=True, text=True, timeout=600, env=env)
     assert r.returncode == 0 and "ALL OK" in r.stdout, f"child failed:\n{r.stdout}\n{r.stderr[-4000:]}"
+
+
+@pytest.mark.parametrize("h_q,d,dtype,scale", [(0, 0, "bf16", 0.0), (7, 96, 2, -1.0), (64, 128, "fp32", float("nan"))])
+def test_of_a_selections_shape_only_the_kv_heads_count(h_q, d, dtype, scale):
+    c = Cut(14, [500, 100, 300], 64, 2, 10)
+    c.shape = kev.make_shape(h_q, c.h_kv, d, dtype, scale)
+    assert kev.kev_evict_workspace_size(3, 64, c.shape) == c.bytes
+    c.select()
+    c.ok()
+    c.check_select()
