@@ -553,13 +553,14 @@ kev_status kev_select_paged(const float* mass, const int32_t* lens, const uint8_
                             size_t workspace_bytes, int32_t* dev_status, kev_stream_t stream);
 
 /* Rows kept[i, g, j] of the K, V (and scales) of kv head g of question i, and of mass where it is given, to position j,
- * for j < kept_lens[i], for every question with kept_lens[i] < lens[i] (the others are left as they are, their kept and
- * pages not looked at).  In place: rows from kept_lens[i] on hold nothing of use afterwards.  kept as kev_select_paged
- * writes it, or by any other rule: per question and head strictly ascending within [0, lens[i]), else KEV_ERR_KEPT (also a
- * kept_lens[i] negative, above keep or above lens[i]).  Other device errors: KEV_ERR_SLOT_OVERFLOW (lens[i] negative or
- * past max_blocks * KEV_PAGE), KEV_ERR_SLOT (a block of pages in use out of range, or used twice).  All are found before
- * anything is written.  After KEV_ERR_TIMEOUT some rows have been moved and others not: K, V, scales and mass of the
- * questions that were to be cut are lost, and the call cannot be repeated on them. */
+ * for j < kept_lens[i], for every question with kept_lens[i] < lens[i].  The others are left as they are, their kept and
+ * pages not looked at (a stopped question's may be stale): a block that one of them shares with a question that is cut is
+ * not found, and rows are moved over it.  In place: rows from kept_lens[i] on hold nothing of use afterwards.  kept as
+ * kev_select_paged writes it, or by any other rule: per question and head strictly ascending within [0, lens[i]), else
+ * KEV_ERR_KEPT (also a kept_lens[i] negative, above keep or above lens[i]).  Other device errors: KEV_ERR_SLOT_OVERFLOW
+ * (lens[i] negative or past max_blocks * KEV_PAGE), KEV_ERR_SLOT (a block of the pages of questions that are cut out of
+ * range, or used twice).  All are found before anything is written.  After KEV_ERR_TIMEOUT some rows have been moved and
+ * others not: K, V, scales and mass of the questions that were to be cut are lost, and the call cannot be repeated on them. */
 kev_status kev_compact_paged(const int32_t* kept, int32_t keep, const int32_t* lens, const int32_t* kept_lens,
                              int32_t n_questions, const kev_paged_cache* cache, float* mass, const kev_attn_shape* shape,
                              void* workspace, size_t workspace_bytes, int32_t* dev_status, kev_stream_t stream);

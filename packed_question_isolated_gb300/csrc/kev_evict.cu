@@ -2,8 +2,10 @@
 //
 // evict_check_kernel   every check of device data, before anything is written: CTA 0 looks at lengths and block tables
 //                      (a bit map of the blocks in use: two questions on one block is the shared-state bug of the
-//                      KV-cache isolation article, hnwysp.cn, §2.3), all CTAs at the kept lists.  Each leaves a verdict
-//                      of its own, and the kernel behind it takes the first error of them all.
+//                      KV-cache isolation article, hnwysp.cn, §2.3 -- of the questions that are cut: the table row of one
+//                      that is not may be stale, so a block that it shares with one that is cut is not found), all CTAs at
+//                      the kept lists.  Each leaves a verdict of its own, and the kernel behind it takes the first error of
+//                      them all.
 //
 // select_kernel        a CTA per (question, kv head).  The kept positions are the protected ones (the first and the last
 //                      few) and of the others those of the `want` largest masses: the want-th largest value is found by
