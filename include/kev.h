@@ -269,8 +269,8 @@ kev_status kev_sample(const void* logits, int32_t n_questions, int32_t vocab, in
                       kev_stream_t stream);
 
 /* Log probabilities of given tokens, entropy and likeliest tokens of n_rows rows of logits (device [n_rows, vocab] of
- * `dtype`; any vocab): what a serving program reports beside the token that kev_sample draws, or how likely a model finds
- * a given text.  With p = softmax(logits_r / T_r):
+ * `dtype`; any vocab; both up to 2^30, else KEV_ERR_UNSUPPORTED): what a serving program reports beside the token that
+ * kev_sample draws, or how likely a model finds a given text.  With p = softmax(logits_r / T_r):
  *   logprobs[r] = log p[tokens[r]],   entropy[r] = -sum_k p[k] log p[k],
  *   top_tokens[r, 0 .. top_n), top_logprobs[r, ..]: the tokens of the largest logits, larger ones first and of equal ones
  *   the lowest index first, and their log p.

@@ -457,8 +457,8 @@ kev_status kev_logprobs(const void* logits, int32_t n_rows, int32_t vocab, int32
                         int32_t* top_tokens, float* top_logprobs, int32_t* dev_status, kev_stream_t stream) {
   if (n_rows < 0 || vocab <= 0 || top_n < 0 || top_n > vocab) return KEV_ERR_INVALID_ARG;
   if (dtype != KEV_BF16 && dtype != KEV_FP32) return KEV_ERR_UNSUPPORTED;
-  // chunks and tiles past a row's end are counted in 32 bits
-  if (top_n > KEV_MAX_TOP || vocab > (1 << 30)) return KEV_ERR_UNSUPPORTED;
+  // chunks and tiles past a row's end, and rows past the last one, are counted in 32 bits
+  if (top_n > KEV_MAX_TOP || vocab > (1 << 30) || n_rows > (1 << 30)) return KEV_ERR_UNSUPPORTED;
   if ((uintptr_t)dev_status & 3u) return KEV_ERR_INVALID_ARG;
   if (n_rows == 0) return KEV_OK;
   if (!logits || !aligned16(logits) || ((uintptr_t)temperature & 3u)) return KEV_ERR_INVALID_ARG;
