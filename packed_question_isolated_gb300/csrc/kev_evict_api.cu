@@ -31,7 +31,9 @@ kev_status mass_attend(const MassArgs& call, int32_t* launches, cudaStream_t s) 
   m.s = bf16 ? span_line(call.s, 0, 128, 2, sms) : span_line(call.s, 0, 64, 1, 2 * sms);
   m.s.unit_cost = bf16 ? 1 : 0;
   m.s.join_from = 2;
-  if (bf16 && (int64_t)call.s.max_chunk * call.s.group <= 16) {  // few rows per question, and the caller said so
+  // few rows per question, and the caller said so; a grid has a cluster of up to 8 CTAs for every question and kv head
+  const bool lists_fit = (int64_t)call.s.n * call.s.h_kv < 1 << 28;
+  if (bf16 && lists_fit && (int64_t)call.s.max_chunk * call.s.group <= 16) {
     *launches = 2;
     cudaError_t e = launch_span_plan(call.s, 0, nullptr, nullptr, s, true);
     if (e == cudaSuccess) e = launch_mass_rows(m, sms, s);
