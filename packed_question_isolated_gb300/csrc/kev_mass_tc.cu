@@ -744,6 +744,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       float* part = reinterpret_cast<float*>(a.ws + a.layout.part_o);                 // [2 * parts][128]
       int32_t* arrived = reinterpret_cast<int32_t*>(a.ws + a.line.arrived);
       const int tok = r / a.group;
+      // Columns that are rows of a full tile.  Those behind them (a group that does not divide 128 leaves fewer than 16) are
+      // q rows of zeros, and beside an infinite key not 0 but NaN: masked in whole tiles too.
+      const int live = a.tile_tokens * a.group;
       uint32_t n = 0, x = 0, mine_n = 0, joins = 0;
       bool ok = true;  // as above
       for (KeyWalk w(p.m, blockIdx.x); w.live(); w.next(), ++n) {
@@ -776,9 +779,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int token0 = w.k.token(w.j) + q * a.tile_tokens;
           const int rows = min(a.tile_tokens, w.k.L - token0) * a.group;       // columns that are rows of the question
           const int from = max(0, u - w.k.prefix - token0) * a.group;          // the first that sees this thread's key
-          // whole: every row of the tile sees every key.  The columns behind the rows of a group that does not divide 128,
-          // fewer than 16 and so among the last 32, are q rows of zeros: beside an infinite key they are not 0 but NaN
-          const bool whole = rows == a.tile_tokens * a.group && u0 + kM - 1 <= w.k.prefix + token0;
+          // whole: every row of the tile sees every key
+          const bool whole = rows == live && u0 + kM - 1 <= w.k.prefix + token0;
           const ulonglong2* ml2 = reinterpret_cast<const ulonglong2*>(ml);
           unsigned long long s2[4] = {0, 0, 0, 0};
           uint32_t v[2][32];
@@ -799,8 +801,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const ulonglong2 nl = ml2[8 * c + e / 4];
                 float2 z0 = unpack2(fma2((unsigned long long)s[e] | (unsigned long long)s[e + 1] << 32, fx2, nl.x));
                 float2 z1 = unpack2(fma2((unsigned long long)s[e + 2] | (unsigned long long)s[e + 3] << 32, fx2, nl.y));
-                if (decltype(masked)::value) {
-                  const int col = 32 * c + e;
+                const int col = 32 * c + e;
+                if (decltype(masked)::value == 1 && e >= 16) {
+                  z0.x = col >= live ? -INFINITY : z0.x;
+                  z0.y = col + 1 >= live ? -INFINITY : z0.y;
+                  z1.x = col + 2 >= live ? -INFINITY : z1.x;
+                  z1.y = col + 3 >= live ? -INFINITY : z1.y;
+                }
+                if (decltype(masked)::value == 2) {
                   z0.x = col < from || col >= rows ? -INFINITY : z0.x;
                   z0.y = col + 1 < from || col + 1 >= rows ? -INFINITY : z0.y;
                   z1.x = col + 2 < from || col + 2 >= rows ? -INFINITY : z1.x;
@@ -810,8 +818,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 s2[((e >> 1) + 1) & 3] = add2(s2[((e >> 1) + 1) & 3], f2pack(ex2_approx(z1.x), ex2_approx(z1.y)));
               }
             };
-            if (whole && (c < 3 || rows == kM)) weights(std::false_type{});
-            else weights(std::true_type{});
+            if (!whole) weights(std::integral_constant<int, 2>{});
+            else if (c == 3 && live < kM) weights(std::integral_constant<int, 1>{});
+            else weights(std::integral_constant<int, 0>{});
           }
           const float2 s0 = unpack2(add2(add2(s2[0], s2[1]), add2(s2[2], s2[3])));
           sum += s0.x + s0.y;
