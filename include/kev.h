@@ -464,7 +464,8 @@ kev_status kev_paged_read(void* k, void* v, int32_t total_tokens, const kev_inte
  * Arithmetic: bf16 q: products on the tensor cores, fp32 accumulation, softmax weights (over
  * KEV_E4M3 times the scale of V's row) rounded for the product with V, to bf16 or (few rows over
  * KEV_E4M3) to fp16, at any size of V's rows down to the smallest; above, |v| < 2^40 is sure to stay
- * finite, since a weight may stand at up to 2^64 before its sum divides it.  fp32 q: fp32 throughout.
+ * finite, since a weight may stand at up to 2^64 before its sum divides it; bf16 q over KEV_E4M3 is multiplied with the
+ * codes before their scale, which is sure to stay finite for |q| < 2^112.  fp32 q: fp32 throughout.
  * What masked positions hold, NaN and infinities in rows or scales among it, does not reach the
  * result. */
 kev_status kev_chunk_attn_paged(const void* q, const void* k, const void* v, int32_t total_tokens,
@@ -527,8 +528,9 @@ size_t kev_attn_mass_workspace_size(int32_t n_questions, int32_t total_tokens, c
  * with w_{j,h} = softmax_u(scale q[begin_i + j, h] . K_i[u, g]) over u <= P_i + j, K_i as the cache holds it.  decay is
  * finite and not negative: 1 adds up, 0 counts afresh (the old values are not read), between them old attention fades.
  * Only K is read; V may be anything.  Questions without new tokens are left as they are.  Errors and max_chunk as for
- * kev_chunk_attn_paged.  Scores and sums in fp32 (bf16 q: products on the tensor cores).  The result does not depend on
- * the order in which the GPU works.  After KEV_ERR_TIMEOUT the mass of questions with new tokens is lost. */
+ * kev_chunk_attn_paged (a decode step that says 1 takes half the time of one that does not).  Scores and sums in fp32 (bf16
+ * q: products on the tensor cores, over KEV_E4M3 with |q| < 2^112 as there).  The result does not depend on the order in
+ * which the GPU works.  After KEV_ERR_TIMEOUT the mass of questions with new tokens is lost. */
 kev_status kev_attn_mass_paged(const void* q, int32_t total_tokens, const kev_interval* intervals, int32_t n_questions,
                                const int32_t* prefix_lens, int32_t max_chunk, const kev_paged_cache* cache, float decay,
                                float* mass, const kev_attn_shape* shape, void* workspace, size_t workspace_bytes,

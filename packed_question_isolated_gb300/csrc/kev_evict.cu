@@ -24,9 +24,9 @@
 //
 // Measured: 16 caches of 2 to 32 Ki positions cut to 4096 (8 kv heads of 128) selected in 31 us, most of it the largest
 // list's: 32 Ki masses in 1024 threads, three counts of them; moved in 85 (bf16, 6.1 TB/s, 90 % of the measured copy rate
-// with the checks).  32 caches of 200 to 2400 positions cut to 1024 selected in 13 us and moved, e4m3, in 21.  Measured and
-// left in the selection: four copies of the counts with 256 threads (17 us against 13), eight masses on their way (38
-// against 31).
+// with the checks; fp32 163).  32 caches of 200 to 2400 positions cut to 1024 selected in 13 us and moved, e4m3, in 21.
+// Measured and left in the selection: four copies of the counts with 256 threads (17 us against 13), eight masses on their
+// way (38 against 31).
 #include "kev_internal.cuh"
 
 namespace kev {
@@ -374,6 +374,9 @@ cudaError_t launch_select(const EvictArgs& call, int num_sms, cudaStream_t s) {
   const int64_t cap = (int64_t)a.max_blocks * kPage;
   constexpr int kMost = 48 * 1024;  // keys: 192 KB
   a.smem_keys = (int32_t)(cap < kMost ? cap : kMost);
+  // The lists' lengths are known to the device only, so the table's width decides.  1024 threads are for long lists, and for
+  // few: 32 lists of 16,000 positions (8 kv heads) take 39 us with them and 43 with 256, 4 of them 21 and 39.  They cost
+  // short lists in a wide table: 32 of 8000 take 28 us and 26, of 2000 18 and 13.5, of 500 16 and 9.4.
   const bool wide = cap > 4096;
   auto kern = wide ? select_kernel<1024> : select_kernel<256>;
   const size_t smem = 4 * (size_t)a.smem_keys;

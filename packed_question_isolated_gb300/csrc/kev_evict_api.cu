@@ -31,7 +31,10 @@ kev_status mass_attend(const MassArgs& call, int32_t* launches, cudaStream_t s) 
   m.s = bf16 ? span_line(call.s, 0, 128, 2, sms) : span_line(call.s, 0, 64, 1, 2 * sms);
   m.s.unit_cost = bf16 ? 1 : 0;
   m.s.join_from = 2;
-  // few rows per question, and the caller said so; a grid has a cluster of up to 8 CTAs for every question and kv head
+  // Few rows per question, and the caller said so; a grid has a cluster of up to 8 CTAs for every question and kv head.  Rows
+  // that fill 16 gain least: 4 tokens (G = 4) of each of 32 caches of 64 to 2400 positions take 41 us, and 40 with the kernels
+  // for chunks (e4m3 41 and 50), of each of 16 caches of 2 to 32 Ki 211 and 238 (181 and 324); one token of each 25 and 40 (26
+  // and 50), 94 and 237 (79 and 327).
   const bool lists_fit = (int64_t)call.s.n * call.s.h_kv < 1 << 28;
   if (bf16 && lists_fit && (int64_t)call.s.max_chunk * call.s.group <= 16) {
     *launches = 2;

@@ -19,11 +19,16 @@
 // this one is finished; what of a row is no whole 16 bytes is read by itself.  Every CTA first checks every live row's
 // temperature and token, so an invalid call writes nothing.
 //
-// Bound by instructions, 9 to 12 a logit with the row's share of the thresholds and sorts, then by memory: 4096 rows of
-// 151,936 bf16 logits with the 5 likeliest tokens take 282 us (4.4 TB/s, 65 % of the measured copy rate), without 233, with
-// 20 of them 329; 2048 rows of fp32 231.  32 rows with 20 tokens take 17 us, one row 13, mostly the chain of loads,
-// thresholds and cluster barriers.  Measured and left: tiles in registers one ahead instead of in shared memory (370 us for
-// the first, the compiler spills them); candidates read again from global memory (760); tiles of 16 KB (410).
+// Bound by no single unit: 4096 rows of 151,936 bf16 logits with the 5 likeliest tokens take 280 us (4.4 TB/s, 65 % of the
+// measured copy rate), without 233, with 20 of them 329; 2048 rows of fp32 230.  An instruction issues in 62 % of the cycles
+// (11.7 a logit), the exponentials' pipe is 25 % busy, and the largest stall, with the wait for a result, is the one at block
+// barriers: 16 of them where a threshold is made, and those of the ranking.  32 rows with 20 tokens take 15 us, one row 12,
+// mostly the chain of loads, thresholds and cluster barriers.
+// Rows with a mask: a thread's tile that holds -infinity beside other logits is summed a second time, one by one.  4096 rows
+// whose mask leaves one logit in fifty, scattered, take 441 us, where it leaves a run of the first ones 232; 2048 rows of
+// fp32 303 and 208.
+// Measured and left: tiles in registers one ahead instead of in shared memory (370 us for the first, the compiler spills
+// them); candidates read again from global memory (760); tiles of 16 KB (410).
 #include <algorithm>
 
 #include "kev_internal.cuh"
@@ -720,7 +725,8 @@ cudaError_t launch_logprobs(const LogprobsArgs& call, int num_sms, cudaStream_t 
   auto kern = a.elem == 2 ? logprobs_kernel<2> : logprobs_kernel<4>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kStageBytes + sizeof(Shared)));
   if (e != cudaSuccess) return e;
-  // kCtas CTAs on every SM: as many rows, or fewer rows in parts of 4096 logits or more
+  // kCtas CTAs on every SM: as many rows, or fewer rows in parts of 4096 logits or more.  Shorter parts cost more than they
+  // share out: 32 rows of 32,000 logits take 10.1 us so, in parts of 2048 13.7, of 8192 9.7; 8 rows of 8000 8.0, 9.3 and 7.8
   const int slots = kCtas * num_sms;
   int S = 1;
   while (S < kMaxCluster && (int64_t)a.n * 2 * S <= slots && a.vocab / (2 * S) >= 4096) S *= 2;

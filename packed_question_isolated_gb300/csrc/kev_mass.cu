@@ -1,6 +1,8 @@
 // Attention mass of fp32 q on the CUDA cores: true fp32 products and sums, cache fp32 or e4m3.  Bound by the multiply-adds
-// and the shared-memory loads beside them: chunks that take bf16 q on the tensor cores 0.21 ms took kernels of this shape
-// 7.5 (their rows widened from bf16 on the way).
+// and the shared-memory loads beside them: 8 chunks of 128 to 1024 tokens behind up to 8192 positions (28/4 heads) take 7.4
+// ms, where the products, twice, are 1.9 at the CUDA cores' nominal 74 TFLOP/s (in bf16 on the tensor cores 0.21).  A decode
+// step of 32 questions over 64 to 2400 positions (32/8 heads) takes 172 us (bf16 23): its row tiles of 64 hold the G rows of
+// one question, so one warp of eight multiplies, and K is read by both passes.
 //
 // mass_rows_kernel   the rows' log sums: 64 (token, q-head) rows, 8 a warp, against 32 keys at a time; a lane owns a key
 //                    and keeps a running maximum and sum of its own for each row, joined at the end.

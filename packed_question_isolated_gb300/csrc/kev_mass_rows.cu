@@ -9,16 +9,17 @@
 //   3. maxima and sums of the cluster's CTAs by distributed shared memory: what each row's weights have to be multiplied
 //      by; a position's mass is the sum over its rows.
 // K is read once and nothing but the result is written.  Where a CTA's part has more positions than its shared memory has
-// room for, those behind are computed twice: their sums with a running maximum in step 1, their weights in step 3.
+// room for, those behind are read and computed twice: their sums with a running maximum in step 1, their weights in step 3.
 //
 // e4m3: the codes become fp16, exactly, one conversion per two; q becomes fp16 with a power of two of its own per row that
 // brings its largest element to 2^14, so that what fp16 cannot hold is 2^-39 of it; the power and the key's scale multiply
 // the score, the power in two halves, which keeps the product in range where one factor is tiny and the other large.
+//
 // Bound by memory over long caches: 16 bf16 caches of 2 to 32 Ki positions (32/8 heads) 91 us with the checks (5.0 TB/s, 73 %
-// of the measured copy rate; DRAM bytes 1.00 of what has to be read).  32 e4m3 caches of 64 to 2400 positions take 19, of
-// which the checks are 4 to 5 and the rest is the chain of a cluster: pages, maxima, two cluster barriers.  Why clusters:
-// scores written out for a second kernel cost a workspace as large as the caches, a second reading of K costs K again.
-// Measured and left: the longest caches first (97 us against 95).
+// of the measured copy rate; DRAM bytes 1.00 of what has to be read, as long as the scores fit).  32 e4m3 caches of 64 to
+// 2400 positions take 19, of which the checks are 4 to 5 and the rest is the chain of a cluster: pages, maxima, two cluster
+// barriers.  Why clusters: scores written out for a second kernel cost a workspace as large as the caches, a second reading
+// of K costs K again.  Measured and left: the longest caches first (97 us against 95).
 #include <cuda_fp16.h>
 
 #include "kev_mass.cuh"
@@ -391,7 +392,13 @@ cudaError_t launch(const MassArgs& m, int num_sms, cudaStream_t s) {
   MassRowsArgs p = {};
   p.m = m;
   p.rows = (m.s.max_chunk * m.s.group + 1) / 2 * 2;
-  // a part of 4 pages or more for each CTA of a cluster
+  // A part of 4 pages or more of the widest cache that the table has room for, for each CTA of a cluster (the lengths are
+  // known to the device only).  16 bf16 caches of 2 to 32 Ki positions (8 kv heads) take 94 us in clusters of 8, 119 of 4,
+  // 238 of 2, 403 of 1; 4 caches of 4000 positions 11.7, 12.4, 16.7 and 25.  It costs many short caches, whose CTAs have
+  // few pages or none: 32 of 64 to 2400 positions take 25 us in the clusters of 4 that their own width of 19 pages asks
+  // for, 44 in those of 8 that a table of 512 does, and would take 20 in clusters of 2.  One cache of 131,072 positions
+  // has 8 CTAs per kv head and no more: 240 us with one kv head of 16 q-heads, 208 with 4 of 4, where the kernels for
+  // chunks take 54 and 100.
   int S = 1;
   while (S < kMaxCluster && m.s.max_blocks >= 8 * S) S *= 2;
   const int64_t most = ((int64_t)(m.s.max_blocks + S - 1) / S) * kPage;

@@ -20,12 +20,12 @@
 // A masked score is replaced, not multiplied, so what lies in keys that a row does not see never counts.  Every wait is
 // bounded, as in the other tensor-core kernels.
 //
-// What bounds it.  8 chunks of 128 to 1024 tokens behind up to 8192 positions (28/4 heads, bf16) take 208 us, 88 of them
-// the first kernel and 119 the second; 32 tokens of each of 8 e4m3 caches of 4 to 16 Ki positions 111 (49 and 59).  The
-// tensor pipe is busy 36 and 30 % of the time (19 and 16 over e4m3), the exponentials' pipe about as much, L2 and DRAM
-// under 15 %.  Neither the exponentials (without them 200 us), nor the MMAs (with one of a tile's eight 186) nor the copies
-// (of half the bytes: no change) carry it alone: what is left is the hand-over of a tile, MMA - barrier - tensor memory -
-// barrier, some 1500 clocks each, and in the second kernel a key tile's beginning and end.
+// What bounds it.  8 chunks of 128 to 1024 tokens behind up to 8192 positions (28/4 heads, bf16) take 208 us, 87 of them
+// the first kernel and 121 the second; over e4m3 248; 32 tokens of each of 8 e4m3 caches of 4 to 16 Ki positions 111 (49
+// and 60), of bf16 ones 90.  The tensor pipe is busy 38 and 30 % of the time (19 and 16 over e4m3), the exponentials' pipe
+// about as much, L2 and DRAM under 15 %.  Neither the exponentials (without them 200 us), nor the MMAs (with one of a
+// tile's eight 186) nor the copies (of half the bytes: no change) carry it alone: what is left is the hand-over of a tile,
+// MMA - barrier - tensor memory - barrier, some 1500 clocks each, and in the second kernel a key tile's beginning and end.
 // Measured and left: four groups of four warps at 96 registers, which spill (235 and 157 us); three groups at 128 that
 // take 32 columns at a time (207 and 124); polling instead of suspended waits, shorter chains for the maximum (no
 // difference).  A second key tile against each loaded q tile is not built.
@@ -48,7 +48,9 @@ constexpr int kLoadWarp = 8, kMmaWarp = 9, kQWarp = 10, kReadyWarp = 12;
 constexpr int kRegsExp = 200, kRegsOther = 56;  // 128 registers a thread at launch: 256 x 200 + 256 x 56 = 512 x 128
 constexpr uint32_t kTmemCols = 512;             // four S buffers of 128 columns
 constexpr long long kDrainBudget = 4000000000ll;
-constexpr int kUnitCost = 1;  // of a unit of mass_keys_tc beside its row tiles, in row tiles
+// Of a unit of mass_keys_tc beside its row tiles, in row tiles: 8 chunks of 128 to 1024 tokens (32/8 heads) take 180 us with
+// 1, 191 with 0, 179 with 2, 185 with 4 (28/4 heads 157, 159, 158, 161); 32 tokens of each of 8 caches the same with all
+constexpr int kUnitCost = 1;
 
 // Where a part of mass_keys_tc's work line begins: key tile `tile` of question and head, its row tile r; r > 0: the cut is
 // inside the unit, which has `parts` parts from part `first` on.

@@ -10,13 +10,14 @@
 // A position is not the cached row's index: a question whose cache had rows evicted counts on from the tokens that
 // it has seen.  So the first position of each question's new tokens is an argument of its own.
 //
-// Bound by memory: every row is read once and written once.  A head row belongs to a group of 4 to 16 lanes; a lane
-// holds 16 bytes of the row's first half and the 16 bytes that they pair with, so the rotation needs no exchange and
-// the sum of squares 2 to 4 shuffles.  A warp takes a token's head rows (q, k, v in order), kSteps of them per group
-// in flight; the token's cos and sin, the same for all of them, stay in registers.  Measured: the prompts of 32 questions
-// (64 to 4096 tokens, 32/8 heads of 128 in bf16, into a bf16 cache) 127 us with the checks, 122 without (5.6 TB/s, 83 % of
-// the measured copy rate); one token of each of 32 questions into an e4m3 cache 6.8 us on the GPU, a chain of dependent
-// loads (intervals, table, angles) behind the checks, where the call takes the host 10.
+// Bound by memory: every row is read once and written once.  A head row belongs to a group of 4 to 16 lanes; a lane holds
+// 16 bytes of the row's first half and the 16 bytes that they pair with, so the rotation needs no exchange and the sum of
+// squares 2 to 4 shuffles.  A warp takes a token's head rows (q, k, v in order), kSteps of them per group in flight; the
+// token's cos and sin, the same for all of them, stay in registers.  Measured: the prompts of 32 questions (64 to 4096
+// tokens, 32/8 heads of 128 in bf16, into a bf16 cache) 127 us with the checks, 122 without (5.6 TB/s, 83 % of the
+// measured copy rate); into an e4m3 cache 141 (4.5 TB/s of its fewer bytes: scales and codes are arithmetic that bf16 rows
+// do not have); in fp32 211, into an e4m3 cache 204; one token of each of 32 questions into an e4m3 cache 6.8 us on the
+// GPU, a chain of dependent loads (intervals, table, angles) behind the checks, where the call takes the host 10.
 #include <cuda_fp8.h>
 
 #include "kev_span.cuh"
