@@ -353,14 +353,16 @@ __global__ void __launch_bounds__(kThreads, 2) mass_rows_kernel(const __grid_con
     float* to = p.m.mass + cell;
     *to = u < prefix && p.m.decay != 0.f ? fmaf(p.m.decay, *to, w) : w;
   };
+  // The first row that sees position u: a row without weights (NaN) does not reach what it does not see
+  auto first_row = [&](int u) { return max(0, u - prefix) * G; };
   for (int x = t; x < here; x += kThreads) {
-    const int u = t0 * kPage + x;
+    const int u = t0 * kPage + x, first = first_row(u);
     const int64_t cell = ((int64_t)table[u / kPage] * a.h_kv + head) * kPage + u % kPage;
     float w = 0.f;
     const float* at = s_scores + x * RS;
 #pragma unroll
     for (int r = 0; r < 8 * NT; ++r)
-      if (r < R) w = fmaf(at[r], sm.factor[r], w);
+      if (r >= first && r < R) w = fmaf(at[r], sm.factor[r], w);
     put(u, cell, w);
   }
 #pragma unroll 1
@@ -370,12 +372,13 @@ __global__ void __launch_bounds__(kThreads, 2) mass_rows_kernel(const __grid_con
     float z[NT][4];
     scores(k, tile, z);
     float w[2] = {0.f, 0.f};
+    const int u0 = tile * kPage + warp * 16 + g, first[2] = {first_row(u0), first_row(u0 + 8)};
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int r = 8 * n + 2 * c + (e & 1);
-        w[e >> 1] += r < R ? ex2(z[n][e] - sm.lse[r]) : 0.f;
+        w[e >> 1] += r >= first[e >> 1] && r < R ? ex2(z[n][e] - sm.lse[r]) : 0.f;
       }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {

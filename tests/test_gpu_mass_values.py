@@ -1,4 +1,4 @@
-"""kev_attn_mass_paged on infinite keys, against the float64 definition.
+"""kev_attn_mass_paged on infinite keys and rows of NaN, against the float64 definition.
 
 Tolerances as derived in test_gpu_mass.py, S taken over the finite keys."""
 import numpy as np
@@ -26,7 +26,8 @@ def definition(m, decay, scale=None):
                 with np.errstate(invalid="ignore"):
                     z = (k[:n, g] * q[t, h]).sum(-1) * scale
                 fine = np.isfinite(z)
-                top = max(top, float((np.abs(k[:n, g][fine]) @ np.abs(q[t, h])).max()) * scale)
+                if fine.any():
+                    top = max(top, float((np.abs(k[:n, g][fine]) @ np.abs(q[t, h])).max()) * scale)
                 w = np.exp(z - z.max())
                 new[:n, g] += w / w.sum()
         if decay:
@@ -71,3 +72,37 @@ def test_an_infinite_key_of_minus_infinite_scores_receives_nothing(h_q, h_kv, dt
     m.call(0.5, max_chunk)
     m.ok()
     near_definition(m, 0.5)
+
+
+@pytest.mark.parametrize("bad", ["q nan", "q inf", "k inf", "k nan"])
+@pytest.mark.parametrize("dtype,pool", [("bf16", "bf16"), ("bf16", "e4m3"), ("fp32", "fp32"), ("fp32", "e4m3")])
+@pytest.mark.parametrize("h_q,h_kv,tokens,prefix,max_chunk", [(2, 2, 11, 164, 0), (6, 2, 5, 60, 5), (4, 1, 4, 127, 4), (8, 1, 2, 15000, 2),
+                                                              (6, 2, 60, 300, 0), (1, 1, 16, 0, 16)])
+def test_a_row_without_weights_does_not_reach_positions_that_it_does_not_see(h_q, h_kv, tokens, prefix, max_chunk, dtype, pool, bad):
+    """One row is NaN throughout, of a NaN or of an infinite score; the positions after it are as the later rows make them."""
+    m = Mass(50, [tokens], [prefix], h_q, h_kv, 64, dtype, pool)
+    t = tokens // 2 if max_chunk != 2 else 0
+    if bad[0] == "q":
+        m.q[t, 1 % h_q] = float(bad[2:])
+        want = np.zeros((prefix + tokens, h_kv), bool)
+        want[:prefix + t + 1, (1 % h_q) // (h_q // h_kv)] = True
+    else:  # a key of a new token: the rows from that token on see it, those before do not
+        k, ks = m.pools[0]
+        b, row = int(m.table[0, (prefix + t) // PAGE]), (prefix + t) % PAGE
+        m.q.copy_(m.q.abs() + 0.125)
+        if pool == "e4m3":
+            k.view(torch.uint8)[b, 0, row] = 0x7f if bad == "k nan" else 0x38  # NaN, 1
+            ks[b, 0, row] = float(bad[2:])
+        else:
+            k[b, 0, row, 3] = float(bad[2:])
+        want = np.zeros((prefix + tokens, h_kv), bool)
+        want[:, 0] = True
+    m.call(0.5, max_chunk)
+    m.ok()
+    got = m.positions(m.mass.cpu().numpy(), 0)
+    assert (np.isnan(got) == want).all(), np.argwhere(np.isnan(got) != want)[:5].tolist()
+    if bad[0] == "q":
+        with np.errstate(invalid="ignore"):
+            ref, top = definition(m, 0.5)
+        rel = ((8 * 72 + 8) * top + 16 + tokens * h_q / h_kv) * 2.0 ** -24
+        assert (np.abs(got - ref[0]) <= rel * ref[0] + 1e-30)[~want].all()
